@@ -237,6 +237,112 @@ GPTQ_API gptq_status gptq_dequant_matmul(const void *A, gptq_dtype a_dtype, int6
                                          void *stream);
 
 /* ---------------------------------------------------------------------------
+ * Fused products with packed layers, forward and backward: what a model of
+ * quantized layers runs around the product ("Optimization Gptq", "Backends de
+ * kernel"), and the gradients that reach its inputs while the packed weights
+ * stay fixed (adapters, prefixes and biases tuned on a quantized model).
+ *
+ * With W_hat as gptq_dequant_matmul defines it and `act` one of the
+ * activations below, for i < m:
+ *   gptq_dequant_linear           Z = A W_hat^T + bias,  Y = act(Z) + residual
+ *   gptq_dequant_linear_backward  dZ = dY act'(Z),  dA = dZ W_hat,
+ *                                 dbias[r] = sum_i dZ[i][r]
+ *                                 (the residual's gradient is dY itself)
+ *   gptq_dequant_gated            G = A W_gate^T + bias_gate,
+ *                                 U = A W_up^T + bias_up,  H = act(G) U
+ *   gptq_dequant_gated_backward   dG = dH U act'(G),  dU = dH act(G),
+ *                                 dA = dG W_gate + dU W_up, and the column
+ *                                 sums of dG and dU as the biases' gradients
+ * Activations: NONE z; RELU max(z, 0), slope 0 at 0; GELU z Phi(z); GELU_TANH
+ * z sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)); SILU z sigmoid(z).
+ *
+ * Arguments common to the four (device pointers, densely packed, row-major,
+ * aligned to their element type; no output may overlap an input or another
+ * output, but Y may be the residual itself):
+ *   A, dA      [m][d_in], a_dtype / da_dtype, in the original column order.
+ *   Y, H, dY, dH, residual, Z, G, U
+ *              [m][d_out] ([m][d_ff] of the gated pair), all of one dtype:
+ *              y_dtype in the forward calls, dy_dtype in the backward ones.
+ *   Qpacked, scales, zeros, perm, bits, group_size
+ *              as gptq_quantize_layer stored the layer; perm NULL: identity.
+ *              The gated pair's two layers share d_in, bits, group_size and
+ *              one perm (as gptq_quantize_layers writes them: layers that read
+ *              one input share its order).
+ *   bias*      [d_out] ([d_ff]), bias_dtype; NULL: none (bias_dtype is then
+ *              not looked at).
+ *   preact (Z), gate_pre (G), up_pre (U)
+ *              forward: optional outputs, rounded to y_dtype, for the backward
+ *              call; the activation itself sees the unrounded fp32 values.
+ *              The gated pair's are given both or neither.  Backward: inputs;
+ *              preact may be NULL when act is NONE.
+ *   dbias*     fp32 outputs, overwritten (not accumulated); NULL: not formed.
+ *   residual   NULL: none.
+ * Numerics: fp32 sums, one rounding of each output to its dtype.  With an F32
+ * output every product keeps fp32 accuracy; with a BF16 output the weights may
+ * be rounded to 11 significand bits on the way (an eighth of the output's own
+ * rounding).  In a forward call's such rounding a row's groups share one
+ * power-of-two range of 2^29, in a backward call's a group's rows do; values
+ * below it lose precision gradually.  All results are deterministic.
+ * workspace  device scratch of the matching size query's bytes (may be NULL
+ *            when that is 0), 256-byte aligned.  Its contents need not be
+ *            prepared and are not kept: calls of any sizes may share one as
+ *            long as they run one after the other.
+ * Limits: d_in, d_out and d_ff up to 2^19, m up to 2^31 - 1.
+ * m == 0 leaves dbias zero and is a no-op otherwise.  Nothing synchronizes;
+ * every call can be captured into a graph.  Errors: EINVAL (sizes, bits,
+ * group_size, dtype, activation, a required pointer NULL; nothing launched),
+ * ENOMEM (workspace too small or misaligned), EHIP.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+    GPTQ_ACT_NONE = 0,
+    GPTQ_ACT_RELU = 1,
+    GPTQ_ACT_GELU = 2,
+    GPTQ_ACT_GELU_TANH = 3,
+    GPTQ_ACT_SILU = 4
+} gptq_activation;
+
+GPTQ_API size_t gptq_dequant_linear_workspace_size(int64_t m, int64_t d_out, int64_t d_in, int bits, int group_size,
+                                                   gptq_dtype a_dtype, gptq_dtype y_dtype);
+GPTQ_API gptq_status gptq_dequant_linear(const void *A, gptq_dtype a_dtype, int64_t m, int64_t d_in,
+                                         const uint32_t *Qpacked, const float *scales, const float *zeros,
+                                         const int32_t *perm, int64_t d_out, int bits, int group_size,
+                                         const void *bias, gptq_dtype bias_dtype, gptq_activation act,
+                                         const void *residual, void *Y, gptq_dtype y_dtype, void *preact,
+                                         void *workspace, size_t workspace_bytes, void *stream);
+
+GPTQ_API size_t gptq_dequant_linear_backward_workspace_size(int64_t m, int64_t d_out, int64_t d_in, int bits,
+                                                            int group_size, gptq_dtype dy_dtype,
+                                                            gptq_dtype da_dtype);
+GPTQ_API gptq_status gptq_dequant_linear_backward(const void *dY, gptq_dtype dy_dtype, int64_t m, int64_t d_out,
+                                                  const void *preact, gptq_activation act, const uint32_t *Qpacked,
+                                                  const float *scales, const float *zeros, const int32_t *perm,
+                                                  int64_t d_in, int bits, int group_size, void *dA,
+                                                  gptq_dtype da_dtype, float *dbias, void *workspace,
+                                                  size_t workspace_bytes, void *stream);
+
+GPTQ_API size_t gptq_dequant_gated_workspace_size(int64_t m, int64_t d_ff, int64_t d_in, int bits, int group_size,
+                                                  gptq_dtype a_dtype, gptq_dtype y_dtype);
+GPTQ_API gptq_status gptq_dequant_gated(const void *A, gptq_dtype a_dtype, int64_t m, int64_t d_in,
+                                        const uint32_t *Qgate, const float *scales_gate, const float *zeros_gate,
+                                        const uint32_t *Qup, const float *scales_up, const float *zeros_up,
+                                        const int32_t *perm, int64_t d_ff, int bits, int group_size,
+                                        const void *bias_gate, const void *bias_up, gptq_dtype bias_dtype,
+                                        gptq_activation act, void *H, gptq_dtype y_dtype, void *gate_pre,
+                                        void *up_pre, void *workspace, size_t workspace_bytes, void *stream);
+
+GPTQ_API size_t gptq_dequant_gated_backward_workspace_size(int64_t m, int64_t d_ff, int64_t d_in, int bits,
+                                                           int group_size, gptq_dtype dy_dtype,
+                                                           gptq_dtype da_dtype);
+GPTQ_API gptq_status gptq_dequant_gated_backward(const void *dH, gptq_dtype dy_dtype, int64_t m, int64_t d_ff,
+                                                 const void *gate_pre, const void *up_pre, gptq_activation act,
+                                                 const uint32_t *Qgate, const float *scales_gate,
+                                                 const float *zeros_gate, const uint32_t *Qup,
+                                                 const float *scales_up, const float *zeros_up, const int32_t *perm,
+                                                 int64_t d_in, int bits, int group_size, void *dA,
+                                                 gptq_dtype da_dtype, float *dbias_gate, float *dbias_up,
+                                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Stage timing (tracing aid).  gptq_profile_enable(stage_mask): bit s set
  * makes every later call record a pair of hipEvents around stage s's launches
  * on the caller's stream (GPTQ_PROFILE_ALL: every stage; 0: none).  Reading

@@ -10,6 +10,10 @@ is used for device memory and streams only.
     q = quantize_layer(W, H, bits=4, group_size=128, block_size=128,
                        damp=0.01, act_order=False)
     q.qpacked, q.scales, q.zeros, q.perm
+    Y = dequant_matmul(A, q)                       # A W_hat^T on the packed layer
+    Y = dequant_linear(A, q, bias, "gelu", residual)   # the same with its epilogue fused
+    h = dequant_gated(A, gate, up, "silu")         # act(A W_gate^T) * (A W_up^T)
+    dA, _ = dequant_linear_backward(dY, q)         # gradients through packed layers
 
 The library must have been built (python -m post_weight_quantization_04_amd.build);
 the first call into it raises ImportError if libgptq.so is missing (there is
@@ -26,10 +30,14 @@ __all__ = [
     "quantize_layer_workspace_size", "inverse_factor", "packed_words", "num_groups", "QuantizedLayer",
     "LIB_PATH", "F32", "BF16", "profile_enable", "profile_read", "hessian_accumulate_noalloc",
     "hessian_noalloc_max_d_in", "dequant_matmul", "dequant_matmul_workspace_size", "quantize_layers",
+    "ACTIVATIONS", "dequant_linear", "dequant_linear_workspace_size", "dequant_linear_backward",
+    "dequant_linear_backward_workspace_size", "dequant_gated", "dequant_gated_workspace_size",
+    "dequant_gated_backward", "dequant_gated_backward_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq.so")
 F32, BF16 = 0, 1
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _STATUS = {0: "GPTQ_OK", 1: "GPTQ_EINVAL", 2: "GPTQ_ENOTSPD", 3: "GPTQ_EHIP", 4: "GPTQ_ENOMEM"}
 
 
@@ -76,6 +84,21 @@ def _load() -> ctypes.CDLL:
                                        c.c_int, c.c_int, c.c_float, c.c_int, c.c_void_p, c.c_void_p, c.c_void_p,
                                        c.c_void_p, c.c_void_p, c.c_size_t, c.c_void_p]
     L.gptq_quantize_layers.restype = c.c_int
+    i64, i32, ptr, size = c.c_int64, c.c_int, c.c_void_p, c.c_size_t
+    for name in ("linear", "linear_backward", "gated", "gated_backward"):
+        f = getattr(L, f"gptq_dequant_{name}_workspace_size")
+        f.argtypes = [i64, i64, i64, i32, i32, i32, i32]
+        f.restype = size
+    L.gptq_dequant_linear.argtypes = [ptr, i32, i64, i64, ptr, ptr, ptr, ptr, i64, i32, i32, ptr, i32, i32, ptr,
+                                      ptr, i32, ptr, ptr, size, ptr]
+    L.gptq_dequant_linear_backward.argtypes = [ptr, i32, i64, i64, ptr, i32, ptr, ptr, ptr, ptr, i64, i32, i32, ptr,
+                                               i32, ptr, ptr, size, ptr]
+    L.gptq_dequant_gated.argtypes = [ptr, i32, i64, i64, ptr, ptr, ptr, ptr, ptr, ptr, ptr, i64, i32, i32, ptr, ptr,
+                                     i32, i32, ptr, i32, ptr, ptr, ptr, size, ptr]
+    L.gptq_dequant_gated_backward.argtypes = [ptr, i32, i64, i64, ptr, ptr, i32, ptr, ptr, ptr, ptr, ptr, ptr, ptr,
+                                              i64, i32, i32, ptr, i32, ptr, ptr, ptr, size, ptr]
+    for name in ("linear", "linear_backward", "gated", "gated_backward"):
+        getattr(L, f"gptq_dequant_{name}").restype = i32
     L.gptq_inverse_factor.argtypes = [c.c_void_p, c.c_int64, c.c_float, c.c_int, c.c_void_p, c.c_void_p,
                                       c.c_void_p, c.c_size_t, c.c_void_p]
     L.gptq_inverse_factor.restype = c.c_int
@@ -352,6 +375,238 @@ def dequant_matmul(A, q: "QuantizedLayer", out_dtype=None, workspace=None, strea
                                       Y.data_ptr(), _dtype_code(Y), ws.data_ptr() if ws is not None else None,
                                       0 if ws is None else ws.numel(), _stream_ptr(stream)))
     return Y
+
+
+# ---------------------------------------------------------------------------
+# fused products with packed layers, forward and backward
+# ---------------------------------------------------------------------------
+def dequant_linear_workspace_size(m, d_out, d_in, bits, group_size, a_dtype_code, y_dtype_code) -> int:
+    return int(_lib().gptq_dequant_linear_workspace_size(m, d_out, d_in, bits, group_size, a_dtype_code,
+                                                         y_dtype_code))
+
+
+def dequant_linear_backward_workspace_size(m, d_out, d_in, bits, group_size, dy_dtype_code, da_dtype_code) -> int:
+    return int(_lib().gptq_dequant_linear_backward_workspace_size(m, d_out, d_in, bits, group_size, dy_dtype_code,
+                                                                  da_dtype_code))
+
+
+def dequant_gated_workspace_size(m, d_ff, d_in, bits, group_size, a_dtype_code, y_dtype_code) -> int:
+    return int(_lib().gptq_dequant_gated_workspace_size(m, d_ff, d_in, bits, group_size, a_dtype_code, y_dtype_code))
+
+
+def dequant_gated_backward_workspace_size(m, d_ff, d_in, bits, group_size, dy_dtype_code, da_dtype_code) -> int:
+    return int(_lib().gptq_dequant_gated_backward_workspace_size(m, d_ff, d_in, bits, group_size, dy_dtype_code,
+                                                                 da_dtype_code))
+
+
+class _FusedCall:
+    """Checks and buffers of one fused call: operands on one device, a
+    workspace and outputs that belong to the stream the work goes to."""
+
+    def __init__(self, x, name, layers, activation, out_dtype, workspace, stream):
+        torch = _torch()
+        _require(x, name, ndim=2)
+        self.in_code = _dtype_code(x)
+        self.device = x.device
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}; got {activation!r}")
+        self.act = ACTIVATIONS[activation]
+        self.out_dtype = out_dtype or x.dtype
+        if self.out_dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"unsupported out_dtype {self.out_dtype}; use float32 or bfloat16")
+        self.out_code = F32 if self.out_dtype == torch.float32 else BF16
+        q = layers[0]
+        self.d_in, self.d_out = q.d_in, q.scales.shape[1]
+        self.tensors = [x]
+        for l in layers:
+            if (l.d_in, l.bits, l.group_size, l.scales.shape[1]) != (self.d_in, q.bits, q.group_size, self.d_out):
+                raise ValueError("the layers must have the same sizes, bits and group_size")
+            if l.act_order != q.act_order or (l.act_order and l.perm.data_ptr() != q.perm.data_ptr()):
+                raise ValueError("the layers must share one perm (quantize_layers gives them one)")
+            words, groups = packed_words(l.d_in, l.bits), num_groups(l.d_in, l.group_size)
+            for t, n, dt, shape in ((l.qpacked, "qpacked", torch.int32, (words, self.d_out)),
+                                    (l.scales, "scales", torch.float32, (groups, self.d_out)),
+                                    (l.zeros, "zeros", torch.float32, (groups, self.d_out))):
+                self.take(t, n, dt, shape)
+            if l.act_order:
+                self.take(l.perm, "perm", torch.int32, (self.d_in,))
+        self.perm = q.perm.data_ptr() if q.act_order else None
+        self.bits, self.group = q.bits, q.group_size
+        self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if self.stream.device != self.device:
+            raise ValueError(f"the stream belongs to {self.stream.device}, {name} to {self.device}")
+        self.given_ws = workspace
+        if workspace is not None:
+            _require(workspace, "workspace")
+            self.take(workspace, "workspace", workspace.dtype, workspace.shape)
+
+    def take(self, t, name, dtype, shape):
+        """An operand: its device pointer, or None for None."""
+        if t is None:
+            return None
+        _require(t, name, dtype=dtype)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, not on {self.device}")
+        self.tensors.append(t)
+        return t.data_ptr()
+
+    def no_autograd(self, what):
+        torch = _torch()
+        if torch.is_grad_enabled() and any(t.requires_grad for t in self.tensors):
+            raise ValueError(f"autograd does not see through {what}: call it under torch.no_grad() (or inside a "
+                             f"torch.autograd.Function) and {what}_backward for the gradients")
+
+    def empty(self, *shape, dtype=None):
+        return _torch().empty(shape, dtype=dtype or self.out_dtype, device=self.device)
+
+    def workspace(self, need):
+        """(pointer, bytes): the caller's when it suffices, otherwise allocated."""
+        if need == 0:
+            return None, 0
+        w = self.given_ws
+        if w is not None and w.numel() * w.element_size() >= need:
+            return w.data_ptr(), w.numel() * w.element_size()
+        w = self.empty(need, dtype=_torch().uint8)
+        return w.data_ptr(), need
+
+    def __enter__(self):
+        # allocations belong to the stream that uses them, on its own device
+        self.guard = _torch().cuda.stream(self.stream)
+        self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def dequant_linear(A, q: "QuantizedLayer", bias=None, activation="none", residual=None, out_dtype=None,
+                   save_preact=False, workspace=None, stream=None):
+    """Y = act(A W_hat^T + bias) + residual on the packed layer q (gptq_dequant_linear).
+
+    A: [m, d_in] bfloat16/float32; bias: [d_out] bfloat16/float32; residual:
+    [m, d_out] of out_dtype (A's dtype by default); activation: one of
+    ACTIVATIONS.  Returns Y, or (Y, Z) with the pre-activation Z = A W_hat^T +
+    bias when save_preact.  workspace: any device tensor of at least
+    dequant_linear_workspace_size bytes (allocated when absent or too small).
+    Not differentiable by autograd: see dequant_linear_backward."""
+    f = _FusedCall(A, "A", (q,), activation, out_dtype, workspace, stream)
+    m = A.shape[0]
+    if A.shape[1] != f.d_in:
+        raise ValueError(f"A has {A.shape[1]} columns, the layer {f.d_in}")
+    b = f.take(bias, "bias", bias.dtype, (f.d_out,)) if bias is not None else None
+    r = f.take(residual, "residual", f.out_dtype, (m, f.d_out))
+    f.no_autograd("dequant_linear")
+    with f:
+        Y = f.empty(m, f.d_out)
+        Z = f.empty(m, f.d_out) if save_preact else None
+        ws, wsb = f.workspace(dequant_linear_workspace_size(m, f.d_out, f.d_in, f.bits, f.group, f.in_code,
+                                                            f.out_code))
+        _check(_lib().gptq_dequant_linear(A.data_ptr(), f.in_code, m, f.d_in, q.qpacked.data_ptr(),
+                                          q.scales.data_ptr(), q.zeros.data_ptr(), f.perm, f.d_out, f.bits, f.group,
+                                          b, _dtype_code(bias) if bias is not None else 0, f.act, r, Y.data_ptr(),
+                                          f.out_code, Z.data_ptr() if save_preact else None, ws, wsb,
+                                          int(f.stream.cuda_stream)))
+    return (Y, Z) if save_preact else Y
+
+
+def dequant_linear_backward(dY, q: "QuantizedLayer", activation="none", preact=None, bias_grad=False, out_dtype=None,
+                            workspace=None, stream=None):
+    """(dA, dbias) of dequant_linear (gptq_dequant_linear_backward): dZ = dY act'(Z),
+    dA = dZ W_hat, dbias the column sums of dZ.
+
+    dY: [m, d_out] bfloat16/float32; preact: the saved Z of dY's dtype (may be
+    None for activation "none").  dA: [m, d_in] in out_dtype (dY's dtype by
+    default); dbias: [d_out] float32, or None unless bias_grad.  The residual's
+    gradient is dY itself."""
+    f = _FusedCall(dY, "dY", (q,), activation, out_dtype, workspace, stream)
+    m = dY.shape[0]
+    if dY.shape[1] != f.d_out:
+        raise ValueError(f"dY has {dY.shape[1]} columns, the layer {f.d_out} rows")
+    if preact is None and f.act:
+        raise ValueError("preact is required unless activation is 'none'")
+    z = f.take(preact, "preact", dY.dtype, (m, f.d_out))
+    f.no_autograd("dequant_linear")
+    with f:
+        dA = f.empty(m, f.d_in)
+        db = f.empty(f.d_out, dtype=_torch().float32) if bias_grad else None
+        ws, wsb = f.workspace(dequant_linear_backward_workspace_size(m, f.d_out, f.d_in, f.bits, f.group, f.in_code,
+                                                                     f.out_code))
+        _check(_lib().gptq_dequant_linear_backward(dY.data_ptr(), f.in_code, m, f.d_out, z, f.act,
+                                                   q.qpacked.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(),
+                                                   f.perm, f.d_in, f.bits, f.group, dA.data_ptr(), f.out_code,
+                                                   db.data_ptr() if bias_grad else None, ws, wsb,
+                                                   int(f.stream.cuda_stream)))
+    return dA, db
+
+
+def dequant_gated(A, gate: "QuantizedLayer", up: "QuantizedLayer", activation="silu", bias_gate=None, bias_up=None,
+                  out_dtype=None, save_preact=False, workspace=None, stream=None):
+    """H = act(A W_gate^T + bias_gate) * (A W_up^T + bias_up) (gptq_dequant_gated):
+    the gated half of a feed-forward block in one call.
+
+    gate, up: packed layers of the same sizes, bits and group_size sharing one
+    perm (quantize_layers).  Returns H [m, d_ff] in out_dtype (A's dtype by
+    default), or (H, G, U) with both pre-activations when save_preact.  Other
+    arguments as for dequant_linear."""
+    f = _FusedCall(A, "A", (gate, up), activation, out_dtype, workspace, stream)
+    m = A.shape[0]
+    if A.shape[1] != f.d_in:
+        raise ValueError(f"A has {A.shape[1]} columns, the layers {f.d_in}")
+    biases = [b for b in (bias_gate, bias_up) if b is not None]
+    if len(biases) == 2 and biases[0].dtype != biases[1].dtype:
+        raise TypeError("both biases must have the same dtype")
+    bcode = _dtype_code(biases[0]) if biases else 0
+    bg = f.take(bias_gate, "bias_gate", biases[0].dtype if biases else None, (f.d_out,))
+    bu = f.take(bias_up, "bias_up", biases[0].dtype if biases else None, (f.d_out,))
+    f.no_autograd("dequant_gated")
+    with f:
+        H = f.empty(m, f.d_out)
+        G, U = (f.empty(m, f.d_out), f.empty(m, f.d_out)) if save_preact else (None, None)
+        ws, wsb = f.workspace(dequant_gated_workspace_size(m, f.d_out, f.d_in, f.bits, f.group, f.in_code,
+                                                           f.out_code))
+        _check(_lib().gptq_dequant_gated(A.data_ptr(), f.in_code, m, f.d_in, gate.qpacked.data_ptr(),
+                                         gate.scales.data_ptr(), gate.zeros.data_ptr(), up.qpacked.data_ptr(),
+                                         up.scales.data_ptr(), up.zeros.data_ptr(), f.perm, f.d_out, f.bits, f.group,
+                                         bg, bu, bcode, f.act, H.data_ptr(), f.out_code,
+                                         G.data_ptr() if save_preact else None,
+                                         U.data_ptr() if save_preact else None, ws, wsb, int(f.stream.cuda_stream)))
+    return (H, G, U) if save_preact else H
+
+
+def dequant_gated_backward(dH, gate: "QuantizedLayer", up: "QuantizedLayer", gate_pre, up_pre, activation="silu",
+                           bias_grad=False, out_dtype=None, workspace=None, stream=None):
+    """(dA, dbias_gate, dbias_up) of dequant_gated (gptq_dequant_gated_backward):
+    dG = dH U act'(G), dU = dH act(G), dA = dG W_gate + dU W_up, and the column
+    sums of dG and dU.
+
+    dH, gate_pre (G), up_pre (U): [m, d_ff], one dtype (G and U as
+    dequant_gated saved them).  dA: [m, d_in] in out_dtype (dH's dtype by
+    default); the bias gradients: [d_ff] float32, or None unless bias_grad."""
+    f = _FusedCall(dH, "dH", (gate, up), activation, out_dtype, workspace, stream)
+    m = dH.shape[0]
+    if dH.shape[1] != f.d_out:
+        raise ValueError(f"dH has {dH.shape[1]} columns, the layers {f.d_out} rows")
+    if gate_pre is None or up_pre is None:
+        raise ValueError("gate_pre and up_pre are required")
+    g = f.take(gate_pre, "gate_pre", dH.dtype, (m, f.d_out))
+    u = f.take(up_pre, "up_pre", dH.dtype, (m, f.d_out))
+    f.no_autograd("dequant_gated")
+    with f:
+        dA = f.empty(m, f.d_in)
+        dbg, dbu = ((f.empty(f.d_out, dtype=_torch().float32), f.empty(f.d_out, dtype=_torch().float32))
+                    if bias_grad else (None, None))
+        ws, wsb = f.workspace(dequant_gated_backward_workspace_size(m, f.d_out, f.d_in, f.bits, f.group, f.in_code,
+                                                                    f.out_code))
+        _check(_lib().gptq_dequant_gated_backward(dH.data_ptr(), f.in_code, m, f.d_out, g, u, f.act,
+                                                  gate.qpacked.data_ptr(), gate.scales.data_ptr(),
+                                                  gate.zeros.data_ptr(), up.qpacked.data_ptr(), up.scales.data_ptr(),
+                                                  up.zeros.data_ptr(), f.perm, f.d_in, f.bits, f.group,
+                                                  dA.data_ptr(), f.out_code, dbg.data_ptr() if bias_grad else None,
+                                                  dbu.data_ptr() if bias_grad else None, ws, wsb,
+                                                  int(f.stream.cuda_stream)))
+    return dA, dbg, dbu
 
 
 def inverse_factor(H, damp: float = 0.01, act_order: bool = False, workspace=None, stream=None):

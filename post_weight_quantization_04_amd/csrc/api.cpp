@@ -288,6 +288,80 @@ gptq_status check_dequant(int64_t m, int64_t d_out, int64_t d_in, int bits, int 
     return GPTQ_OK;
 }
 
+bool valid_act(const gptq_activation &a) { return raw(a) >= GPTQ_ACT_NONE && raw(a) <= GPTQ_ACT_SILU; }
+
+// sizes of the fused products; in_dtype / out_dtype: of the product's input
+// and result (A and Y, or dY and dA)
+gptq_status check_fused(int64_t m, int64_t d_out, int64_t d_in, int bits, int group_size, int layers,
+                        const gptq_dtype &in_dtype, const gptq_dtype &out_dtype, gptq::FusedShape &f) {
+    int g = 0;
+    gptq_status s = check_dequant(m, d_out, d_in, bits, group_size, g);
+    if (s != GPTQ_OK) return s;
+    if (m > (int64_t)0x7fffffff) return fail(GPTQ_EINVAL, "m must be below 2^31");
+    if (d_in > (int64_t)1 << 19 || d_out > (int64_t)1 << 19)
+        return fail(GPTQ_EINVAL, "d_in and the output width must be at most 2^19");
+    if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype))
+        return fail(GPTQ_EINVAL, "every dtype must be GPTQ_F32 or GPTQ_BF16");
+    f.m = m;
+    f.d_out = d_out;
+    f.d_in = d_in;
+    f.bits = bits;
+    f.group = g;
+    f.ngroups = (int)cdiv(d_in, g);
+    f.layers = layers;
+    f.in_bf16 = in_dtype == GPTQ_BF16;
+    f.out_bf16 = out_dtype == GPTQ_BF16;
+    return GPTQ_OK;
+}
+
+gptq_status check_ws(const void *workspace, size_t bytes, size_t need) {
+    if (need == 0) return GPTQ_OK;
+    if (!workspace || bytes < need)
+        return fail(GPTQ_ENOMEM, "workspace of %zu bytes needed, %zu given", need, workspace ? bytes : 0);
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+        return fail(GPTQ_ENOMEM, "the workspace must be 256-byte aligned");
+    return GPTQ_OK;
+}
+
+gptq_status run_forward(gptq::FusedForward &a, const gptq_dtype &bias_dtype, const gptq_activation &act,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+    if (!valid_act(act)) return fail(GPTQ_EINVAL, "unknown activation (got %d)", raw(act));
+    if ((a.bias[0] || a.bias[1]) && !valid_dtype(bias_dtype))
+        return fail(GPTQ_EINVAL, "bias_dtype must be GPTQ_F32 or GPTQ_BF16");
+    if (a.s.m == 0) return GPTQ_OK;
+    bool ok = a.A && a.Y;
+    for (int l = 0; l < a.s.layers; ++l) ok = ok && a.w[l].Q && a.w[l].scales && a.w[l].zeros;
+    if (!ok) return fail(GPTQ_EINVAL, "a required pointer is NULL");
+    if (a.s.layers == 2 && !a.pre[0] != !a.pre[1])
+        return fail(GPTQ_EINVAL, "gate_pre and up_pre are given both or neither");
+    gptq_status s = check_ws(workspace, workspace_bytes, gptq::fused_forward_ws(a.s));
+    if (s != GPTQ_OK) return s;
+    a.bias_bf16 = (a.bias[0] || a.bias[1]) && bias_dtype == GPTQ_BF16;
+    a.act = raw(act);
+    a.ws = (char *)workspace;
+    HIPCHECK(gptq::fused_forward_launch(a, (hipStream_t)stream));
+    return GPTQ_OK;
+}
+
+gptq_status run_backward(gptq::FusedBackward &a, const gptq_activation &act, void *workspace, size_t workspace_bytes,
+                         void *stream) {
+    if (!valid_act(act)) return fail(GPTQ_EINVAL, "unknown activation (got %d)", raw(act));
+    const bool empty = a.s.m == 0;
+    bool ok = empty || (a.dY && a.dA);
+    for (int l = 0; l < a.s.layers; ++l) ok = ok && (empty || (a.w[l].Q && a.w[l].scales && a.w[l].zeros));
+    if (!ok) return fail(GPTQ_EINVAL, "a required pointer is NULL");
+    if (!empty && a.s.layers == 2 && (!a.pre[0] || !a.pre[1]))
+        return fail(GPTQ_EINVAL, "gate_pre and up_pre are required");
+    if (!empty && a.s.layers == 1 && raw(act) != GPTQ_ACT_NONE && !a.pre[0])
+        return fail(GPTQ_EINVAL, "preact is required unless the activation is GPTQ_ACT_NONE");
+    gptq_status s = check_ws(workspace, workspace_bytes, gptq::fused_backward_ws(a.s));
+    if (s != GPTQ_OK) return s;
+    a.act = raw(act);
+    a.ws = (char *)workspace;
+    HIPCHECK(gptq::fused_backward_launch(a, (hipStream_t)stream));
+    return GPTQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -550,6 +624,116 @@ gptq_status gptq_dequant_matmul(const void *A, gptq_dtype a_dtype, int64_t m, in
     a.ngroups = (int)cdiv(d_in, g);
     HIPCHECK(gptq::dequant_matmul_launch(a, (hipStream_t)stream));
     return GPTQ_OK;
+}
+
+size_t gptq_dequant_linear_workspace_size(int64_t m, int64_t d_out, int64_t d_in, int bits, int group_size,
+                                          gptq_dtype a_dtype, gptq_dtype y_dtype) {
+    gptq::FusedShape f{};
+    if (check_fused(m, d_out, d_in, bits, group_size, 1, a_dtype, y_dtype, f) != GPTQ_OK) return 0;
+    return gptq::fused_forward_ws(f);
+}
+
+gptq_status gptq_dequant_linear(const void *A, gptq_dtype a_dtype, int64_t m, int64_t d_in, const uint32_t *Qpacked,
+                                const float *scales, const float *zeros, const int32_t *perm, int64_t d_out, int bits,
+                                int group_size, const void *bias, gptq_dtype bias_dtype, gptq_activation act,
+                                const void *residual, void *Y, gptq_dtype y_dtype, void *preact, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    g_err.clear();
+    gptq::FusedForward a{};
+    gptq_status s = check_fused(m, d_out, d_in, bits, group_size, 1, a_dtype, y_dtype, a.s);
+    if (s != GPTQ_OK) return s;
+    a.A = A;
+    a.w[0] = {Qpacked, scales, zeros};
+    a.perm = perm;
+    a.bias[0] = bias;
+    a.residual = residual;
+    a.Y = Y;
+    a.pre[0] = preact;
+    return run_forward(a, bias_dtype, act, workspace, workspace_bytes, stream);
+}
+
+size_t gptq_dequant_linear_backward_workspace_size(int64_t m, int64_t d_out, int64_t d_in, int bits, int group_size,
+                                                   gptq_dtype dy_dtype, gptq_dtype da_dtype) {
+    gptq::FusedShape f{};
+    if (check_fused(m, d_out, d_in, bits, group_size, 1, dy_dtype, da_dtype, f) != GPTQ_OK) return 0;
+    return gptq::fused_backward_ws(f);
+}
+
+gptq_status gptq_dequant_linear_backward(const void *dY, gptq_dtype dy_dtype, int64_t m, int64_t d_out,
+                                         const void *preact, gptq_activation act, const uint32_t *Qpacked,
+                                         const float *scales, const float *zeros, const int32_t *perm, int64_t d_in,
+                                         int bits, int group_size, void *dA, gptq_dtype da_dtype, float *dbias,
+                                         void *workspace, size_t workspace_bytes, void *stream) {
+    g_err.clear();
+    gptq::FusedBackward a{};
+    gptq_status s = check_fused(m, d_out, d_in, bits, group_size, 1, dy_dtype, da_dtype, a.s);
+    if (s != GPTQ_OK) return s;
+    a.dY = dY;
+    a.pre[0] = preact;
+    a.w[0] = {Qpacked, scales, zeros};
+    a.perm = perm;
+    a.dA = dA;
+    a.dbias[0] = dbias;
+    return run_backward(a, act, workspace, workspace_bytes, stream);
+}
+
+size_t gptq_dequant_gated_workspace_size(int64_t m, int64_t d_ff, int64_t d_in, int bits, int group_size,
+                                         gptq_dtype a_dtype, gptq_dtype y_dtype) {
+    gptq::FusedShape f{};
+    if (check_fused(m, d_ff, d_in, bits, group_size, 2, a_dtype, y_dtype, f) != GPTQ_OK) return 0;
+    return gptq::fused_forward_ws(f);
+}
+
+gptq_status gptq_dequant_gated(const void *A, gptq_dtype a_dtype, int64_t m, int64_t d_in, const uint32_t *Qgate,
+                               const float *scales_gate, const float *zeros_gate, const uint32_t *Qup,
+                               const float *scales_up, const float *zeros_up, const int32_t *perm, int64_t d_ff,
+                               int bits, int group_size, const void *bias_gate, const void *bias_up,
+                               gptq_dtype bias_dtype, gptq_activation act, void *H, gptq_dtype y_dtype,
+                               void *gate_pre, void *up_pre, void *workspace, size_t workspace_bytes, void *stream) {
+    g_err.clear();
+    gptq::FusedForward a{};
+    gptq_status s = check_fused(m, d_ff, d_in, bits, group_size, 2, a_dtype, y_dtype, a.s);
+    if (s != GPTQ_OK) return s;
+    a.A = A;
+    a.w[0] = {Qgate, scales_gate, zeros_gate};
+    a.w[1] = {Qup, scales_up, zeros_up};
+    a.perm = perm;
+    a.bias[0] = bias_gate;
+    a.bias[1] = bias_up;
+    a.Y = H;
+    a.pre[0] = gate_pre;
+    a.pre[1] = up_pre;
+    return run_forward(a, bias_dtype, act, workspace, workspace_bytes, stream);
+}
+
+size_t gptq_dequant_gated_backward_workspace_size(int64_t m, int64_t d_ff, int64_t d_in, int bits, int group_size,
+                                                  gptq_dtype dy_dtype, gptq_dtype da_dtype) {
+    gptq::FusedShape f{};
+    if (check_fused(m, d_ff, d_in, bits, group_size, 2, dy_dtype, da_dtype, f) != GPTQ_OK) return 0;
+    return gptq::fused_backward_ws(f);
+}
+
+gptq_status gptq_dequant_gated_backward(const void *dH, gptq_dtype dy_dtype, int64_t m, int64_t d_ff,
+                                        const void *gate_pre, const void *up_pre, gptq_activation act,
+                                        const uint32_t *Qgate, const float *scales_gate, const float *zeros_gate,
+                                        const uint32_t *Qup, const float *scales_up, const float *zeros_up,
+                                        const int32_t *perm, int64_t d_in, int bits, int group_size, void *dA,
+                                        gptq_dtype da_dtype, float *dbias_gate, float *dbias_up, void *workspace,
+                                        size_t workspace_bytes, void *stream) {
+    g_err.clear();
+    gptq::FusedBackward a{};
+    gptq_status s = check_fused(m, d_ff, d_in, bits, group_size, 2, dy_dtype, da_dtype, a.s);
+    if (s != GPTQ_OK) return s;
+    a.dY = dH;
+    a.pre[0] = gate_pre;
+    a.pre[1] = up_pre;
+    a.w[0] = {Qgate, scales_gate, zeros_gate};
+    a.w[1] = {Qup, scales_up, zeros_up};
+    a.perm = perm;
+    a.dA = dA;
+    a.dbias[0] = dbias_gate;
+    a.dbias[1] = dbias_up;
+    return run_backward(a, act, workspace, workspace_bytes, stream);
 }
 
 gptq_status gptq_inverse_factor(const float *H, int64_t d_in, float damp, int act_order, int32_t *perm, float *U,

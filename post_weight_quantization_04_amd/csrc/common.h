@@ -154,4 +154,48 @@ struct DequantWs {
 DequantWs dequant_ws_layout(int64_t m, int64_t d_out, int64_t d_in, int bits);
 hipError_t dequant_matmul_launch(const DequantArgs &a, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// Fused products with packed layers (fused.hip): bias, activation, residual,
+// the gated pair, and the gradients with respect to the activations
+// ---------------------------------------------------------------------------
+struct PackedLayer {
+    const uint32_t *Q;      // [words][d_out] packed codes
+    const float *scales;    // [G][d_out]
+    const float *zeros;     // [G][d_out]
+};
+struct FusedShape {
+    int64_t m, d_out, d_in;
+    int bits, group;        // group: effective group size
+    int ngroups;
+    int layers;             // 1, or 2: the gated pair (gate, up)
+    int in_bf16, out_bf16;  // dtype of A / dY and its kin, and of Y / dA
+};
+struct FusedForward {
+    FusedShape s;
+    const void *A;          // [m][d_in]
+    PackedLayer w[2];
+    const int32_t *perm;    // NULL: identity
+    const void *bias[2];    // NULL: none
+    int bias_bf16, act;
+    const void *residual;   // NULL: none
+    void *Y;                // [m][d_out]
+    void *pre[2];           // pre-activations kept (NULL: not)
+    char *ws;
+};
+struct FusedBackward {
+    FusedShape s;
+    const void *dY;         // [m][d_out]
+    const void *pre[2];     // saved pre-activations (Z, or G and U)
+    int act;
+    PackedLayer w[2];
+    const int32_t *perm;
+    void *dA;               // [m][d_in]
+    float *dbias[2];        // NULL: not formed
+    char *ws;
+};
+size_t fused_forward_ws(const FusedShape &s);
+size_t fused_backward_ws(const FusedShape &s);
+hipError_t fused_forward_launch(const FusedForward &a, hipStream_t st);
+hipError_t fused_backward_launch(const FusedBackward &a, hipStream_t st);
+
 }  // namespace gptq
