@@ -1,0 +1,111 @@
+// Device helpers and internal entry points of the fused products with packed
+// layers (fused.hip, fused_gemm.hip).
+#pragma once
+
+#include "common.h"
+
+namespace gptq {
+
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+typedef __attribute__((ext_vector_type(2))) __bf16 fz_bf16x2;
+
+__device__ __forceinline__ float fz_bf16(uint16_t b) { return __builtin_bit_cast(float, (unsigned)b << 16); }
+__device__ __forceinline__ uint16_t fz_to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }   // RNE
+__device__ __forceinline__ float fz_ld(const void *p, int64_t i, int bf16) {
+    return bf16 ? fz_bf16(((const uint16_t *)p)[i]) : ((const float *)p)[i];
+}
+__device__ __forceinline__ void fz_st(void *p, int64_t i, float v, int bf16) {
+    if (bf16)
+        ((uint16_t *)p)[i] = fz_to_bf16(v);
+    else
+        ((float *)p)[i] = v;
+}
+// four consecutive values of an operand whose element 0 is aligned to four
+__device__ __forceinline__ f32x4 fz_ld4(const void *p, int64_t i, int bf16) {
+    if (!bf16) return *(const f32x4 *)((const float *)p + i);
+    const u32x2 u = *(const u32x2 *)((const uint16_t *)p + i);
+    return f32x4{__builtin_bit_cast(float, u[0] << 16), __builtin_bit_cast(float, u[0] & 0xffff0000u),
+                 __builtin_bit_cast(float, u[1] << 16), __builtin_bit_cast(float, u[1] & 0xffff0000u)};
+}
+__device__ __forceinline__ unsigned fz_pack_bf16(float a, float b) {
+    const fz_bf16x2 p = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(unsigned, p);
+}
+__device__ __forceinline__ void fz_st4(void *p, int64_t i, f32x4 v, int bf16) {
+    if (bf16)
+        *(u32x2 *)((uint16_t *)p + i) = u32x2{fz_pack_bf16(v[0], v[1]), fz_pack_bf16(v[2], v[3])};
+    else
+        *(f32x4 *)((float *)p + i) = v;
+}
+
+// ---------------------------------------------------------------------------
+// activations and their slopes (fp32)
+// ---------------------------------------------------------------------------
+constexpr float FZ_SQRT_HALF = 0.70710678118654752f, FZ_INV_SQRT_2PI = 0.39894228040143268f;
+constexpr float FZ_TWO_SQRT_2_PI = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+
+__device__ __forceinline__ float fz_sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+
+template <int ACT>
+__device__ __forceinline__ float fz_act(float z) {
+    if constexpr (ACT == 1) return z < 0.f ? 0.f : z;   // NaN stays NaN
+    if constexpr (ACT == 2) return 0.5f * z * erfcf(-z * FZ_SQRT_HALF);
+    if constexpr (ACT == 3) return z * fz_sigmoid(FZ_TWO_SQRT_2_PI * (z + 0.044715f * z * z * z));
+    if constexpr (ACT == 4) return z * fz_sigmoid(z);
+    return z;
+}
+
+// (beyond |z| = 64 every slope is 0 or 1 in fp32: clamped there, so that no
+// product of a vanishing and an overflowing factor arises; NaN stays NaN)
+template <int ACT>
+__device__ __forceinline__ float fz_slope(float z) {
+    z = z > 64.f ? 64.f : (z < -64.f ? -64.f : z);
+    if constexpr (ACT == 1) return z > 0.f ? 1.f : 0.f;
+    if constexpr (ACT == 2) return 0.5f * erfcf(-z * FZ_SQRT_HALF) + z * FZ_INV_SQRT_2PI * expf(-0.5f * z * z);
+    if constexpr (ACT == 3) {
+        const float u = FZ_TWO_SQRT_2_PI * (z + 0.044715f * z * z * z);
+        const float p = fz_sigmoid(u);
+        return p + z * p * fz_sigmoid(-u) * FZ_TWO_SQRT_2_PI * (1.f + 3.f * 0.044715f * z * z);
+    }
+    if constexpr (ACT == 4) {
+        const float p = fz_sigmoid(z);
+        return p + z * p * fz_sigmoid(-z);
+    }
+    return 1.f;
+}
+
+// f(std::integral_constant<int, act>) for a run-time activation
+template <class F>
+__host__ __device__ __forceinline__ void fz_with_act(int act, F f) {
+    switch (act) {
+        case 1: f(std::integral_constant<int, 1>{}); break;
+        case 2: f(std::integral_constant<int, 2>{}); break;
+        case 3: f(std::integral_constant<int, 3>{}); break;
+        case 4: f(std::integral_constant<int, 4>{}); break;
+        default: f(std::integral_constant<int, 0>{}); break;
+    }
+}
+
+// The eight codes k0 .. k0 + 7 (k0 % 8 == 0) of a row lie in the 64 bits (hi,
+// lo) of the words (bits k0) / 32 and the next one, shifted down by the first
+// code's place in its word: code e is bits [bits e, bits e + bits).
+template <int BITS>
+__device__ __forceinline__ uint64_t fz_codes8(unsigned lo, unsigned hi, int sh) {
+    return (((uint64_t)hi << 32) | (uint64_t)lo) >> sh;
+}
+template <int BITS>
+constexpr bool fz_two_words() { return BITS == 3 || BITS == 8; }   // eight codes may span two words
+template <int BITS>
+__device__ __forceinline__ float fz_code(uint64_t v, int e) {
+    return (float)((unsigned)(v >> (BITS * e)) & ((1u << BITS) - 1u));
+}
+
+// ---------------------------------------------------------------------------
+// dense form (fused_gemm.hip)
+// ---------------------------------------------------------------------------
+size_t dense_forward_ws(const FusedShape &s);
+size_t dense_backward_ws(const FusedShape &s);
+hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st);
+hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st);
+
+}  // namespace gptq

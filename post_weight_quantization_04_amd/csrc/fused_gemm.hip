@@ -1,0 +1,1033 @@
+// Dense form of the fused products with packed layers (many activation rows).
+//
+// The packed weights of the call are written once, dequantized, as 11-bit
+// (f16) values into the workspace, contraction index contiguous, and the
+// product runs as a plain NT matrix product on the f16 matrix cores with the
+// bias, activation, residual or gate product in its epilogue:
+//   forward   Z[i][n]  = sum_k A16[i][k] W16[n][k]   n: output, k: input column
+//   backward  dA[i][n] = sum_k D16[i][k] W16[n][k]   n: input column, k: output
+//             (the gated pair: k runs over the gate's outputs, then the up's)
+// A layer's dequantization costs d_out d_in elements of traffic, the product
+// m times as many multiplications: from about a hundred rows on the products
+// dominate, and the inner loop then carries neither code extraction nor group
+// scales.
+//
+// f16 operands.  Every row of A16 / D16 is scaled by a power of two that
+// brings its largest finite magnitude to [2^14, 2^15), every row n of W16 by
+// one that does the same for its weights; the epilogue undoes both exactly.
+// bf16 activations are then exact in f16 (down to 2^-29 of their row's
+// largest), weights and computed gradients are rounded once to 11 bits, an
+// eighth of a bf16 result's own rounding.  For an F32 result the operands are
+// split in two f16 planes, x = hi + lo (22 bits), and the product is three
+// passes over K, hi hi + hi lo + lo hi (two when the activations are exact),
+// which the matrix cores' fp32 accumulators add in one run.
+#include "fused.h"
+
+#include <algorithm>
+
+namespace gptq {
+
+namespace {
+
+constexpr int GK = 32;                    // contraction elements per stage
+constexpr int64_t DENSE_ROWS = 16384;     // activation rows per pass (bounds the workspace)
+constexpr int BIAS_ROWS = 64;             // rows summed by one work group for a bias gradient
+
+// 2^-e for a positive finite v in [2^e, 2^(e+1)) times 2^14, as a factor and
+// its inverse (both normal); 1 for 0
+__device__ __forceinline__ void pow2_scale(float v, float &mul, float &inv) {
+    int e = (int)((__builtin_bit_cast(unsigned, v) >> 23) & 255u) - 127;   // (subnormals: -127)
+    if (v == 0.f) e = 14;
+    const int t = max(-126, min(126, 14 - e));
+    mul = __builtin_bit_cast(float, (unsigned)(127 + t) << 23);
+    inv = __builtin_bit_cast(float, (unsigned)(127 - t) << 23);
+}
+
+__device__ __forceinline__ float finite_abs(float v) {
+    const float a = fabsf(v);
+    return a < __builtin_inff() ? a : 0.f;   // NaN and infinities do not count
+}
+
+// largest of v over the work group's 256 threads
+__device__ __forceinline__ float block_max(float v) {
+    __shared__ float red[4];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+}
+
+// Eight values as f16 planes at out and, when there are two, out + plane.
+// One plane: the rounded values.  Two: hi, and lo = x - hi; of activations
+// that are exact in f16 (EXACT), x itself again.  Values that are not finite
+// appear in the second plane only, which meets the weights' high plane alone:
+// an infinity must not meet the low one, whose signs are arbitrary.
+// The value is pinned to its register first: otherwise the compiler may round
+// the product behind it to f16 twice, once from its exact value and once from
+// its fp32 one, and the two parts no longer belong together.
+__device__ __forceinline__ void put_planes(uint16_t *out, int64_t plane, int planes, int exact, const float (&v)[8]) {
+    f16x8 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float x = v[e];
+        asm("" : "+v"(x));
+        const bool finite = fabsf(x) < __builtin_inff();
+        hi[e] = (_Float16)(finite || planes == 1 ? x : 0.f);
+        lo[e] = (_Float16)(finite && !exact ? x - (float)hi[e] : x);
+    }
+    *(f16x8 *)out = hi;
+    if (planes > 1) *(f16x8 *)(out + plane) = lo;
+}
+
+// ---------------------------------------------------------------------------
+// forward operands: rows of A (gathered into processing order), weights [n][k]
+// ---------------------------------------------------------------------------
+struct ForwardPrep {
+    const void *A;
+    int a_bf16, vec;            // vec: whole aligned 16-byte pieces
+    const int32_t *perm;
+    int64_t m, d_in, kp;        // kp: d_in padded to whole stages
+    uint16_t *A16;              // [m][planes_a][kp]
+    int planes_a;
+    float *fa;                  // [m] inverse row factors
+    int in_lds;                 // the row fits the launch's LDS
+    PackedLayer w[2];
+    int64_t d_out, nwords;
+    int g, ngroups, layers;
+    uint16_t *W16;              // [layers][d_out][planes_w][kp]
+    int planes_w;
+    float *fw;                  // [layers][d_out] inverse factors
+    int64_t row_blocks;         // work groups of the activation rows, then those of the weights
+    int kchunks;
+};
+
+__device__ void prep_row(const ForwardPrep &p, int64_t i, char *lds) {
+    const int tid = threadIdx.x;
+    const int esize = p.a_bf16 ? 2 : 4;
+    const char *row = (const char *)p.A + i * p.d_in * esize;
+    float mx = 0.f;
+    if (p.vec) {
+        const int np = (int)(p.d_in * esize / 16);
+        for (int q = tid; q < np; q += 256) {
+            const u32x4 u = ((const u32x4 *)row)[q];
+            if (p.in_lds) ((u32x4 *)lds)[q] = u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const unsigned x = u[e];   // (the compiler's bit cast of a vector element itself takes element 0)
+                if (p.a_bf16) {
+                    mx = fmaxf(mx, finite_abs(__builtin_bit_cast(float, x << 16)));
+                    mx = fmaxf(mx, finite_abs(__builtin_bit_cast(float, x & 0xffff0000u)));
+                } else {
+                    mx = fmaxf(mx, finite_abs(__builtin_bit_cast(float, x)));
+                }
+            }
+        }
+    } else {
+        for (int64_t k = tid; k < p.d_in; k += 256) {
+            const float v = fz_ld(row, k, p.a_bf16);
+            if (p.in_lds) fz_st(lds, k, v, p.a_bf16);
+            mx = fmaxf(mx, finite_abs(v));
+        }
+    }
+    float mul, inv;
+    pow2_scale(block_max(mx), mul, inv);   // (its barriers also cover the staged row)
+    if (tid == 0) p.fa[i] = inv;
+    const void *src = p.in_lds ? (const void *)lds : (const void *)row;
+    uint16_t *out = p.A16 + i * p.planes_a * p.kp;
+    for (int64_t k0 = 8 * tid; k0 < p.kp; k0 += 8 * 256) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t k = k0 + e;
+            v[e] = k < p.d_in ? fz_ld(src, p.perm ? (int64_t)p.perm[k] : k, p.a_bf16) * mul : 0.f;
+        }
+        put_planes(out + k0, p.kp, p.planes_a, p.a_bf16, v);
+    }
+}
+
+// One work group: 32 rows of the layer(s) and FW_K of their columns.  A wave
+// takes 8 rows by 64 columns at a time, so that it reads words of eight rows
+// side by side and writes whole 128-byte lines.
+constexpr int FW_ROWS = 32, FW_K = 1024;
+template <int BITS>
+__device__ void prep_weights(const ForwardPrep &p, int64_t b, float *lds) {
+    const int tid = threadIdx.x;
+    const int64_t tiles = cdiv(p.d_out, FW_ROWS);
+    const int kc = (int)(b % p.kchunks);
+    const int64_t t = b / p.kchunks;
+    const int l = (int)(t / tiles);
+    const int64_t r0 = (t % tiles) * FW_ROWS;
+    const PackedLayer w = p.w[l];
+    // the rows' largest scales, over all groups
+    float mx = 0.f;
+    {
+        const int64_t r = std::min<int64_t>(r0 + (tid & 31), p.d_out - 1);
+        for (int gi = tid >> 5; gi < p.ngroups; gi += 8) mx = fmaxf(mx, finite_abs(w.scales[(int64_t)gi * p.d_out + r]));
+        lds[tid] = mx;
+    }
+    __syncthreads();
+    const int wave = tid >> 6, lane = tid & 63;
+    const int rl = 8 * wave + (lane & 7);       // row within the tile
+    const int64_t r = std::min<int64_t>(r0 + rl, p.d_out - 1);
+    mx = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, lds[32 * e + rl]);
+    float mul, inv;
+    pow2_scale(mx * (float)((1 << BITS) - 1), mul, inv);
+    if (kc == 0 && lane < 8 && r0 + rl < p.d_out) p.fw[l * p.d_out + r] = inv;
+    if (r0 + rl >= p.d_out) return;
+    uint16_t *out = p.W16 + (l * p.d_out + r) * p.planes_w * p.kp;
+    const int64_t kend = std::min<int64_t>(p.kp, (int64_t)(kc + 1) * FW_K);
+    for (int64_t k0 = (int64_t)kc * FW_K + 8 * (lane >> 3); k0 < kend; k0 += 64) {
+        float v[8];
+        if (k0 < p.d_in) {
+            const int64_t pos = BITS * k0, j = pos >> 5;
+            const unsigned lo = w.Q[j * p.d_out + r];
+            const unsigned hi = fz_two_words<BITS>() ? w.Q[std::min<int64_t>(j + 1, p.nwords - 1) * p.d_out + r] : 0u;
+            const uint64_t c = fz_codes8<BITS>(lo, hi, (int)(pos & 31));
+            const int64_t gi = k0 / p.g;
+            const float s = w.scales[gi * p.d_out + r] * mul, z = w.zeros[gi * p.d_out + r];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = k0 + e < p.d_in ? (fz_code<BITS>(c, e) - z) * s : 0.f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        }
+        put_planes(out + k0, p.kp, p.planes_w, 0, v);
+    }
+}
+
+template <int BITS>
+__global__ __launch_bounds__(256) void forward_prep_kernel(ForwardPrep p) {
+    extern __shared__ __attribute__((aligned(16))) char dyn[];
+    if ((int64_t)blockIdx.x < p.row_blocks)
+        prep_row(p, blockIdx.x, dyn);
+    else
+        prep_weights<BITS>(p, (int64_t)blockIdx.x - p.row_blocks, (float *)dyn);
+}
+
+// ---------------------------------------------------------------------------
+// backward operands: dZ rows, weights [input column][output]
+// ---------------------------------------------------------------------------
+struct BackwardPrep {
+    const void *dY;
+    const void *pre[2];
+    int act;
+    int bf16, vec;              // vec: rows of whole aligned 8-element pieces
+    int64_t m, d_out, kp;       // kp: d_out padded to whole stages
+    int layers;
+    uint16_t *D16;              // [m][planes_a][layers][kp]
+    int planes_a;
+    float *fa;                  // [m] row factors (mul), then [m] their inverses
+    float *bias_part;           // [row blocks][layers][d_out], or NULL
+    PackedLayer w[2];
+    const int32_t *perm;
+    int64_t d_in, nwords;
+    int g, ngroups, wvec;       // wvec: four rows' words load together
+    float *fg;                  // [ngroups] weight factors (mul), then their inverses
+    uint16_t *W16;              // [d_in][planes_w][layers][kp]
+    int planes_w;
+    float *fw;                  // [d_in] inverse factors, original order
+    int64_t dz_blocks, dz_cols; // dZ tiles, then weight tiles
+};
+
+// First pass: a bound on every row's |dZ| (one work group per row: |act'| and
+// |act(z) / z| are below 1.13 and 1), and every group's largest scale
+__global__ __launch_bounds__(256) void backward_range_kernel(BackwardPrep p) {
+    const int tid = threadIdx.x;
+    float mul, inv;
+    if ((int64_t)blockIdx.x < p.m) {
+        const int64_t i = blockIdx.x, o = i * p.d_out;
+        float md = 0.f, mg = 0.f, mu = 0.f;
+        auto fold = [&](float &mx, const void *x) {
+            if (p.vec) {
+                for (int64_t r = 4 * tid; r < p.d_out; r += 4 * 256) {
+                    const f32x4 v = fz_ld4(x, o + r, p.bf16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx = fmaxf(mx, finite_abs(v[e]));
+                }
+            } else {
+                for (int64_t r = tid; r < p.d_out; r += 256) mx = fmaxf(mx, finite_abs(fz_ld(x, o + r, p.bf16)));
+            }
+        };
+        fold(md, p.dY);
+        if (p.layers == 2) {
+            fold(mg, p.pre[0]);
+            fold(mu, p.pre[1]);
+        }
+        md = block_max(md);
+        if (p.layers == 2) {
+            mg = block_max(mg);
+            mu = block_max(mu);
+        }
+        const float f = p.layers == 2 ? fmaxf(mg, 1.13f * mu) : (p.pre[0] ? 1.13f : 1.f);
+        // (an overflowing bound: the largest finite one)
+        pow2_scale(fminf(md * f, 3.0e38f), mul, inv);
+        if (tid == 0) {
+            p.fa[i] = mul;
+            p.fa[p.m + i] = inv;
+        }
+    } else {
+        const int gi = (int)((int64_t)blockIdx.x - p.m);
+        float mx = 0.f;
+        for (int l = 0; l < p.layers; ++l)
+            for (int64_t r = tid; r < p.d_out; r += 256)
+                mx = fmaxf(mx, finite_abs(p.w[l].scales[(int64_t)gi * p.d_out + r]));
+        mx = block_max(mx);
+        if (tid == 0) p.fg[gi] = mx;
+    }
+}
+
+// 64 rows by 256 columns of dZ (of dG and dU): rounded to f16 planes, and the
+// columns' sums over the tile's rows when bias gradients are wanted
+__device__ void prep_dz(const BackwardPrep &p, int64_t b, float *lds) {
+    const int tid = threadIdx.x;
+    const int64_t cb = b % p.dz_cols, rb = b / p.dz_cols;
+    const int64_t r0 = cb * 256 + 8 * (tid & 31);
+    const int64_t ilast = std::min<int64_t>(p.m, (rb + 1) * BIAS_ROWS);
+    float sum[2][8] = {};
+    auto load8 = [&](const void *x, int64_t o, float (&v)[8]) {
+        if (p.vec) {
+            if (r0 < p.d_out) {
+                const f32x4 a = fz_ld4(x, o, p.bf16), c = fz_ld4(x, o + 4, p.bf16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = a[e];
+                    v[4 + e] = c[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = 0.f;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = r0 + e < p.d_out ? fz_ld(x, o + e, p.bf16) : 0.f;
+        }
+    };
+    auto put = [&](int l, int64_t i, const float (&d)[8], float mul) {
+        if (r0 >= p.kp) return;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[e] = r0 + e < p.d_out ? d[e] * mul : 0.f;
+            if (r0 + e < p.d_out) sum[l][e] += d[e];
+        }
+        put_planes(p.D16 + (i * p.planes_a * p.layers + l) * p.kp + r0, p.layers * p.kp, p.planes_a, 0, v);
+    };
+    for (int64_t i = rb * BIAS_ROWS + (tid >> 5); i < ilast; i += 8) {
+        const int64_t o = i * p.d_out + r0;
+        const float mul = p.fa[i];
+        float d[8], z[8], u[8];
+        load8(p.dY, o, d);
+        if (p.layers == 2) {
+            load8(p.pre[0], o, z);
+            load8(p.pre[1], o, u);
+            float dg[8], du[8];
+            fz_with_act(p.act, [&](auto act) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dg[e] = d[e] * u[e] * fz_slope<decltype(act)::value>(z[e]);
+                    du[e] = d[e] * fz_act<decltype(act)::value>(z[e]);
+                }
+            });
+            put(0, i, dg, mul);
+            put(1, i, du, mul);
+        } else {
+            if (p.act != 0) {
+                load8(p.pre[0], o, z);
+                fz_with_act(p.act, [&](auto act) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d[e] *= fz_slope<decltype(act)::value>(z[e]);
+                });
+            }
+            put(0, i, d, mul);
+        }
+    }
+    if (!p.bias_part) return;
+    // the eight row lanes of a column, added in their order
+    for (int l = 0; l < p.layers; ++l) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) lds[(tid >> 5) * 256 + 8 * (tid & 31) + e] = sum[l][e];
+        __syncthreads();
+        float v = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v += lds[256 * e + tid];
+        if (cb * 256 + tid < p.d_out) p.bias_part[(rb * p.layers + l) * p.d_out + cb * 256 + tid] = v;
+    }
+}
+
+// 512 outputs by 32 processing columns: a thread turns blocks of 8 outputs by
+// 8 columns around in registers, so that words are read and rows of W16
+// written as whole lines
+constexpr int BW_ROWS = 512, BW_COLS = 32;
+template <int BITS>
+__device__ void prep_weights_t(const BackwardPrep &p, int64_t b) {
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int64_t rtiles = cdiv(p.kp, BW_ROWS);
+    const int64_t ctiles = cdiv(p.d_in, BW_COLS);
+    const int l = (int)(b / (rtiles * ctiles));
+    const int64_t t = b % (rtiles * ctiles);
+    const int64_t r0 = (t % rtiles) * BW_ROWS + 8 * lane;
+    const int64_t k0 = (t / rtiles) * BW_COLS + 8 * wave;
+    if (r0 >= p.kp || k0 >= p.d_in) return;
+    const PackedLayer w = p.w[l];
+    const int64_t gi = k0 / p.g;
+    float mul, inv;
+    pow2_scale(p.fg[gi] * (float)((1 << BITS) - 1), mul, inv);
+    const int64_t pos = BITS * k0, j = pos >> 5, j1 = std::min<int64_t>(j + 1, p.nwords - 1);
+    const int sh = (int)(pos & 31);
+    float s[8], z[8];
+    unsigned lo[8], hi[8];
+    const bool whole = p.wvec && r0 + 8 <= p.d_out;
+    if (whole) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x4 sv = *(const f32x4 *)(w.scales + gi * p.d_out + r0 + 4 * h);
+            const f32x4 zv = *(const f32x4 *)(w.zeros + gi * p.d_out + r0 + 4 * h);
+            const u32x4 lv = *(const u32x4 *)(w.Q + j * p.d_out + r0 + 4 * h);
+            const u32x4 hv = fz_two_words<BITS>() ? *(const u32x4 *)(w.Q + j1 * p.d_out + r0 + 4 * h)
+                                                  : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[4 * h + e] = sv[e] * mul;
+                z[4 * h + e] = zv[e];
+                lo[4 * h + e] = lv[e];
+                hi[4 * h + e] = hv[e];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t r = r0 + e;
+            const bool in = r < p.d_out;
+            s[e] = in ? w.scales[gi * p.d_out + r] * mul : 0.f;
+            z[e] = in ? w.zeros[gi * p.d_out + r] : 0.f;
+            lo[e] = in ? w.Q[j * p.d_out + r] : 0u;
+            hi[e] = in && fz_two_words<BITS>() ? w.Q[j1 * p.d_out + r] : 0u;
+        }
+    }
+    uint64_t c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = fz_codes8<BITS>(lo[e], hi[e], sh);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (k0 + k >= p.d_in) break;
+        const int64_t col = p.perm ? (int64_t)p.perm[k0 + k] : k0 + k;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (fz_code<BITS>(c[e], k) - z[e]) * s[e];
+        put_planes(p.W16 + (col * p.planes_w * p.layers + l) * p.kp + r0, p.layers * p.kp, p.planes_w, 0, v);
+        if (l == 0 && r0 == 0) p.fw[col] = inv;
+    }
+}
+
+template <int BITS>
+__global__ __launch_bounds__(256) void backward_prep_kernel(BackwardPrep p) {
+    __shared__ float lds[2048];
+    if ((int64_t)blockIdx.x < p.dz_blocks)
+        prep_dz(p, blockIdx.x, lds);
+    else
+        prep_weights_t<BITS>(p, (int64_t)blockIdx.x - p.dz_blocks);
+}
+
+// a bias gradient from its row blocks' sums, in their order; more: added to
+// what earlier passes left
+__global__ __launch_bounds__(256) void bias_reduce_kernel(const float *part, int64_t blocks, int layers,
+                                                          int64_t d_out, float *db0, float *db1, int more) {
+    const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int l = blockIdx.y;
+    float *db = l ? db1 : db0;
+    if (r >= d_out || !db) return;
+    float v = more ? db[r] : 0.f;
+    for (int64_t b = 0; b < blocks; ++b) v += part[(b * layers + l) * d_out + r];
+    db[r] = v;
+}
+
+// ---------------------------------------------------------------------------
+// the product
+// ---------------------------------------------------------------------------
+struct Gemm {
+    const uint16_t *A, *B;      // f16 [m][lda], [layers * n][ldb]
+    int64_t lda, ldb;
+    int64_t kp;                 // elements of one pass over the contraction (whole stages)
+    int passes;                 // pass 1 reads B's second plane, pass 2 (with exact: pass 0) A's
+    int exact;
+    int64_t a_plane, b_plane;   // elements between the planes of a row
+    int64_t m, n;
+    int layers;                 // 2: the gated pair's forward product
+    const float *fa, *fw;       // inverse factors [m], [layers * n]
+    const void *bias[2];
+    int bias_bf16, act;
+    const void *residual;
+    void *Y;
+    void *pre[2];
+    int out_bf16, vec;          // vec: four consecutive outputs load and store together
+    float *part;                // [nsplit][layers][m][n] when nsplit > 1
+    int nsplit;
+    int mt, nt;                 // tiles
+};
+
+// The epilogue of four consecutive columns n .. n + 3 of row i (of both
+// layers, when gated), from their sums
+template <bool GATED>
+__device__ __forceinline__ void epilogue4(const Gemm &p, int64_t i, int64_t n, float fa, f32x4 z, f32x4 u) {
+    const int64_t o = i * p.n + n;
+    const int count = (int)std::min<int64_t>(4, p.n - n);
+    auto load = [&](const void *x, int64_t at, int bf16) {
+        if (p.vec) return fz_ld4(x, at, bf16);   // the four exist together
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < count) v[e] = fz_ld(x, at + e, bf16);
+        return v;
+    };
+    auto store = [&](void *x, f32x4 v) {
+        if (p.vec) {
+            fz_st4(x, o, v, p.out_bf16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < count) fz_st(x, o + e, v[e], p.out_bf16);
+        }
+    };
+    z = z * fa * load(p.fw, n, 0);
+    if (p.bias[0]) z += load(p.bias[0], n, p.bias_bf16);
+    if (p.pre[0]) store(p.pre[0], z);
+    f32x4 y;
+    fz_with_act(p.act, [&](auto act) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = fz_act<decltype(act)::value>(z[e]);
+    });
+    if constexpr (GATED) {
+        u = u * fa * load(p.fw, p.n + n, 0);
+        if (p.bias[1]) u += load(p.bias[1], n, p.bias_bf16);
+        if (p.pre[1]) store(p.pre[1], u);
+        y *= u;
+    }
+    if (p.residual) y += load(p.residual, o, p.out_bf16);
+    store(p.Y, y);
+}
+
+typedef __attribute__((address_space(3))) void gm_lds_void;
+
+template <int N>
+__device__ __forceinline__ void gm_wait() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+// barrier without the fence of __syncthreads(), which would wait for every
+// stage in flight; this wave's LDS reads are drained first
+__device__ __forceinline__ void gm_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+// buffer resource over [p, p + bytes), base and size in scalar registers
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t gm_rsrc(const void *p, int64_t bytes) {
+    const uint64_t b = reinterpret_cast<uint64_t>(p);
+    const uint64_t bu = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((unsigned)(b >> 32)) << 32) |
+                        (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((unsigned)b);
+    const int n = __builtin_amdgcn_readfirstlane((int)std::min<int64_t>(std::max<int64_t>(bytes, 0), (int64_t)0x7fffffff));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)bu, (short)0, n, 0x00020000);
+}
+
+// C tile of 256 columns n by 64 MI rows, four waves of 128 by 32 MI as 32 x 32
+// MFMA tiles.  The weights are the MFMA's first operand, so that a lane holds
+// four consecutive columns of one activation row.  Both operands move by
+// 16-byte buffer loads straight into a ring of four LDS stages of 32 k;
+// rows of 64 bytes whose 16-byte pieces are permuted so that the operand
+// reads of a wave fall on distinct banks.  Each half stage's MFMAs run
+// between the reads of the next half's operands and half of a refill; the
+// wait for a stage counts loads, so two later stages stay in flight across
+// the one barrier per stage.
+//
+// The sums leave through LDS, 64 rows at a time in two buffers, so that the
+// epilogue reads and writes whole row segments.
+template <int MI, bool GATED>
+__global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
+    constexpr int BM = 64 * MI, BN = 256, NBUF = 4;
+    constexpr int NSIDE = BN * GK * 2, STAGE = NSIDE + BM * GK * 2;   // bytes
+    constexpr int NDMA = 4, MDMA = MI;                                // loads per wave and stage
+    constexpr int PER_STAGE = NDMA + MDMA;
+    constexpr int COLS = GATED ? 128 : 256;                           // columns n of one layer
+    constexpr int EROW = 256 + 4;                                     // floats of an epilogue row (padded)
+    __shared__ __attribute__((aligned(16))) char lds[std::max(NBUF * STAGE, 2 * 64 * EROW * 4)];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = wave >> 1, wm = wave & 1;
+    const int h = lane >> 5, li = lane & 31;
+
+    // Work groups go round the 8 XCDs in turn; each XCD takes a contiguous
+    // run of tiles, ordered in strips of four tiles n by all tiles m, so that
+    // the tiles it works on at once share their operands in its L2.
+    const int total = p.mt * p.nt * p.nsplit;
+    const int q8 = total / 8, r8 = total % 8;
+    const int x = (int)blockIdx.x % 8, y = (int)blockIdx.x / 8;
+    int id = x * q8 + min(x, r8) + y;
+    const int split = id / (p.mt * p.nt);
+    id -= split * p.mt * p.nt;
+    const int strip = id / (4 * p.mt), in = id - strip * 4 * p.mt;
+    const int width = min(4, p.nt - 4 * strip);
+    const int64_t m0 = (int64_t)(in / width) * BM, n0 = (int64_t)(4 * strip + in % width) * COLS;
+
+    const int spp = (int)(p.kp / GK);                 // stages per pass
+    const int all = spp * p.passes;
+    const int st0 = (int)((int64_t)all * split / p.nsplit);
+    const int nst = (int)((int64_t)all * (split + 1) / p.nsplit) - st0;   // >= 1
+
+    // rows past the end re-read the last one (only results that are never
+    // stored see them)
+    const int arows = (int)(std::min<int64_t>(p.m, m0 + BM) - m0);
+    const int brows = (int)(std::min<int64_t>(p.n, n0 + COLS) - n0);
+    const __amdgpu_buffer_rsrc_t arsrc = gm_rsrc(p.A + m0 * p.lda, (int64_t)arows * p.lda * 2);
+    const int64_t bfirst = (GATED && wave >= 2 ? p.n : 0) + n0;   // waves 2, 3 move the up layer's rows
+    const __amdgpu_buffer_rsrc_t brsrc = gm_rsrc(p.B + bfirst * p.ldb, (int64_t)brows * p.ldb * 2);
+    auto swz = [](int row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); };
+    int boff[4], aoff[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int row = 16 * (NDMA * wave + q) + (lane >> 2);
+        const int src = std::min(GATED ? row & 127 : row, brows - 1);
+        boff[q] = src * (int)p.ldb * 2 + 16 * ((lane & 3) ^ swz(row));
+    }
+#pragma unroll
+    for (int q = 0; q < MDMA; ++q) {
+        const int row = 16 * (MDMA * wave + q) + (lane >> 2);
+        aoff[q] = std::min(row, arows - 1) * (int)p.lda * 2 + 16 * ((lane & 3) ^ swz(row));
+    }
+    // first (part 0) or second half of this wave's loads of stage st; stages
+    // past the end re-read the last one, unused
+    auto issue = [&](int st, int part) {
+        char *buf = lds + (st % NBUF) * STAGE;
+        const int s = st0 + std::min(st, nst - 1);
+        const int pass = (s >= spp) + (s >= 2 * spp), kk = (s - pass * spp) * GK * 2;
+        const int bk = __builtin_amdgcn_readfirstlane(kk + (pass == 1 ? (int)p.b_plane * 2 : 0));
+        const int ak = __builtin_amdgcn_readfirstlane(kk + (pass == (p.exact ? 0 : 2) ? (int)p.a_plane * 2 : 0));
+#pragma unroll
+        for (int q = NDMA / 2 * part; q < NDMA / 2 * (part + 1); ++q)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(brsrc, (gm_lds_void *)(buf + (NDMA * wave + q) * 1024), 16,
+                                                     boff[q], bk, 0, 0);
+#pragma unroll
+        for (int q = MDMA / 2 * part; q < MDMA / 2 * (part + 1); ++q)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(arsrc, (gm_lds_void *)(buf + NSIDE + (MDMA * wave + q) * 1024),
+                                                     16, aoff[q], ak, 0, 0);
+    };
+
+    // operand reads: lane l supplies row l % 32 of a 32-row tile, k 8 (l / 32) .. +7
+    const int sw = swz(li);
+    int brow[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) brow[j] = (GATED ? (j >> 1) * 128 + wn * 64 + (j & 1) * 32 : wn * 128 + 32 * j) + li;
+    const int arow = wm * 32 * MI + li;
+    auto frags = [&](int st, int ks, f16x8 (&fb)[4], f16x8 (&fa)[MI]) {
+        const char *buf = lds + (st % NBUF) * STAGE;
+        const int piece = 16 * ((2 * ks + h) ^ sw);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fb[j] = *(const f16x8 *)(buf + brow[j] * GK * 2 + piece);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) fa[i] = *(const f16x8 *)(buf + NSIDE + (arow + 32 * i) * GK * 2 + piece);
+    };
+    f32x16 acc[4][MI];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < MI; ++i) acc[j][i] = f32x16{};
+    auto products = [&](const f16x8 (&fb)[4], const f16x8 (&fa)[MI]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+                acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[j], fa[i], acc[j][i], 0, 0, 0);
+    };
+    // the half stage's instruction order: operand reads one per MFMA, then
+    // its loads, spread over the rest
+    auto spread = [] {
+        constexpr int MFMA = 0x008, VMEM = 0x010, DSR = 0x100;
+#pragma unroll
+        for (int i = 0; i < 4 + MI; ++i) {
+            __builtin_amdgcn_sched_group_barrier(DSR, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < PER_STAGE / 2; ++i) {
+            __builtin_amdgcn_sched_group_barrier(VMEM, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(MFMA, MI == 4 ? 2 : 1, 0);
+        }
+    };
+    f16x8 fb0[4], fa0[MI], fb1[4], fa1[MI];
+    for (int st = 0; st < NBUF - 1; ++st) {
+        issue(st, 0);
+        issue(st, 1);
+    }
+    gm_wait<(NBUF - 2) * PER_STAGE>();     // stage 0 landed
+    gm_barrier();
+    issue(NBUF - 1, 0);
+    frags(0, 0, fb0, fa0);
+    for (int st = 0; st < nst - 1; ++st) {
+        frags(st, 1, fb1, fa1);
+        issue(st - 1 + NBUF, 1);
+        products(fb0, fa0);
+        spread();
+        __builtin_amdgcn_sched_barrier(0);
+        gm_wait<(NBUF - 2) * PER_STAGE>(); // stage st + 1 landed
+        gm_barrier();                      // every wave has read stage st: its buffer is free
+        __builtin_amdgcn_sched_barrier(0);
+        frags(st + 1, 0, fb0, fa0);
+        issue(st + NBUF, 0);
+        products(fb1, fa1);
+        spread();
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    frags(nst - 1, 1, fb1, fa1);
+    products(fb0, fa0);
+    products(fb1, fa1);
+    gm_wait<0>();   // the loads past the end must land before the ring is reused
+    gm_barrier();
+
+    // lane (h, li), register 4 q + e of tile (j, i) <-> column 8 q + 4 h + e, row li
+    constexpr int TPR = COLS / 4;   // threads per row of outputs
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        float *out = (float *)lds + (i & 1) * 64 * EROW;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int col = brow[j] - li + 8 * q + 4 * h;
+                *(f32x4 *)(out + (wm * 32 + li) * EROW + col) =
+                    f32x4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+            }
+        gm_barrier();   // (the buffer two passes back was read before the previous barrier)
+        const int c = 4 * ((int)threadIdx.x % TPR);
+        for (int rr = (int)threadIdx.x / TPR; rr < 64; rr += 256 / TPR) {
+            const int64_t row = m0 + (rr >> 5) * 32 * MI + 32 * i + (rr & 31), n = n0 + c;
+            if (row >= p.m || n >= p.n) continue;
+            const f32x4 z = *(const f32x4 *)(out + rr * EROW + c);
+            f32x4 u = {0.f, 0.f, 0.f, 0.f};
+            if (GATED) u = *(const f32x4 *)(out + rr * EROW + 128 + c);
+            if (p.nsplit > 1) {
+                float *part = p.part + ((int64_t)split * p.layers * p.m + row) * p.n + n;
+                if (p.vec) {
+                    *(f32x4 *)part = z;
+                    if (GATED) *(f32x4 *)(part + p.m * p.n) = u;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < p.n) {
+                            part[e] = z[e];
+                            if (GATED) part[p.m * p.n + e] = u[e];
+                        }
+                }
+            } else {
+                epilogue4<GATED>(p, row, n, p.fa[row], z, u);
+            }
+        }
+    }
+}
+
+// the splits' sums in split order, and the epilogue: four columns per thread
+template <bool GATED>
+__global__ __launch_bounds__(256) void split_reduce_kernel(Gemm p) {
+    const int64_t quads = (p.n + 3) / 4;
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= p.m * quads) return;
+    const int64_t i = t / quads, n = 4 * (t - i * quads);
+    f32x4 z = {0.f, 0.f, 0.f, 0.f}, u = z;
+    for (int s = 0; s < p.nsplit; ++s) {
+        const float *z0 = p.part + ((int64_t)s * p.layers * p.m + i) * p.n + n;
+        const float *u0 = z0 + p.m * p.n;
+        if (p.vec) {
+            z += *(const f32x4 *)z0;
+            if (GATED) u += *(const f32x4 *)u0;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < p.n) {
+                    z[e] += z0[e];
+                    if (GATED) u[e] += u0[e];
+                }
+        }
+    }
+    epilogue4<GATED>(p, i, n, p.fa[i], z, u);
+}
+
+int64_t pad_stage(int64_t k) { return cdiv(k, GK) * GK; }
+bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+struct Plan {
+    int mi, mt, nt, nsplit;
+};
+// Tiles of 256 rows unless half as many would do; k splits for grids that
+// leave CUs idle, each of at least eight stages.
+Plan plan_gemm(int64_t m, int64_t n, int layers, int stages) {
+    Plan p;
+    const int cols = layers == 2 ? 128 : 256;
+    p.nt = (int)cdiv(n, cols);
+    p.mi = m > 128 ? 4 : 2;
+    p.mt = (int)cdiv(m, 64 * p.mi);
+    const int64_t tiles = (int64_t)p.mt * p.nt;
+    p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, (int64_t)stages / 8, (int64_t)16}));
+    return p;
+}
+
+struct Layout {
+    size_t bytes = 0;
+    char *base;
+    explicit Layout(char *b) : base(b) {}
+    template <class T>
+    T *take(int64_t count) {
+        char *p = base + bytes;   // (a size query only reads `bytes`)
+        bytes += align256((size_t)count * sizeof(T));
+        return base ? (T *)p : nullptr;
+    }
+};
+
+struct ForwardWs {
+    float *fw, *fa, *part;
+    uint16_t *W16, *A16;
+    size_t bytes;
+    int planes_a, planes_w, passes;
+    int64_t kp, rows;
+    Plan plan;
+};
+ForwardWs forward_layout(const FusedShape &s, char *base) {
+    ForwardWs w{};
+    w.planes_a = w.planes_w = s.out_bf16 ? 1 : 2;
+    w.passes = s.out_bf16 ? 1 : (s.in_bf16 ? 2 : 3);
+    w.kp = pad_stage(s.d_in);
+    w.rows = std::min(s.m, DENSE_ROWS);
+    w.plan = plan_gemm(w.rows, s.d_out, s.layers, (int)(w.kp / GK) * w.passes);
+    Layout l(base);
+    w.fw = l.take<float>(s.layers * s.d_out);
+    w.fa = l.take<float>(w.rows);
+    w.W16 = l.take<uint16_t>(s.layers * s.d_out * w.planes_w * w.kp);
+    w.A16 = l.take<uint16_t>(w.rows * w.planes_a * w.kp);
+    w.part = l.take<float>(w.plan.nsplit > 1 ? w.plan.nsplit * s.layers * w.rows * s.d_out : 0);
+    w.bytes = l.bytes;
+    return w;
+}
+
+struct BackwardWs {
+    float *fw, *fg, *fa, *part, *bias;
+    uint16_t *W16, *D16;
+    size_t bytes;
+    int planes_a, planes_w, passes;
+    int64_t kp, rows;
+    Plan plan;
+};
+BackwardWs backward_layout(const FusedShape &s, char *base) {
+    BackwardWs w{};
+    w.planes_a = w.planes_w = s.out_bf16 ? 1 : 2;
+    w.passes = s.out_bf16 ? 1 : 3;
+    w.kp = pad_stage(s.d_out);
+    w.rows = std::min(s.m, DENSE_ROWS);
+    w.plan = plan_gemm(w.rows, s.d_in, 1, (int)(w.kp / GK) * s.layers * w.passes);
+    Layout l(base);
+    w.fw = l.take<float>(s.d_in);
+    w.fg = l.take<float>(s.ngroups);
+    w.fa = l.take<float>(2 * w.rows);
+    w.W16 = l.take<uint16_t>(s.d_in * w.planes_w * s.layers * w.kp);
+    w.D16 = l.take<uint16_t>(w.rows * w.planes_a * s.layers * w.kp);
+    w.bias = l.take<float>(cdiv(w.rows, BIAS_ROWS) * s.layers * s.d_out);
+    w.part = l.take<float>(w.plan.nsplit > 1 ? w.plan.nsplit * w.rows * s.d_in : 0);
+    w.bytes = l.bytes;
+    return w;
+}
+
+template <int MI, bool GATED>
+hipError_t launch_gemm_k(const Gemm &g, hipStream_t st) {
+    fused_gemm_kernel<MI, GATED><<<(unsigned)(g.mt * g.nt * g.nsplit), 256, 0, st>>>(g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || g.nsplit == 1) return e;
+    split_reduce_kernel<GATED><<<(unsigned)cdiv(g.m * cdiv(g.n, 4), 256), 256, 0, st>>>(g);
+    return hipGetLastError();
+}
+
+hipError_t launch_gemm(const Gemm &g, int mi, hipStream_t st) {
+    if (g.layers == 2) return mi == 4 ? launch_gemm_k<4, true>(g, st) : launch_gemm_k<2, true>(g, st);
+    return mi == 4 ? launch_gemm_k<4, false>(g, st) : launch_gemm_k<2, false>(g, st);
+}
+
+constexpr size_t PREP_LDS_MAX = 128 * 1024;   // bytes of an activation row staged for its gather
+
+template <int BITS>
+hipError_t launch_forward_prep(const ForwardPrep &p, int64_t blocks, hipStream_t st) {
+    const size_t row = (size_t)p.d_in * (p.a_bf16 ? 2 : 4);
+    const size_t lds = std::max<size_t>(p.in_lds ? (row + 15) / 16 * 16 : 0, 1024);
+    if (lds > 64 * 1024) {   // above the default limit a launch needs the kernel's attribute
+        const hipError_t e = hipFuncSetAttribute((const void *)forward_prep_kernel<BITS>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)PREP_LDS_MAX);
+        if (e != hipSuccess) return e;
+    }
+    forward_prep_kernel<BITS><<<(unsigned)blocks, 256, lds, st>>>(p);
+    return hipGetLastError();
+}
+
+const char *at(const void *p, int64_t elements, int bf16) { return (const char *)p + elements * (bf16 ? 2 : 4); }
+
+}  // namespace
+
+size_t dense_forward_ws(const FusedShape &s) { return forward_layout(s, nullptr).bytes; }
+size_t dense_backward_ws(const FusedShape &s) { return backward_layout(s, nullptr).bytes; }
+
+hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st) {
+    const FusedShape &s = a.s;
+    const ForwardWs w = forward_layout(s, a.ws);
+    for (int64_t i0 = 0; i0 < s.m; i0 += DENSE_ROWS) {
+        const int64_t m = std::min(DENSE_ROWS, s.m - i0);
+        ForwardPrep p{};
+        p.A = at(a.A, i0 * s.d_in, s.in_bf16);
+        p.a_bf16 = s.in_bf16;
+        p.vec = s.d_in % 8 == 0 && aligned(a.A, 16);
+        p.perm = a.perm;
+        p.m = m;
+        p.d_in = s.d_in;
+        p.kp = w.kp;
+        p.A16 = w.A16;
+        p.planes_a = w.planes_a;
+        p.fa = w.fa;
+        p.in_lds = (size_t)s.d_in * (s.in_bf16 ? 2 : 4) <= PREP_LDS_MAX;
+        for (int l = 0; l < s.layers; ++l) p.w[l] = a.w[l];
+        p.d_out = s.d_out;
+        p.nwords = cdiv(s.bits * s.d_in, 32);
+        p.g = s.group;
+        p.ngroups = s.ngroups;
+        p.layers = s.layers;
+        p.W16 = w.W16;
+        p.planes_w = w.planes_w;
+        p.fw = w.fw;
+        p.row_blocks = m;
+        p.kchunks = (int)cdiv(w.kp, FW_K);
+        // the weights once, with the first rows
+        const int64_t blocks = m + (i0 == 0 ? s.layers * cdiv(s.d_out, FW_ROWS) * p.kchunks : 0);
+        hipError_t e = hipErrorInvalidValue;
+        switch (s.bits) {
+            case 2: e = launch_forward_prep<2>(p, blocks, st); break;
+            case 3: e = launch_forward_prep<3>(p, blocks, st); break;
+            case 4: e = launch_forward_prep<4>(p, blocks, st); break;
+            case 8: e = launch_forward_prep<8>(p, blocks, st); break;
+        }
+        if (e != hipSuccess) return e;
+        Gemm g{};
+        g.A = w.A16;
+        g.B = w.W16;
+        g.lda = w.planes_a * w.kp;
+        g.ldb = w.planes_w * w.kp;
+        g.kp = g.a_plane = g.b_plane = w.kp;
+        g.passes = w.passes;
+        g.exact = w.passes == 2;
+        g.m = m;
+        g.n = s.d_out;
+        g.layers = s.layers;
+        g.fa = w.fa;
+        g.fw = w.fw;
+        g.bias_bf16 = a.bias_bf16;
+        g.act = a.act;
+        const int64_t o = i0 * s.d_out;
+        g.vec = s.d_out % 4 == 0 && aligned(a.Y, 16) && (!a.residual || aligned(a.residual, 16));
+        for (int l = 0; l < s.layers; ++l) {
+            g.bias[l] = a.bias[l];
+            g.pre[l] = a.pre[l] ? (void *)at(a.pre[l], o, s.out_bf16) : nullptr;
+            g.vec = g.vec && (!a.bias[l] || aligned(a.bias[l], 16)) && (!a.pre[l] || aligned(a.pre[l], 16));
+        }
+        g.residual = a.residual ? at(a.residual, o, s.out_bf16) : nullptr;
+        g.Y = (void *)at(a.Y, o, s.out_bf16);
+        g.out_bf16 = s.out_bf16;
+        g.part = w.part;
+        g.nsplit = w.plan.nsplit;
+        g.mt = (int)cdiv(m, 64 * w.plan.mi);   // (the last rows may be fewer)
+        g.nt = w.plan.nt;
+        e = launch_gemm(g, w.plan.mi, st);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st) {
+    const FusedShape &s = a.s;
+    const BackwardWs w = backward_layout(s, a.ws);
+    const bool bias = a.dbias[0] || a.dbias[1];
+    for (int64_t i0 = 0; i0 < s.m; i0 += DENSE_ROWS) {
+        const int64_t m = std::min(DENSE_ROWS, s.m - i0), o = i0 * s.d_out;
+        BackwardPrep p{};
+        p.dY = at(a.dY, o, s.in_bf16);
+        p.bf16 = s.in_bf16;
+        p.vec = s.d_out % 8 == 0 && aligned(a.dY, 16);
+        const int npre = s.layers == 2 ? 2 : (a.act ? 1 : 0);
+        for (int l = 0; l < npre; ++l) {
+            p.pre[l] = at(a.pre[l], o, s.in_bf16);
+            p.vec = p.vec && aligned(a.pre[l], 16);
+        }
+        p.act = a.act;
+        p.m = m;
+        p.d_out = s.d_out;
+        p.kp = w.kp;
+        p.layers = s.layers;
+        p.D16 = w.D16;
+        p.planes_a = w.planes_a;
+        p.fa = w.fa;
+        p.bias_part = bias ? w.bias : nullptr;
+        p.perm = a.perm;
+        p.d_in = s.d_in;
+        p.nwords = cdiv(s.bits * s.d_in, 32);
+        p.g = s.group;
+        p.ngroups = s.ngroups;
+        p.wvec = s.d_out % 4 == 0;
+        for (int l = 0; l < s.layers; ++l) {
+            p.w[l] = a.w[l];
+            p.wvec = p.wvec && aligned(a.w[l].Q, 16) && aligned(a.w[l].scales, 16) && aligned(a.w[l].zeros, 16);
+        }
+        p.fg = w.fg;
+        p.W16 = w.W16;
+        p.planes_w = w.planes_w;
+        p.fw = w.fw;
+        p.dz_cols = cdiv(w.kp, 256);
+        const int64_t row_blocks = cdiv(m, BIAS_ROWS);
+        p.dz_blocks = p.dz_cols * row_blocks;
+        // the groups' ranges and the weights once, with the first rows
+        backward_range_kernel<<<(unsigned)(m + (i0 == 0 ? s.ngroups : 0)), 256, 0, st>>>(p);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const int64_t blocks =
+            p.dz_blocks + (i0 == 0 ? s.layers * cdiv(w.kp, BW_ROWS) * cdiv(s.d_in, BW_COLS) : 0);
+        switch (s.bits) {
+            case 2: backward_prep_kernel<2><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+            case 3: backward_prep_kernel<3><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+            case 4: backward_prep_kernel<4><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+            case 8: backward_prep_kernel<8><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+        }
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        if (bias) {
+            bias_reduce_kernel<<<dim3((unsigned)cdiv(s.d_out, 256), (unsigned)s.layers), 256, 0, st>>>(
+                w.bias, row_blocks, s.layers, s.d_out, a.dbias[0], a.dbias[1], i0 > 0);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        Gemm g{};
+        g.A = w.D16;
+        g.B = w.W16;
+        g.kp = s.layers * w.kp;
+        g.lda = w.planes_a * g.kp;
+        g.ldb = w.planes_w * g.kp;
+        g.a_plane = g.b_plane = g.kp;
+        g.passes = w.passes;
+        g.m = m;
+        g.n = s.d_in;
+        g.layers = 1;
+        g.fa = w.fa + m;
+        g.fw = w.fw;
+        g.Y = (void *)at(a.dA, i0 * s.d_in, s.out_bf16);
+        g.out_bf16 = s.out_bf16;
+        g.vec = s.d_in % 4 == 0 && aligned(a.dA, 16);
+        g.part = w.part;
+        g.nsplit = w.plan.nsplit;
+        g.mt = (int)cdiv(m, 64 * w.plan.mi);
+        g.nt = w.plan.nt;
+        e = launch_gemm(g, w.plan.mi, st);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace gptq

@@ -359,11 +359,12 @@ def test_ranges_of_scales_and_rows(m, in_dt):
 # values that are not finite, zeros, empty batches
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("m", [4, 20, 140])
-@pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_nonfinite_rows_stay_their_own(m, dt):
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
+def test_nonfinite_rows_stay_their_own(m, dt, out):
     rng = np.random.default_rng(m)
     l = Layer(rng, 150, 256, 4, 64, False, False)
-    for n, call in ((256, lambda x: P.dequant_linear(x, l.q)), (150, lambda x: P.dequant_linear_backward(x, l.q)[0])):
+    for n, call in ((256, lambda x: P.dequant_linear(x, l.q, out_dtype=DT[out])),
+                    (150, lambda x: P.dequant_linear_backward(x, l.q, out_dtype=DT[out])[0])):
         x = values(rng, (m, n), dt)
         x[1, 3], x[2, 5] = float("nan"), float("inf")
         clean = x.clone()
