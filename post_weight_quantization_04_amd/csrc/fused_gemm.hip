@@ -59,6 +59,19 @@ __device__ __forceinline__ float block_max(float v) {
     return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
 }
 
+// Operand layout: tiles of 256 rows, inside a tile stages of GK contraction
+// elements, a stage's 256 rows of 64 bytes side by side with their 16-byte
+// pieces permuted as the product's LDS reads want them.  A stage of a tile is
+// then 16 contiguous kilobytes, moved into LDS as it is.
+constexpr int64_t TILE_STAGE = 256 * GK;   // elements of a stage of a tile
+__host__ __device__ __forceinline__ int64_t pad_tile(int64_t rows) { return (rows + 255) / 256 * 256; }
+__host__ __device__ __forceinline__ int swz(int row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); }
+// element k (a multiple of 8) of row `row`, ktot contraction elements per row
+__device__ __forceinline__ int64_t operand_at(int64_t row, int64_t k, int64_t ktot) {
+    return ((row >> 8) * (ktot / GK) + k / GK) * TILE_STAGE + (row & 255) * GK +
+           8 * ((int)((k >> 3) & 3) ^ swz((int)row));
+}
+
 // Eight values as f16 planes at out and, when there are two, out + plane.
 // One plane: the rounded values.  Two: hi, and lo = x - hi; of activations
 // that are exact in f16 (EXACT), x itself again.  Values that are not finite
@@ -84,19 +97,26 @@ __device__ __forceinline__ void put_planes(uint16_t *out, int64_t plane, int pla
 // ---------------------------------------------------------------------------
 // forward operands: rows of A (gathered into processing order), weights [n][k]
 // ---------------------------------------------------------------------------
+// Work group b's row: two rows that share a 128-byte line of the operand go to
+// groups of one XCD (groups go round the 8 XCDs in turn), so that its L2
+// writes whole lines.
+__device__ __forceinline__ int64_t paired_row(int64_t b, int64_t m) {
+    return b < m / 16 * 16 ? b / 16 * 16 + b % 8 * 2 + b / 8 % 2 : b;
+}
+
 struct ForwardPrep {
     const void *A;
     int a_bf16, vec;            // vec: whole aligned 16-byte pieces
     const int32_t *perm;
     int64_t m, d_in, kp;        // kp: d_in padded to whole stages
-    uint16_t *A16;              // [m][planes_a][kp]
+    uint16_t *A16;              // rows [m], contraction [planes_a][kp]
     int planes_a;
     float *fa;                  // [m] inverse row factors
     int in_lds;                 // the row fits the launch's LDS
     PackedLayer w[2];
     int64_t d_out, nwords;
     int g, ngroups, layers;
-    uint16_t *W16;              // [layers][d_out][planes_w][kp]
+    uint16_t *W16;              // per layer: rows [d_out], contraction [planes_w][kp]
     int planes_w;
     float *fw;                  // [layers][d_out] inverse factors
     int64_t row_blocks;         // work groups of the activation rows, then those of the weights
@@ -135,7 +155,6 @@ __device__ void prep_row(const ForwardPrep &p, int64_t i, char *lds) {
     pow2_scale(block_max(mx), mul, inv);   // (its barriers also cover the staged row)
     if (tid == 0) p.fa[i] = inv;
     const void *src = p.in_lds ? (const void *)lds : (const void *)row;
-    uint16_t *out = p.A16 + i * p.planes_a * p.kp;
     for (int64_t k0 = 8 * tid; k0 < p.kp; k0 += 8 * 256) {
         float v[8];
 #pragma unroll
@@ -143,7 +162,7 @@ __device__ void prep_row(const ForwardPrep &p, int64_t i, char *lds) {
             const int64_t k = k0 + e;
             v[e] = k < p.d_in ? fz_ld(src, p.perm ? (int64_t)p.perm[k] : k, p.a_bf16) * mul : 0.f;
         }
-        put_planes(out + k0, p.kp, p.planes_a, p.a_bf16, v);
+        put_planes(p.A16 + operand_at(i, k0, p.planes_a * p.kp), p.kp * 256, p.planes_a, p.a_bf16, v);
     }
 }
 
@@ -178,7 +197,7 @@ __device__ void prep_weights(const ForwardPrep &p, int64_t b, float *lds) {
     pow2_scale(mx * (float)((1 << BITS) - 1), mul, inv);
     if (kc == 0 && lane < 8 && r0 + rl < p.d_out) p.fw[l * p.d_out + r] = inv;
     if (r0 + rl >= p.d_out) return;
-    uint16_t *out = p.W16 + (l * p.d_out + r) * p.planes_w * p.kp;
+    uint16_t *out = p.W16 + l * pad_tile(p.d_out) * p.planes_w * p.kp;
     const int64_t kend = std::min<int64_t>(p.kp, (int64_t)(kc + 1) * FW_K);
     for (int64_t k0 = (int64_t)kc * FW_K + 8 * (lane >> 3); k0 < kend; k0 += 64) {
         float v[8];
@@ -195,7 +214,7 @@ __device__ void prep_weights(const ForwardPrep &p, int64_t b, float *lds) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = 0.f;
         }
-        put_planes(out + k0, p.kp, p.planes_w, 0, v);
+        put_planes(out + operand_at(r, k0, p.planes_w * p.kp), p.kp * 256, p.planes_w, 0, v);
     }
 }
 
@@ -203,7 +222,7 @@ template <int BITS>
 __global__ __launch_bounds__(256) void forward_prep_kernel(ForwardPrep p) {
     extern __shared__ __attribute__((aligned(16))) char dyn[];
     if ((int64_t)blockIdx.x < p.row_blocks)
-        prep_row(p, blockIdx.x, dyn);
+        prep_row(p, paired_row(blockIdx.x, p.m), dyn);
     else
         prep_weights<BITS>(p, (int64_t)blockIdx.x - p.row_blocks, (float *)dyn);
 }
@@ -218,7 +237,7 @@ struct BackwardPrep {
     int bf16, vec;              // vec: rows of whole aligned 8-element pieces
     int64_t m, d_out, kp;       // kp: d_out padded to whole stages
     int layers;
-    uint16_t *D16;              // [m][planes_a][layers][kp]
+    uint16_t *D16;              // rows [m], contraction [planes_a][layers][kp]
     int planes_a;
     float *fa;                  // [m] row factors (mul), then [m] their inverses
     float *bias_part;           // [row blocks][layers][d_out], or NULL
@@ -227,7 +246,7 @@ struct BackwardPrep {
     int64_t d_in, nwords;
     int g, ngroups, wvec;       // wvec: four rows' words load together
     float *fg;                  // [ngroups] weight factors (mul), then their inverses
-    uint16_t *W16;              // [d_in][planes_w][layers][kp]
+    uint16_t *W16;              // rows [d_in], contraction [planes_w][layers][kp]
     int planes_w;
     float *fw;                  // [d_in] inverse factors, original order
     int64_t dz_blocks, dz_cols; // dZ tiles, then weight tiles
@@ -314,7 +333,8 @@ __device__ void prep_dz(const BackwardPrep &p, int64_t b, float *lds) {
             v[e] = r0 + e < p.d_out ? d[e] * mul : 0.f;
             if (r0 + e < p.d_out) sum[l][e] += d[e];
         }
-        put_planes(p.D16 + (i * p.planes_a * p.layers + l) * p.kp + r0, p.layers * p.kp, p.planes_a, 0, v);
+        put_planes(p.D16 + operand_at(i, l * p.kp + r0, p.planes_a * p.layers * p.kp), p.layers * p.kp * 256, p.planes_a,
+                   0, v);
     };
     for (int64_t i = rb * BIAS_ROWS + (tid >> 5); i < ilast; i += 8) {
         const int64_t o = i * p.d_out + r0;
@@ -359,10 +379,11 @@ __device__ void prep_dz(const BackwardPrep &p, int64_t b, float *lds) {
     }
 }
 
-// 512 outputs by 32 processing columns: a thread turns blocks of 8 outputs by
-// 8 columns around in registers, so that words are read and rows of W16
-// written as whole lines
-constexpr int BW_ROWS = 512, BW_COLS = 32;
+// 128 outputs by 128 processing columns: a thread turns a block of 8 outputs
+// by 8 columns around in registers.  A wave's lanes take 32 outputs (a
+// stage's 64 bytes of a W16 row) of 16 column blocks: words are read as whole
+// 128-byte lines, and eight consecutive columns are 512 contiguous bytes.
+constexpr int BW_ROWS = 128, BW_COLS = 128;
 template <int BITS>
 __device__ void prep_weights_t(const BackwardPrep &p, int64_t b) {
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
@@ -370,8 +391,8 @@ __device__ void prep_weights_t(const BackwardPrep &p, int64_t b) {
     const int64_t ctiles = cdiv(p.d_in, BW_COLS);
     const int l = (int)(b / (rtiles * ctiles));
     const int64_t t = b % (rtiles * ctiles);
-    const int64_t r0 = (t % rtiles) * BW_ROWS + 8 * lane;
-    const int64_t k0 = (t / rtiles) * BW_COLS + 8 * wave;
+    const int64_t r0 = (t % rtiles) * BW_ROWS + 32 * wave + 8 * (lane & 3);
+    const int64_t k0 = (t / rtiles) * BW_COLS + 8 * (lane >> 2);
     if (r0 >= p.kp || k0 >= p.d_in) return;
     const PackedLayer w = p.w[l];
     const int64_t gi = k0 / p.g;
@@ -419,7 +440,8 @@ __device__ void prep_weights_t(const BackwardPrep &p, int64_t b) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = (fz_code<BITS>(c[e], k) - z[e]) * s[e];
-        put_planes(p.W16 + (col * p.planes_w * p.layers + l) * p.kp + r0, p.layers * p.kp, p.planes_w, 0, v);
+        put_planes(p.W16 + operand_at(col, l * p.kp + r0, p.planes_w * p.layers * p.kp), p.layers * p.kp * 256,
+                   p.planes_w, 0, v);
         if (l == 0 && r0 == 0) p.fw[col] = inv;
     }
 }
@@ -450,8 +472,8 @@ __global__ __launch_bounds__(256) void bias_reduce_kernel(const float *part, int
 // the product
 // ---------------------------------------------------------------------------
 struct Gemm {
-    const uint16_t *A, *B;      // f16 [m][lda], [layers * n][ldb]
-    int64_t lda, ldb;
+    const uint16_t *A, *B;      // f16 operands of m rows, and of n rows for each layer
+    int64_t lda, ldb;           // contraction elements of a row, all planes
     int64_t kp;                 // elements of one pass over the contraction (whole stages)
     int passes;                 // pass 1 reads B's second plane, pass 2 (with exact: pass 0) A's
     int exact;
@@ -534,9 +556,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t gm_rsrc(const void *p, int64_t
 // C tile of 256 columns n by 64 MI rows, four waves of 128 by 32 MI as 32 x 32
 // MFMA tiles.  The weights are the MFMA's first operand, so that a lane holds
 // four consecutive columns of one activation row.  Both operands move by
-// 16-byte buffer loads straight into a ring of four LDS stages of 32 k;
-// rows of 64 bytes whose 16-byte pieces are permuted so that the operand
-// reads of a wave fall on distinct banks.  Each half stage's MFMAs run
+// 16-byte buffer loads straight into a ring of four LDS stages of 32 k (each
+// load a contiguous kilobyte: read from rows a stage apart in K-major
+// matrices, 64 bytes each, the same loop reached 55% of the matrix cores);
+// the permuted 16-byte pieces put the operand reads of a wave on distinct
+// banks.  Each half stage's MFMAs run
 // between the reads of the next half's operands and half of a refill; the
 // wait for a stage counts loads, so two later stages stay in flight across
 // the one barrier per stage.
@@ -575,42 +599,30 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
     const int st0 = (int)((int64_t)all * split / p.nsplit);
     const int nst = (int)((int64_t)all * (split + 1) / p.nsplit) - st0;   // >= 1
 
-    // rows past the end re-read the last one (only results that are never
-    // stored see them)
-    const int arows = (int)(std::min<int64_t>(p.m, m0 + BM) - m0);
-    const int brows = (int)(std::min<int64_t>(p.n, n0 + COLS) - n0);
-    const __amdgpu_buffer_rsrc_t arsrc = gm_rsrc(p.A + m0 * p.lda, (int64_t)arows * p.lda * 2);
-    const int64_t bfirst = (GATED && wave >= 2 ? p.n : 0) + n0;   // waves 2, 3 move the up layer's rows
-    const __amdgpu_buffer_rsrc_t brsrc = gm_rsrc(p.B + bfirst * p.ldb, (int64_t)brows * p.ldb * 2);
-    auto swz = [](int row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); };
-    int boff[4], aoff[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int row = 16 * (NDMA * wave + q) + (lane >> 2);
-        const int src = std::min(GATED ? row & 127 : row, brows - 1);
-        boff[q] = src * (int)p.ldb * 2 + 16 * ((lane & 3) ^ swz(row));
-    }
-#pragma unroll
-    for (int q = 0; q < MDMA; ++q) {
-        const int row = 16 * (MDMA * wave + q) + (lane >> 2);
-        aoff[q] = std::min(row, arows - 1) * (int)p.lda * 2 + 16 * ((lane & 3) ^ swz(row));
-    }
+    // (rows past the end are room of the operands' last tiles: whatever they
+    // hold only reaches results that are never stored)
+    const uint16_t *abase = p.A + (m0 >> 8) * (p.lda / GK) * TILE_STAGE + (m0 & 255) * GK;
+    // the gated pair: waves 2 and 3 move the up layer's rows
+    const int64_t bskip = GATED ? (wave >> 1) * pad_tile(p.n) * p.ldb - (wave >> 1) * 128 * GK : 0;
+    const uint16_t *bbase = p.B + (n0 >> 8) * (p.ldb / GK) * TILE_STAGE + (n0 & 255) * GK + bskip;
+    const __amdgpu_buffer_rsrc_t arsrc = gm_rsrc(abase, p.lda / GK * TILE_STAGE * 2);
+    const __amdgpu_buffer_rsrc_t brsrc = gm_rsrc(bbase, p.ldb / GK * TILE_STAGE * 2);
     // first (part 0) or second half of this wave's loads of stage st; stages
     // past the end re-read the last one, unused
     auto issue = [&](int st, int part) {
         char *buf = lds + (st % NBUF) * STAGE;
         const int s = st0 + std::min(st, nst - 1);
-        const int pass = (s >= spp) + (s >= 2 * spp), kk = (s - pass * spp) * GK * 2;
-        const int bk = __builtin_amdgcn_readfirstlane(kk + (pass == 1 ? (int)p.b_plane * 2 : 0));
-        const int ak = __builtin_amdgcn_readfirstlane(kk + (pass == (p.exact ? 0 : 2) ? (int)p.a_plane * 2 : 0));
+        const int pass = (s >= spp) + (s >= 2 * spp), kk = (s - pass * spp) * (int)TILE_STAGE * 2;
+        const int bk = __builtin_amdgcn_readfirstlane(kk + (pass == 1 ? (int)(p.b_plane / GK * TILE_STAGE) * 2 : 0));
+        const int ak = __builtin_amdgcn_readfirstlane(kk + (pass == (p.exact ? 0 : 2) ? (int)(p.a_plane / GK * TILE_STAGE) * 2 : 0));
 #pragma unroll
         for (int q = NDMA / 2 * part; q < NDMA / 2 * (part + 1); ++q)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(brsrc, (gm_lds_void *)(buf + (NDMA * wave + q) * 1024), 16,
-                                                     boff[q], bk, 0, 0);
+                                                     (NDMA * wave + q) * 1024 + lane * 16, bk, 0, 0);
 #pragma unroll
         for (int q = MDMA / 2 * part; q < MDMA / 2 * (part + 1); ++q)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(arsrc, (gm_lds_void *)(buf + NSIDE + (MDMA * wave + q) * 1024),
-                                                     16, aoff[q], ak, 0, 0);
+                                                     16, (MDMA * wave + q) * 1024 + lane * 16, ak, 0, 0);
     };
 
     // operand reads: lane l supplies row l % 32 of a 32-row tile, k 8 (l / 32) .. +7
@@ -800,8 +812,8 @@ ForwardWs forward_layout(const FusedShape &s, char *base) {
     Layout l(base);
     w.fw = l.take<float>(s.layers * s.d_out);
     w.fa = l.take<float>(w.rows);
-    w.W16 = l.take<uint16_t>(s.layers * s.d_out * w.planes_w * w.kp);
-    w.A16 = l.take<uint16_t>(w.rows * w.planes_a * w.kp);
+    w.W16 = l.take<uint16_t>(s.layers * pad_tile(s.d_out) * w.planes_w * w.kp);
+    w.A16 = l.take<uint16_t>(pad_tile(w.rows) * w.planes_a * w.kp);
     w.part = l.take<float>(w.plan.nsplit > 1 ? w.plan.nsplit * s.layers * w.rows * s.d_out : 0);
     w.bytes = l.bytes;
     return w;
@@ -826,8 +838,8 @@ BackwardWs backward_layout(const FusedShape &s, char *base) {
     w.fw = l.take<float>(s.d_in);
     w.fg = l.take<float>(s.ngroups);
     w.fa = l.take<float>(2 * w.rows);
-    w.W16 = l.take<uint16_t>(s.d_in * w.planes_w * s.layers * w.kp);
-    w.D16 = l.take<uint16_t>(w.rows * w.planes_a * s.layers * w.kp);
+    w.W16 = l.take<uint16_t>(pad_tile(s.d_in) * w.planes_w * s.layers * w.kp);
+    w.D16 = l.take<uint16_t>(pad_tile(w.rows) * w.planes_a * s.layers * w.kp);
     w.bias = l.take<float>(cdiv(w.rows, BIAS_ROWS) * s.layers * s.d_out);
     w.part = l.take<float>(w.plan.nsplit > 1 ? w.plan.nsplit * w.rows * s.d_in : 0);
     w.bytes = l.bytes;
