@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libgptq.so")
 
 SOURCES = ["api.cpp", "hessian.hip", "prep.hip", "factor.hip", "quant.hip", "trail.hip", "pack.hip", "dequant.hip",
-           "fused.hip", "fused_gemm.hip"]
+           "fused.hip", "fused_gemm.hip", "fused_skinny.hip"]
 ARCH = "gfx950"
 
 

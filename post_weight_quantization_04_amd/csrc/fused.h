@@ -1,5 +1,5 @@
 // Device helpers and internal entry points of the fused products with packed
-// layers (fused.hip, fused_gemm.hip).
+// layers (fused.hip, fused_gemm.hip, fused_skinny.hip).
 #pragma once
 
 #include "common.h"
@@ -107,5 +107,15 @@ size_t dense_forward_ws(const FusedShape &s);
 size_t dense_backward_ws(const FusedShape &s);
 hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st);
 hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// packed form (fused_skinny.hip)
+// ---------------------------------------------------------------------------
+bool skinny_forward_takes(const FusedShape &s);
+size_t skinny_forward_ws(const FusedShape &s);
+hipError_t skinny_forward_launch(const FusedForward &a, hipStream_t st);
+bool skinny_backward_takes(const FusedShape &s);
+size_t skinny_backward_ws(const FusedShape &s);
+hipError_t skinny_backward_launch(const FusedBackward &a, hipStream_t st);
 
 }  // namespace gptq

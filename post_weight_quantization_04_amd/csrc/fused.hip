@@ -20,10 +20,18 @@ __global__ __launch_bounds__(256) void zero_kernel(float *a, float *b, int64_t n
 
 }  // namespace
 
-size_t fused_forward_ws(const FusedShape &s) { return s.m ? dense_forward_ws(s) : 0; }
-size_t fused_backward_ws(const FusedShape &s) { return s.m ? dense_backward_ws(s) : 0; }
+size_t fused_forward_ws(const FusedShape &s) {
+    if (s.m == 0) return 0;
+    return skinny_forward_takes(s) ? skinny_forward_ws(s) : dense_forward_ws(s);
+}
+size_t fused_backward_ws(const FusedShape &s) {
+    if (s.m == 0) return 0;
+    return skinny_backward_takes(s) ? skinny_backward_ws(s) : dense_backward_ws(s);
+}
 
-hipError_t fused_forward_launch(const FusedForward &a, hipStream_t st) { return dense_forward_launch(a, st); }
+hipError_t fused_forward_launch(const FusedForward &a, hipStream_t st) {
+    return skinny_forward_takes(a.s) ? skinny_forward_launch(a, st) : dense_forward_launch(a, st);
+}
 
 hipError_t fused_backward_launch(const FusedBackward &a, hipStream_t st) {
     if (a.s.m == 0) {
@@ -31,7 +39,7 @@ hipError_t fused_backward_launch(const FusedBackward &a, hipStream_t st) {
         zero_kernel<<<(unsigned)cdiv(a.s.d_out, 256), 256, 0, st>>>(a.dbias[0], a.dbias[1], a.s.d_out);
         return hipGetLastError();
     }
-    return dense_backward_launch(a, st);
+    return skinny_backward_takes(a.s) ? skinny_backward_launch(a, st) : dense_backward_launch(a, st);
 }
 
 }  // namespace gptq
