@@ -86,18 +86,37 @@ __host__ __device__ __forceinline__ void fz_with_act(int act, F f) {
     }
 }
 
-// The eight codes k0 .. k0 + 7 (k0 % 8 == 0) of a row lie in the 64 bits (hi,
-// lo) of the words (bits k0) / 32 and the next one, shifted down by the first
-// code's place in its word: code e is bits [bits e, bits e + bits).
+// The eight codes k0 .. k0 + 7 (k0 % 8 == 0) of a row lie in the word (bits
+// k0) / 32 and, for 3 and 8 bits, the next one, from bit (bits k0) % 32 of the
+// first on.  fz_codes8 moves them to bit 0 of one word (two for 8 bits).
 template <int BITS>
-__device__ __forceinline__ uint64_t fz_codes8(unsigned lo, unsigned hi, int sh) {
-    return (((uint64_t)hi << 32) | (uint64_t)lo) >> sh;
-}
+constexpr bool fz_two_words() { return BITS == 3 || BITS == 8; }
 template <int BITS>
-constexpr bool fz_two_words() { return BITS == 3 || BITS == 8; }   // eight codes may span two words
+struct Codes8 {
+    unsigned w[BITS == 8 ? 2 : 1];
+    // code e as fp32
+    __device__ __forceinline__ float at(int e) const {
+        if constexpr (BITS == 8) return (float)((w[e >> 2] >> (8 * (e & 3))) & 255u);
+        // two shared shifts and masks, then byte conversions
+        if constexpr (BITS == 4) {
+            const unsigned half = (e & 1) ? (w[0] >> 4) & 0x0f0f0f0fu : w[0] & 0x0f0f0f0fu;
+            return (float)((half >> (8 * (e >> 1))) & 255u);
+        }
+        return (float)__builtin_amdgcn_ubfe(w[0], BITS * e, BITS);
+    }
+};
 template <int BITS>
-__device__ __forceinline__ float fz_code(uint64_t v, int e) {
-    return (float)((unsigned)(v >> (BITS * e)) & ((1u << BITS) - 1u));
+__device__ __forceinline__ Codes8<BITS> fz_codes8(unsigned lo, unsigned hi, int sh) {
+    Codes8<BITS> c;
+    if constexpr (BITS == 8) {
+        c.w[0] = lo;
+        c.w[BITS == 8 ? 1 : 0] = hi;
+    } else if constexpr (BITS == 3) {
+        c.w[0] = __builtin_amdgcn_alignbit(hi, lo, sh);
+    } else {
+        c.w[0] = BITS == 4 ? lo : lo >> sh;
+    }
+    return c;
 }
 
 // ---------------------------------------------------------------------------

@@ -205,11 +205,11 @@ __device__ void prep_weights(const ForwardPrep &p, int64_t b, float *lds) {
             const int64_t pos = BITS * k0, j = pos >> 5;
             const unsigned lo = w.Q[j * p.d_out + r];
             const unsigned hi = fz_two_words<BITS>() ? w.Q[std::min<int64_t>(j + 1, p.nwords - 1) * p.d_out + r] : 0u;
-            const uint64_t c = fz_codes8<BITS>(lo, hi, (int)(pos & 31));
+            const Codes8<BITS> c = fz_codes8<BITS>(lo, hi, (int)(pos & 31));
             const int64_t gi = k0 / p.g;
             const float s = w.scales[gi * p.d_out + r] * mul, z = w.zeros[gi * p.d_out + r];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = k0 + e < p.d_in ? (fz_code<BITS>(c, e) - z) * s : 0.f;
+            for (int e = 0; e < 8; ++e) v[e] = k0 + e < p.d_in ? (c.at(e) - z) * s : 0.f;
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = 0.f;
@@ -430,7 +430,7 @@ __device__ void prep_weights_t(const BackwardPrep &p, int64_t b) {
             hi[e] = in && fz_two_words<BITS>() ? w.Q[j1 * p.d_out + r] : 0u;
         }
     }
-    uint64_t c[8];
+    Codes8<BITS> c[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) c[e] = fz_codes8<BITS>(lo[e], hi[e], sh);
 #pragma unroll
@@ -439,7 +439,7 @@ __device__ void prep_weights_t(const BackwardPrep &p, int64_t b) {
         const int64_t col = p.perm ? (int64_t)p.perm[k0 + k] : k0 + k;
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (fz_code<BITS>(c[e], k) - z[e]) * s[e];
+        for (int e = 0; e < 8; ++e) v[e] = (c[e].at(k) - z[e]) * s[e];
         put_planes(p.W16 + operand_at(col, l * p.kp + r0, p.planes_w * p.layers * p.kp), p.layers * p.kp * 256,
                    p.planes_w, 0, v);
         if (l == 0 && r0 == 0) p.fw[col] = inv;

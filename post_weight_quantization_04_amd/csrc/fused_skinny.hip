@@ -25,131 +25,119 @@ __device__ __forceinline__ int xcd_run(int b, int total) {
 // layers of a gated pair, so that the product act(G) U is local) and the whole
 // contraction, each wave a contiguous run of 32-code units; the waves' sums
 // meet in LDS in wave order, and no group waits for another.  The bound is the
-// latency and rate of the packed words' read: every lane loads the words of V
-// adjacent outputs for its eight codes of a unit (a quarter wave's 16 V
-// outputs are 64 V contiguous bytes), PF units ahead.
+// read of the packed words and the conversion of their codes: every lane loads
+// the words of V adjacent outputs for its eight codes of a unit (a quarter
+// wave's 16 V outputs are 64 V contiguous bytes), PF units ahead.  The loop
+// has no branch around a load: rows past m and outputs past the end re-read
+// the last ones, units past a wave's run its last unit.
 // ---------------------------------------------------------------------------
 constexpr int SK_NW = 8;
 
 struct SkinnyForward {
     FusedForward f;
-    const void *A;          // the rows as the units read them
-    const int32_t *perm;    // gathered while loading (NULL: already in order)
-    int avec;               // whole aligned 8-element pieces, no gather
-    int wvec;               // V outputs' words, scales, zero points load together
+    const void *A;          // the rows in processing order, 16-byte aligned
+    int64_t lda;            // elements of a row: whole units, zeros past d_in
     int nunits, gs;         // units of 32 codes; 16-code halves per group
-    int64_t nwords;
+    int tail;               // words of the last unit
     int tiles;
 };
 
 template <int V>
-__device__ __forceinline__ void load_rows(const unsigned *base, int64_t off, int64_t row, int64_t d_out, int vec,
-                                          unsigned (&out)[V]) {
+__device__ __forceinline__ void load_rows(const char *base, unsigned off, unsigned (&out)[V]) {
     if constexpr (V == 2) {
-        if (vec) {   // d_out even: both rows exist, or the last pair stands in
-            const u32x2 v = *(const u32x2 *)(base + off + std::min(row, d_out - 2));
-            out[0] = v[0];
-            out[1] = v[1];
-            return;
-        }
+        const u32x2 v = *(const u32x2 *)(base + off);
+        out[0] = v[0];
+        out[1] = v[1];
+    } else {
+        out[0] = *(const unsigned *)(base + off);
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) out[j] = base[off + std::min<int64_t>(row + j, d_out - 1)];
-}
-template <int V>
-__device__ __forceinline__ void load_rows(const float *base, int64_t off, int64_t row, int64_t d_out, int vec,
-                                          float (&out)[V]) {
-    unsigned u[V];
-    load_rows<V>((const unsigned *)base, off, row, d_out, vec, u);
-#pragma unroll
-    for (int j = 0; j < V; ++j) out[j] = __builtin_bit_cast(float, u[j]);
 }
 
 // eight codes as bf16 integers q - z
 template <int BITS>
-__device__ __forceinline__ bf16x8 int_weights(uint64_t c, float z) {
+__device__ __forceinline__ bf16x8 int_weights(const Codes8<BITS> &c, float z) {
     bf16x8 w;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = (__bf16)(fz_code<BITS>(c, e) - z);
+    for (int e = 0; e < 8; ++e) w[e] = (__bf16)(c.at(e) - z);
     return w;
 }
 
-template <int BITS, int V, int MT, int NL, bool A32>
+// HALF: groups may end between the halves of a unit (g not a multiple of 32)
+template <int BITS, int V, int MT, int NL, bool A32, bool HALF>
 __global__ __launch_bounds__(64 * SK_NW) void skinny_forward_kernel(SkinnyForward p) {
     constexpr int ROWS = 16 * V, NWD = fz_two_words<BITS>() ? 2 : 1;
-    constexpr int PF = MT > 1 ? 2 : (V * NL == 1 ? 6 : 4);      // units in flight
-    constexpr int AP = A32 ? 3 : 1;                             // bf16 terms of an activation
+    constexpr int PF = MT > 1 ? 2 : (V * NL == 1 ? 8 : 4);      // units in flight
+    constexpr int AP = A32 ? 3 : 1, AL = A32 ? 2 : 1, ES = A32 ? 4 : 2;   // bf16 terms, loads and bytes of activations
     __shared__ float red[SK_NW * NL * 16 * ROWS];
     const FusedShape &s = p.f.s;
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t r0 = (int64_t)xcd_run(blockIdx.x, p.tiles) * ROWS, row = r0 + V * li;
+    const int64_t r0 = (int64_t)xcd_run(blockIdx.x, p.tiles) * ROWS;
     const int u0 = __builtin_amdgcn_readfirstlane((int)((int64_t)p.nunits * wave / SK_NW));
     const int u1 = __builtin_amdgcn_readfirstlane((int)((int64_t)p.nunits * (wave + 1) / SK_NW));
 
     struct Slot {
-        unsigned w[NL][NWD][V];
-        float z[NL][V], s0[NL][V], s1[NL][V];   // the halves' scales (equal unless a group ends between them)
-        u32x4 a[MT][A32 ? 2 : 1];
+        unsigned w[NL][NWD][V], z[NL][V], s0[NL][V], s1[NL][HALF ? V : 1];   // (s1: the second half's scale)
+        u32x4 a[MT][AL];
     };
     // group of a unit's first half, and that half's place in the group
     struct Place {
         int g, at;
         __device__ __forceinline__ void next(int gs) {
             at += 2;
-            while (at >= gs) {
-                at -= gs;
-                ++g;
+            g += at >= gs;
+            at -= at >= gs ? gs : 0;
+            if (HALF) {   // (two groups a unit for g of 16)
+                g += at >= gs;
+                at -= at >= gs ? gs : 0;
             }
         }
     };
-    Place fetch_at, use_at;
-    fetch_at.g = use_at.g = __builtin_amdgcn_readfirstlane(2 * u0 / p.gs);
-    fetch_at.at = use_at.at = __builtin_amdgcn_readfirstlane(2 * u0 - use_at.g * p.gs);
+    Place ahead, here;
+    ahead.g = here.g = __builtin_amdgcn_readfirstlane(2 * u0 / p.gs);
+    ahead.at = here.at = __builtin_amdgcn_readfirstlane(2 * u0 - here.g * p.gs);
 
-    auto fetch = [&](int u, Slot &sl) {
-        const int g0 = std::min(fetch_at.g, s.ngroups - 1);
-        const int g1 = std::min(fetch_at.g + (fetch_at.at + 1 >= p.gs), s.ngroups - 1);
-        fetch_at.next(p.gs);
-        const int64_t k = (int64_t)u * 32 + 8 * kg, j = (BITS * k) >> 5;
-        const int64_t gz = kg < 2 ? g0 : g1;
+    // Units are fetched in order: scalar pointers move along, the lanes'
+    // offsets stay.
+    const unsigned stride = (unsigned)s.d_out * 4;   // bytes of a word row, of a group's scales
+    const unsigned ro = (unsigned)std::min<int64_t>(r0 + V * li, s.d_out - V) * 4;
+    const int wd = (BITS * 8 * kg) >> 5;             // the lane's first word of a unit
+    unsigned qo[NWD], qlast[NWD], ao[MT];
+#pragma unroll
+    for (int d = 0; d < NWD; ++d) {
+        qo[d] = (unsigned)std::min(wd + d, BITS - 1) * stride + ro;
+        qlast[d] = (unsigned)std::min(wd + d, p.tail - 1) * stride + ro;
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+        ao[t] = (unsigned)((std::min(16 * t + li, (int)s.m - 1) * (int)p.lda + 8 * kg) * ES);
+    int at = std::min(u0, p.nunits - 1);             // the next unit to fetch
+    const char *qp[NL], *ap = (const char *)p.A + (int64_t)at * 32 * ES;
+#pragma unroll
+    for (int l = 0; l < NL; ++l) qp[l] = (const char *)p.f.w[l].Q + (int64_t)at * BITS * stride;
+    auto fetch = [&](Slot &sl) {
+        const bool last = at == p.nunits - 1;
+        const int64_t go = (int64_t)std::min(ahead.g, s.ngroups - 1) * stride;
+        const bool between = HALF && ahead.at + 1 >= p.gs && ahead.g + 1 < s.ngroups;
+        const unsigned second = between ? stride : 0u;
 #pragma unroll
         for (int l = 0; l < NL; ++l) {
-            const PackedLayer &w = p.f.w[l];
 #pragma unroll
-            for (int d = 0; d < NWD; ++d)
-                load_rows<V>(w.Q, std::min(j + d, p.nwords - 1) * s.d_out, row, s.d_out, p.wvec, sl.w[l][d]);
-            load_rows<V>(w.zeros, gz * s.d_out, row, s.d_out, p.wvec, sl.z[l]);
-            load_rows<V>(w.scales, (int64_t)g0 * s.d_out, row, s.d_out, p.wvec, sl.s0[l]);
-            if (g1 != g0) load_rows<V>(w.scales, (int64_t)g1 * s.d_out, row, s.d_out, p.wvec, sl.s1[l]);
+            for (int d = 0; d < NWD; ++d) load_rows<V>(qp[l], last ? qlast[d] : qo[d], sl.w[l][d]);
+            load_rows<V>((const char *)p.f.w[l].zeros + go, ro + (HALF && kg >= 2 ? second : 0u), sl.z[l]);
+            load_rows<V>((const char *)p.f.w[l].scales + go, ro, sl.s0[l]);
+            if constexpr (HALF) load_rows<V>((const char *)p.f.w[l].scales + go, ro + second, sl.s1[l]);
         }
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int64_t i = 16 * t + li;
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int h = 0; h < (A32 ? 2 : 1); ++h) sl.a[t][h] = u32x4{0u, 0u, 0u, 0u};
-            if (i >= s.m || k >= s.d_in) continue;
-            if (p.avec) {
-                const u32x4 *src = (const u32x4 *)((const char *)p.A + (i * s.d_in + k) * (A32 ? 4 : 2));
+            for (int h = 0; h < AL; ++h) sl.a[t][h] = *(const u32x4 *)(ap + ao[t] + 16 * h);
+        const bool more = at + 1 < u1;
+        ap += more ? 32 * ES : 0;
 #pragma unroll
-                for (int h = 0; h < (A32 ? 2 : 1); ++h) sl.a[t][h] = src[h];
-            } else {
-                unsigned v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int64_t c = k + e < s.d_in ? (p.perm ? (int64_t)p.perm[k + e] : k + e) : -1;
-                    v[e] = c < 0 ? 0u
-                                 : (A32 ? ((const unsigned *)p.A)[i * s.d_in + c]
-                                        : (unsigned)((const uint16_t *)p.A)[i * s.d_in + c]);
-                }
-                if constexpr (A32) {
-                    sl.a[t][0] = u32x4{v[0], v[1], v[2], v[3]};
-                    sl.a[t][1] = u32x4{v[4], v[5], v[6], v[7]};
-                } else {
-                    sl.a[t][0] = u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
-                }
-            }
-        }
+        for (int l = 0; l < NL; ++l) qp[l] += more ? BITS * stride : 0u;
+        at += more;
+        if (more) ahead.next(p.gs);
     };
 
     f32x4 acc[NL][V][MT], dg[NL][V][MT];
@@ -179,16 +167,17 @@ __global__ __launch_bounds__(64 * SK_NW) void skinny_forward_kernel(SkinnyForwar
         for (int l = 0; l < NL; ++l)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                w[l][j] = int_weights<BITS>(fz_codes8<BITS>(sl.w[l][0][j], NWD == 2 ? sl.w[l][NWD - 1][j] : 0u, sh),
-                                            sl.z[l][j]);
-                scale[l][j] = sl.s0[l][j];
+                const unsigned zb = sl.z[l][j], sb = sl.s0[l][j];
+                w[l][j] = int_weights<BITS>(fz_codes8<BITS>(sl.w[l][0][j], sl.w[l][NWD - 1][j], sh),
+                                            __builtin_bit_cast(float, zb));
+                scale[l][j] = __builtin_bit_cast(float, sb);
             }
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             if constexpr (A32) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const unsigned bits = sl.a[t][e >> 2][e & 3];
+                    const unsigned bits = sl.a[t][e >> 2 & (AL - 1)][e & 3];
                     const float x = __builtin_bit_cast(float, bits);
                     const bool finite = fabsf(x) < __builtin_inff();   // (others only in the first term)
                     const __bf16 b0 = (__bf16)x;
@@ -215,34 +204,34 @@ __global__ __launch_bounds__(64 * SK_NW) void skinny_forward_kernel(SkinnyForwar
                             dg[l][j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[l][j], dg[l][j][t], 0, 0, 0);
                 }
         };
-        if (use_at.at + 1 < p.gs) {        // both halves in one group
+        if (!HALF || here.at + 1 < p.gs) {   // both halves in one group
             multiply(true);
-            if (use_at.at + 2 == p.gs) fold();
-        } else {                           // a group ends between them
+            if (here.at + 2 == p.gs) fold();
+        } else {                             // a group ends between them
             multiply(kg < 2);
             fold();
 #pragma unroll
             for (int l = 0; l < NL; ++l)
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    scale[l][j] = use_at.g + 1 < s.ngroups ? sl.s1[l][j] : sl.s0[l][j];
+                for (int j = 0; j < V; ++j) {
+                    const unsigned sb = sl.s1[l][HALF ? j : 0];
+                    scale[l][j] = __builtin_bit_cast(float, sb);
+                }
             multiply(kg >= 2);
             if (p.gs == 1) fold();
         }
-        use_at.next(p.gs);
+        here.next(p.gs);
     };
 
     Slot sl[PF];
 #pragma unroll
-    for (int q = 0; q < PF; ++q)
-        if (u0 + q < u1) fetch(u0 + q, sl[q]);
+    for (int q = 0; q < PF; ++q) fetch(sl[q]);
     for (int u = u0; u < u1; u += PF) {
 #pragma unroll
-        for (int q = 0; q < PF; ++q)
-            if (u + q < u1) {
-                use(sl[q]);
-                if (u + q + PF < u1) fetch(u + q + PF, sl[q]);
-            }
+        for (int q = 0; q < PF; ++q) {
+            if (u + q < u1) use(sl[q]);
+            fetch(sl[q]);
+        }
     }
     if (u1 > u0) fold();
 
@@ -286,11 +275,12 @@ __global__ __launch_bounds__(64 * SK_NW) void skinny_forward_kernel(SkinnyForwar
     }
 }
 
-// rows of A in processing order, for more rows than the units gather themselves
+// rows of A in processing order, padded to whole units with zeros
 template <class T>
-__global__ __launch_bounds__(256) void gather_rows_kernel(const T *A, const int32_t *perm, T *out, int64_t d_in) {
+__global__ __launch_bounds__(256) void gather_rows_kernel(const T *A, const int32_t *perm, T *out, int64_t d_in,
+                                                          int64_t lda) {
     const int64_t i = blockIdx.y, k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k < d_in) out[i * d_in + k] = A[i * d_in + perm[k]];
+    if (k < lda) out[i * lda + k] = k < d_in ? A[i * d_in + (perm ? (int64_t)perm[k] : k)] : (T)0;
 }
 
 // ---------------------------------------------------------------------------
@@ -452,7 +442,7 @@ __global__ __launch_bounds__(256) void skinny_backward_kernel(SkinnyBackward p) 
         const f16x8 a0 = *(const f16x8 *)&dz[0][li][32 * step + 8 * kg];
         f16x8 a1 = a0;
         if (HI) a1 = *(const f16x8 *)&dz[AP - 1][li][32 * step + 8 * kg];
-        uint64_t c[8];
+        Codes8<BITS> c[8];
         float sc[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -464,7 +454,7 @@ __global__ __launch_bounds__(256) void skinny_backward_kernel(SkinnyBackward p) 
             f16x8 h, r;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float x = (fz_code<BITS>(c[e], j) - sl.z[e]) * sc[e];
+                float x = (c[e].at(j) - sl.z[e]) * sc[e];
                 if (HI) asm("" : "+v"(x));
                 h[e] = (_Float16)x;
                 if (HI) r[e] = (_Float16)(x - (float)h[e]);
@@ -537,25 +527,31 @@ void backward_ranges(const FusedShape &s, int &splits, int &range) {
 
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-constexpr int64_t GATHER_IN_PLACE = 4;   // rows
-
-template <int BITS, int V, int NL>
-hipError_t launch_forward_k(const SkinnyForward &p, hipStream_t st) {
+template <int BITS, int V, int NL, bool HALF>
+void launch_forward_k(const SkinnyForward &p, hipStream_t st) {
     const dim3 grid((unsigned)p.tiles), block(64 * SK_NW);
-    if (!p.f.s.in_bf16)
-        skinny_forward_kernel<BITS, V, 1, NL, true><<<grid, block, 0, st>>>(p);
-    else if (p.f.s.m <= 16)
-        skinny_forward_kernel<BITS, V, 1, NL, false><<<grid, block, 0, st>>>(p);
-    else if constexpr (V * NL <= 2)
-        skinny_forward_kernel<BITS, V, 4, NL, false><<<grid, block, 0, st>>>(p);
-    return hipGetLastError();
+    if (p.f.s.m > 16) {
+        if constexpr (V * NL <= 2) skinny_forward_kernel<BITS, V, 4, NL, false, HALF><<<grid, block, 0, st>>>(p);
+    } else if (p.f.s.in_bf16) {
+        skinny_forward_kernel<BITS, V, 1, NL, false, HALF><<<grid, block, 0, st>>>(p);
+    } else {
+        if constexpr (V == 1) skinny_forward_kernel<BITS, V, 1, NL, true, HALF><<<grid, block, 0, st>>>(p);
+    }
 }
 
+template <int BITS, int NL>
+hipError_t launch_forward(const SkinnyForward &p, int v, hipStream_t st) {
+    if (p.gs % 2 == 1)
+        launch_forward_k<BITS, 1, NL, true>(p, st);
+    else if (v == 2)
+        launch_forward_k<BITS, 2, NL, false>(p, st);
+    else
+        launch_forward_k<BITS, 1, NL, false>(p, st);
+    return hipGetLastError();
+}
 template <int BITS>
 hipError_t launch_forward(const SkinnyForward &p, int v, hipStream_t st) {
-    if (p.f.s.layers == 2)
-        return v == 2 ? launch_forward_k<BITS, 2, 2>(p, st) : launch_forward_k<BITS, 1, 2>(p, st);
-    return v == 2 ? launch_forward_k<BITS, 2, 1>(p, st) : launch_forward_k<BITS, 1, 1>(p, st);
+    return p.f.s.layers == 2 ? launch_forward<BITS, 2>(p, v, st) : launch_forward<BITS, 1>(p, v, st);
 }
 
 template <int BITS>
@@ -572,7 +568,7 @@ void launch_backward(const SkinnyBackward &p, hipStream_t st) {
 bool skinny_forward_takes(const FusedShape &s) { return s.m <= (s.in_bf16 ? 64 : 16); }
 
 size_t skinny_forward_ws(const FusedShape &s) {
-    return s.m > GATHER_IN_PLACE ? align256((size_t)(s.m * s.d_in) * (s.in_bf16 ? 2 : 4)) : 0;
+    return align256((size_t)(s.m * cdiv(s.d_in, 32) * 32) * (s.in_bf16 ? 2 : 4));   // gathered rows
 }
 
 hipError_t skinny_forward_launch(const FusedForward &a, hipStream_t st) {
@@ -580,28 +576,30 @@ hipError_t skinny_forward_launch(const FusedForward &a, hipStream_t st) {
     SkinnyForward p{};
     p.f = a;
     p.A = a.A;
-    p.perm = a.perm;
-    if (a.perm && s.m > GATHER_IN_PLACE) {
-        const dim3 grid((unsigned)cdiv(s.d_in, 256), (unsigned)s.m);
-        if (s.in_bf16)
-            gather_rows_kernel<<<grid, 256, 0, st>>>((const uint16_t *)a.A, a.perm, (uint16_t *)a.ws, s.d_in);
-        else
-            gather_rows_kernel<<<grid, 256, 0, st>>>((const float *)a.A, a.perm, (float *)a.ws, s.d_in);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        p.A = a.ws;
-        p.perm = nullptr;
-    }
-    p.avec = !p.perm && s.d_in % 8 == 0 && aligned(p.A, 16);
-    // adjacent outputs per lane: two when that still fills the CUs (a pair of
-    // layers with four row tiles would not fit the registers)
-    const int v = cdiv(s.d_out, 32) >= 256 && !(s.layers == 2 && s.m > 16) ? 2 : 1;
-    p.wvec = s.d_out % 2 == 0;
-    for (int l = 0; l < s.layers; ++l)
-        p.wvec = p.wvec && aligned(a.w[l].Q, 8) && aligned(a.w[l].scales, 8) && aligned(a.w[l].zeros, 8);
+    p.lda = s.d_in;
     p.nunits = (int)cdiv(s.d_in, 32);
     p.gs = s.ngroups == 1 ? 1 << 30 : s.group / 16;
-    p.nwords = cdiv(s.bits * s.d_in, 32);
+    p.tail = (int)(cdiv(s.bits * s.d_in, 32) - (int64_t)s.bits * (p.nunits - 1));
+    if (a.perm || s.d_in % 32 != 0 || !aligned(a.A, 16)) {
+        p.A = a.ws;
+        p.lda = (int64_t)p.nunits * 32;
+        const dim3 grid((unsigned)cdiv(p.lda, 256), (unsigned)s.m);
+        if (s.in_bf16)
+            gather_rows_kernel<<<grid, 256, 0, st>>>((const uint16_t *)a.A, a.perm, (uint16_t *)a.ws, s.d_in, p.lda);
+        else
+            gather_rows_kernel<<<grid, 256, 0, st>>>((const float *)a.A, a.perm, (float *)a.ws, s.d_in, p.lda);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    // Adjacent outputs per lane: two where that still fills the CUs and pairs
+    // load together (not for groups that end inside a unit, for fp32
+    // activations, or for a pair of layers with four row tiles, whose
+    // registers it would double).
+    bool pairs = s.d_out % 2 == 0 && cdiv(s.d_out, 32) >= 256 && p.gs % 2 == 0 && s.in_bf16 &&
+                 !(s.layers == 2 && s.m > 16);
+    for (int l = 0; l < s.layers; ++l)
+        pairs = pairs && aligned(a.w[l].Q, 8) && aligned(a.w[l].scales, 8) && aligned(a.w[l].zeros, 8);
+    const int v = pairs ? 2 : 1;
     p.tiles = (int)cdiv(s.d_out, 16 * v);
     switch (s.bits) {
         case 2: return launch_forward<2>(p, v, st);
