@@ -399,15 +399,30 @@ def dequant_gated_backward_workspace_size(m, d_ff, d_in, bits, group_size, dy_dt
                                                                  da_dtype_code))
 
 
+def _operand(t, name, dtype, shape, device) -> int:
+    """The device pointer of a packed tensor of this dtype and shape on `device`; raises otherwise."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _require(t, name, dtype=dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
 class _FusedCall:
     """Checks and buffers of one fused call: operands on one device, a
     workspace and outputs that belong to the stream the work goes to."""
+    __slots__ = ("device", "in_code", "act", "out_dtype", "out_code", "d_in", "d_out", "words", "groups", "perm",
+                 "bits", "group", "stream", "given_ws", "guard")
 
-    def __init__(self, x, name, layers, activation, out_dtype, workspace, stream):
+    def __init__(self, x, name, q, activation, out_dtype, workspace, stream):
         torch = _torch()
         _require(x, name, ndim=2)
         self.in_code = _dtype_code(x)
-        self.device = x.device
+        device = self.device = x.device
         if activation not in ACTIVATIONS:
             raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}; got {activation!r}")
         self.act = ACTIVATIONS[activation]
@@ -415,70 +430,78 @@ class _FusedCall:
         if self.out_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"unsupported out_dtype {self.out_dtype}; use float32 or bfloat16")
         self.out_code = F32 if self.out_dtype == torch.float32 else BF16
-        q = layers[0]
-        self.d_in, self.d_out = q.d_in, q.scales.shape[1]
-        self.tensors = [x]
-        for l in layers:
-            if (l.d_in, l.bits, l.group_size, l.scales.shape[1]) != (self.d_in, q.bits, q.group_size, self.d_out):
-                raise ValueError("the layers must have the same sizes, bits and group_size")
-            if l.act_order != q.act_order or (l.act_order and l.perm.data_ptr() != q.perm.data_ptr()):
-                raise ValueError("the layers must share one perm (quantize_layers gives them one)")
-            words, groups = packed_words(l.d_in, l.bits), num_groups(l.d_in, l.group_size)
-            for t, n, dt, shape in ((l.qpacked, "qpacked", torch.int32, (words, self.d_out)),
-                                    (l.scales, "scales", torch.float32, (groups, self.d_out)),
-                                    (l.zeros, "zeros", torch.float32, (groups, self.d_out))):
-                self.take(t, n, dt, shape)
-            if l.act_order:
-                self.take(l.perm, "perm", torch.int32, (self.d_in,))
-        self.perm = q.perm.data_ptr() if q.act_order else None
-        self.bits, self.group = q.bits, q.group_size
-        self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if self.stream.device != self.device:
-            raise ValueError(f"the stream belongs to {self.stream.device}, {name} to {self.device}")
+        self.d_in, self.d_out, self.bits, self.group = q.d_in, q.scales.shape[1], q.bits, q.group_size
+        one = self.group == -1 or self.group >= self.d_in
+        self.words = -(-self.bits * self.d_in // 32)
+        self.groups = 1 if one or self.group < 1 else -(-self.d_in // self.group)
+        self.perm = _operand(q.perm, "perm", torch.int32, (self.d_in,), device) if q.act_order else None
+        self.guard = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream belongs to {stream.device}, {name} to {device}")
+            self.stream = stream.cuda_stream
+            self.guard = torch.cuda.stream(stream)
+        else:
+            self.stream = torch.cuda.current_stream(device).cuda_stream
+            if device.index != torch.cuda.current_device():
+                self.guard = torch.cuda.device(device)
         self.given_ws = workspace
         if workspace is not None:
-            _require(workspace, "workspace")
-            self.take(workspace, "workspace", workspace.dtype, workspace.shape)
+            _operand(workspace, "workspace", workspace.dtype, workspace.shape, device)
+        if torch.is_grad_enabled():
+            self.no_grad(x, q.scales, q.zeros)
+
+    def layer(self, q):
+        """A packed layer's pointers (codes, scales, zero points)."""
+        torch = _torch()
+        params = (self.groups, self.d_out)
+        return (_operand(q.qpacked, "qpacked", torch.int32, (self.words, self.d_out), self.device),
+                _operand(q.scales, "scales", torch.float32, params, self.device),
+                _operand(q.zeros, "zeros", torch.float32, params, self.device))
+
+    def pair(self, gate, up):
+        if (up.d_in, up.bits, up.group_size, up.scales.shape[1]) != (self.d_in, self.bits, self.group, self.d_out):
+            raise ValueError("the layers must have the same sizes, bits and group_size")
+        if up.act_order != gate.act_order or (up.act_order and up.perm.data_ptr() != self.perm):
+            raise ValueError("the layers must share one perm (quantize_layers gives them one)")
+        if _torch().is_grad_enabled():
+            self.no_grad(up.scales, up.zeros)
 
     def take(self, t, name, dtype, shape):
-        """An operand: its device pointer, or None for None."""
+        """An optional operand's pointer."""
         if t is None:
             return None
-        _require(t, name, dtype=dtype)
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, not on {self.device}")
-        self.tensors.append(t)
-        return t.data_ptr()
+        if _torch().is_grad_enabled():
+            self.no_grad(t)
+        return _operand(t, name, dtype, shape, self.device)
 
-    def no_autograd(self, what):
-        torch = _torch()
-        if torch.is_grad_enabled() and any(t.requires_grad for t in self.tensors):
-            raise ValueError(f"autograd does not see through {what}: call it under torch.no_grad() (or inside a "
-                             f"torch.autograd.Function) and {what}_backward for the gradients")
+    @staticmethod
+    def no_grad(*tensors):
+        if any(t.requires_grad for t in tensors):
+            raise ValueError("autograd does not see through the fused products: call them under torch.no_grad() (or "
+                             "inside a torch.autograd.Function) and their _backward calls for the gradients")
 
-    def empty(self, *shape, dtype=None):
+    def empty(self, shape, dtype=None):
         return _torch().empty(shape, dtype=dtype or self.out_dtype, device=self.device)
 
     def workspace(self, need):
-        """(pointer, bytes): the caller's when it suffices, otherwise allocated."""
-        if need == 0:
-            return None, 0
+        """(owner, pointer, bytes): the caller's when it suffices, otherwise allocated."""
         w = self.given_ws
         if w is not None and w.numel() * w.element_size() >= need:
-            return w.data_ptr(), w.numel() * w.element_size()
-        w = self.empty(need, dtype=_torch().uint8)
-        return w.data_ptr(), need
+            return w, w.data_ptr(), w.numel() * w.element_size()
+        if need == 0:
+            return None, None, 0
+        w = self.empty((need,), dtype=_torch().uint8)
+        return w, w.data_ptr(), need
 
     def __enter__(self):
         # allocations belong to the stream that uses them, on its own device
-        self.guard = _torch().cuda.stream(self.stream)
-        self.guard.__enter__()
-        return self
+        if self.guard is not None:
+            self.guard.__enter__()
 
     def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def dequant_linear(A, q: "QuantizedLayer", bias=None, activation="none", residual=None, out_dtype=None,
@@ -491,23 +514,22 @@ def dequant_linear(A, q: "QuantizedLayer", bias=None, activation="none", residua
     bias when save_preact.  workspace: any device tensor of at least
     dequant_linear_workspace_size bytes (allocated when absent or too small).
     Not differentiable by autograd: see dequant_linear_backward."""
-    f = _FusedCall(A, "A", (q,), activation, out_dtype, workspace, stream)
-    m = A.shape[0]
-    if A.shape[1] != f.d_in:
-        raise ValueError(f"A has {A.shape[1]} columns, the layer {f.d_in}")
+    f = _FusedCall(A, "A", q, activation, out_dtype, workspace, stream)
+    m, d_in = A.shape
+    if d_in != f.d_in:
+        raise ValueError(f"A has {d_in} columns, the layer {f.d_in}")
+    Qp, Sp, Zp = f.layer(q)
     b = f.take(bias, "bias", bias.dtype, (f.d_out,)) if bias is not None else None
+    bcode = _dtype_code(bias) if bias is not None else 0
     r = f.take(residual, "residual", f.out_dtype, (m, f.d_out))
-    f.no_autograd("dequant_linear")
     with f:
-        Y = f.empty(m, f.d_out)
-        Z = f.empty(m, f.d_out) if save_preact else None
-        ws, wsb = f.workspace(dequant_linear_workspace_size(m, f.d_out, f.d_in, f.bits, f.group, f.in_code,
-                                                            f.out_code))
-        _check(_lib().gptq_dequant_linear(A.data_ptr(), f.in_code, m, f.d_in, q.qpacked.data_ptr(),
-                                          q.scales.data_ptr(), q.zeros.data_ptr(), f.perm, f.d_out, f.bits, f.group,
-                                          b, _dtype_code(bias) if bias is not None else 0, f.act, r, Y.data_ptr(),
-                                          f.out_code, Z.data_ptr() if save_preact else None, ws, wsb,
-                                          int(f.stream.cuda_stream)))
+        Y = f.empty((m, f.d_out))
+        Z = f.empty((m, f.d_out)) if save_preact else None
+        _own, ws, wsb = f.workspace(dequant_linear_workspace_size(m, f.d_out, d_in, f.bits, f.group, f.in_code,
+                                                                  f.out_code))
+        _check(_lib().gptq_dequant_linear(A.data_ptr(), f.in_code, m, d_in, Qp, Sp, Zp, f.perm, f.d_out, f.bits,
+                                          f.group, b, bcode, f.act, r, Y.data_ptr(), f.out_code,
+                                          Z.data_ptr() if save_preact else None, ws, wsb, f.stream))
     return (Y, Z) if save_preact else Y
 
 
@@ -520,24 +542,22 @@ def dequant_linear_backward(dY, q: "QuantizedLayer", activation="none", preact=N
     None for activation "none").  dA: [m, d_in] in out_dtype (dY's dtype by
     default); dbias: [d_out] float32, or None unless bias_grad.  The residual's
     gradient is dY itself."""
-    f = _FusedCall(dY, "dY", (q,), activation, out_dtype, workspace, stream)
-    m = dY.shape[0]
-    if dY.shape[1] != f.d_out:
-        raise ValueError(f"dY has {dY.shape[1]} columns, the layer {f.d_out} rows")
+    f = _FusedCall(dY, "dY", q, activation, out_dtype, workspace, stream)
+    m, d_out = dY.shape
+    if d_out != f.d_out:
+        raise ValueError(f"dY has {d_out} columns, the layer {f.d_out} rows")
     if preact is None and f.act:
         raise ValueError("preact is required unless activation is 'none'")
-    z = f.take(preact, "preact", dY.dtype, (m, f.d_out))
-    f.no_autograd("dequant_linear")
+    Qp, Sp, Zp = f.layer(q)
+    z = f.take(preact, "preact", dY.dtype, (m, d_out))
     with f:
-        dA = f.empty(m, f.d_in)
-        db = f.empty(f.d_out, dtype=_torch().float32) if bias_grad else None
-        ws, wsb = f.workspace(dequant_linear_backward_workspace_size(m, f.d_out, f.d_in, f.bits, f.group, f.in_code,
-                                                                     f.out_code))
-        _check(_lib().gptq_dequant_linear_backward(dY.data_ptr(), f.in_code, m, f.d_out, z, f.act,
-                                                   q.qpacked.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(),
-                                                   f.perm, f.d_in, f.bits, f.group, dA.data_ptr(), f.out_code,
-                                                   db.data_ptr() if bias_grad else None, ws, wsb,
-                                                   int(f.stream.cuda_stream)))
+        dA = f.empty((m, f.d_in))
+        db = f.empty((d_out,), dtype=_torch().float32) if bias_grad else None
+        _own, ws, wsb = f.workspace(dequant_linear_backward_workspace_size(m, d_out, f.d_in, f.bits, f.group,
+                                                                           f.in_code, f.out_code))
+        _check(_lib().gptq_dequant_linear_backward(dY.data_ptr(), f.in_code, m, d_out, z, f.act, Qp, Sp, Zp, f.perm,
+                                                   f.d_in, f.bits, f.group, dA.data_ptr(), f.out_code,
+                                                   db.data_ptr() if bias_grad else None, ws, wsb, f.stream))
     return dA, db
 
 
@@ -550,28 +570,28 @@ def dequant_gated(A, gate: "QuantizedLayer", up: "QuantizedLayer", activation="s
     perm (quantize_layers).  Returns H [m, d_ff] in out_dtype (A's dtype by
     default), or (H, G, U) with both pre-activations when save_preact.  Other
     arguments as for dequant_linear."""
-    f = _FusedCall(A, "A", (gate, up), activation, out_dtype, workspace, stream)
-    m = A.shape[0]
-    if A.shape[1] != f.d_in:
-        raise ValueError(f"A has {A.shape[1]} columns, the layers {f.d_in}")
+    f = _FusedCall(A, "A", gate, activation, out_dtype, workspace, stream)
+    m, d_in = A.shape
+    if d_in != f.d_in:
+        raise ValueError(f"A has {d_in} columns, the layers {f.d_in}")
+    f.pair(gate, up)
+    Qg, Sg, Zg = f.layer(gate)
+    Qu, Su, Zu = f.layer(up)
     biases = [b for b in (bias_gate, bias_up) if b is not None]
     if len(biases) == 2 and biases[0].dtype != biases[1].dtype:
         raise TypeError("both biases must have the same dtype")
-    bcode = _dtype_code(biases[0]) if biases else 0
-    bg = f.take(bias_gate, "bias_gate", biases[0].dtype if biases else None, (f.d_out,))
-    bu = f.take(bias_up, "bias_up", biases[0].dtype if biases else None, (f.d_out,))
-    f.no_autograd("dequant_gated")
+    bdtype, bcode = (biases[0].dtype, _dtype_code(biases[0])) if biases else (None, 0)
+    bg = f.take(bias_gate, "bias_gate", bdtype, (f.d_out,))
+    bu = f.take(bias_up, "bias_up", bdtype, (f.d_out,))
     with f:
-        H = f.empty(m, f.d_out)
-        G, U = (f.empty(m, f.d_out), f.empty(m, f.d_out)) if save_preact else (None, None)
-        ws, wsb = f.workspace(dequant_gated_workspace_size(m, f.d_out, f.d_in, f.bits, f.group, f.in_code,
-                                                           f.out_code))
-        _check(_lib().gptq_dequant_gated(A.data_ptr(), f.in_code, m, f.d_in, gate.qpacked.data_ptr(),
-                                         gate.scales.data_ptr(), gate.zeros.data_ptr(), up.qpacked.data_ptr(),
-                                         up.scales.data_ptr(), up.zeros.data_ptr(), f.perm, f.d_out, f.bits, f.group,
-                                         bg, bu, bcode, f.act, H.data_ptr(), f.out_code,
+        H = f.empty((m, f.d_out))
+        G, U = (f.empty((m, f.d_out)), f.empty((m, f.d_out))) if save_preact else (None, None)
+        _own, ws, wsb = f.workspace(dequant_gated_workspace_size(m, f.d_out, d_in, f.bits, f.group, f.in_code,
+                                                                 f.out_code))
+        _check(_lib().gptq_dequant_gated(A.data_ptr(), f.in_code, m, d_in, Qg, Sg, Zg, Qu, Su, Zu, f.perm, f.d_out,
+                                         f.bits, f.group, bg, bu, bcode, f.act, H.data_ptr(), f.out_code,
                                          G.data_ptr() if save_preact else None,
-                                         U.data_ptr() if save_preact else None, ws, wsb, int(f.stream.cuda_stream)))
+                                         U.data_ptr() if save_preact else None, ws, wsb, f.stream))
     return (H, G, U) if save_preact else H
 
 
@@ -584,28 +604,27 @@ def dequant_gated_backward(dH, gate: "QuantizedLayer", up: "QuantizedLayer", gat
     dH, gate_pre (G), up_pre (U): [m, d_ff], one dtype (G and U as
     dequant_gated saved them).  dA: [m, d_in] in out_dtype (dH's dtype by
     default); the bias gradients: [d_ff] float32, or None unless bias_grad."""
-    f = _FusedCall(dH, "dH", (gate, up), activation, out_dtype, workspace, stream)
-    m = dH.shape[0]
-    if dH.shape[1] != f.d_out:
-        raise ValueError(f"dH has {dH.shape[1]} columns, the layers {f.d_out} rows")
+    f = _FusedCall(dH, "dH", gate, activation, out_dtype, workspace, stream)
+    m, d_ff = dH.shape
+    if d_ff != f.d_out:
+        raise ValueError(f"dH has {d_ff} columns, the layers {f.d_out} rows")
     if gate_pre is None or up_pre is None:
         raise ValueError("gate_pre and up_pre are required")
-    g = f.take(gate_pre, "gate_pre", dH.dtype, (m, f.d_out))
-    u = f.take(up_pre, "up_pre", dH.dtype, (m, f.d_out))
-    f.no_autograd("dequant_gated")
+    f.pair(gate, up)
+    Qg, Sg, Zg = f.layer(gate)
+    Qu, Su, Zu = f.layer(up)
+    g = f.take(gate_pre, "gate_pre", dH.dtype, (m, d_ff))
+    u = f.take(up_pre, "up_pre", dH.dtype, (m, d_ff))
     with f:
-        dA = f.empty(m, f.d_in)
-        dbg, dbu = ((f.empty(f.d_out, dtype=_torch().float32), f.empty(f.d_out, dtype=_torch().float32))
-                    if bias_grad else (None, None))
-        ws, wsb = f.workspace(dequant_gated_backward_workspace_size(m, f.d_out, f.d_in, f.bits, f.group, f.in_code,
-                                                                    f.out_code))
-        _check(_lib().gptq_dequant_gated_backward(dH.data_ptr(), f.in_code, m, f.d_out, g, u, f.act,
-                                                  gate.qpacked.data_ptr(), gate.scales.data_ptr(),
-                                                  gate.zeros.data_ptr(), up.qpacked.data_ptr(), up.scales.data_ptr(),
-                                                  up.zeros.data_ptr(), f.perm, f.d_in, f.bits, f.group,
-                                                  dA.data_ptr(), f.out_code, dbg.data_ptr() if bias_grad else None,
-                                                  dbu.data_ptr() if bias_grad else None, ws, wsb,
-                                                  int(f.stream.cuda_stream)))
+        f32 = _torch().float32
+        dA = f.empty((m, f.d_in))
+        dbg, dbu = (f.empty((d_ff,), dtype=f32), f.empty((d_ff,), dtype=f32)) if bias_grad else (None, None)
+        _own, ws, wsb = f.workspace(dequant_gated_backward_workspace_size(m, d_ff, f.d_in, f.bits, f.group,
+                                                                          f.in_code, f.out_code))
+        _check(_lib().gptq_dequant_gated_backward(dH.data_ptr(), f.in_code, m, d_ff, g, u, f.act, Qg, Sg, Zg, Qu, Su,
+                                                  Zu, f.perm, f.d_in, f.bits, f.group, dA.data_ptr(), f.out_code,
+                                                  dbg.data_ptr() if bias_grad else None,
+                                                  dbu.data_ptr() if bias_grad else None, ws, wsb, f.stream))
     return dA, dbg, dbu
 
 

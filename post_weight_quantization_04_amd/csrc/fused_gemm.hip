@@ -31,7 +31,8 @@ namespace {
 
 constexpr int GK = 32;                    // contraction elements per stage
 constexpr int64_t DENSE_ROWS = 16384;     // activation rows per pass (bounds the workspace)
-constexpr int BIAS_ROWS = 64;             // rows summed by one work group for a bias gradient
+constexpr int DZ_ROWS = 16;                // rows of dZ formed by one work group
+constexpr int BIAS_ROWS = 64;             // ... when it also sums them for a bias gradient of many rows
 
 // 2^-e for a positive finite v in [2^e, 2^(e+1)) times 2^14, as a factor and
 // its inverse (both normal); 1 for 0
@@ -249,6 +250,7 @@ struct BackwardPrep {
     uint16_t *W16;              // rows [d_in], contraction [planes_w][layers][kp]
     int planes_w;
     float *fw;                  // [d_in] inverse factors, original order
+    int dz_rows;                // rows of a dZ tile
     int64_t dz_blocks, dz_cols; // dZ tiles, then weight tiles
 };
 
@@ -299,13 +301,13 @@ __global__ __launch_bounds__(256) void backward_range_kernel(BackwardPrep p) {
     }
 }
 
-// 64 rows by 256 columns of dZ (of dG and dU): rounded to f16 planes, and the
+// dz_rows rows by 256 columns of dZ (of dG and dU): rounded to f16 planes, and the
 // columns' sums over the tile's rows when bias gradients are wanted
 __device__ void prep_dz(const BackwardPrep &p, int64_t b, float *lds) {
     const int tid = threadIdx.x;
     const int64_t cb = b % p.dz_cols, rb = b / p.dz_cols;
     const int64_t r0 = cb * 256 + 8 * (tid & 31);
-    const int64_t ilast = std::min<int64_t>(p.m, (rb + 1) * BIAS_ROWS);
+    const int64_t ilast = std::min<int64_t>(p.m, (rb + 1) * p.dz_rows);
     float sum[2][8] = {};
     auto load8 = [&](const void *x, int64_t o, float (&v)[8]) {
         if (p.vec) {
@@ -336,7 +338,7 @@ __device__ void prep_dz(const BackwardPrep &p, int64_t b, float *lds) {
         put_planes(p.D16 + operand_at(i, l * p.kp + r0, p.planes_a * p.layers * p.kp), p.layers * p.kp * 256, p.planes_a,
                    0, v);
     };
-    for (int64_t i = rb * BIAS_ROWS + (tid >> 5); i < ilast; i += 8) {
+    for (int64_t i = rb * p.dz_rows + (tid >> 5); i < ilast; i += 8) {
         const int64_t o = i * p.d_out + r0;
         const float mul = p.fa[i];
         float d[8], z[8], u[8];
@@ -487,7 +489,8 @@ struct Gemm {
     void *Y;
     void *pre[2];
     int out_bf16, vec;          // vec: four consecutive outputs load and store together
-    float *part;                // [nsplit][layers][m][n] when nsplit > 1
+    float *part;                // [nsplit][layers][m][np] when nsplit > 1
+    int64_t np;                 // n padded to whole quads
     int nsplit;
     int mt, nt;                 // tiles
 };
@@ -553,8 +556,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t gm_rsrc(const void *p, int64_t
     return __builtin_amdgcn_make_buffer_rsrc((void *)bu, (short)0, n, 0x00020000);
 }
 
-// C tile of 256 columns n by 64 MI rows, four waves of 128 by 32 MI as 32 x 32
-// MFMA tiles.  The weights are the MFMA's first operand, so that a lane holds
+// C tile of 64 NJ columns n by 64 MI rows, four waves of 32 NJ by 32 MI as
+// 32 x 32 MFMA tiles.  The weights are the MFMA's first operand, so that a lane holds
 // four consecutive columns of one activation row.  Both operands move by
 // 16-byte buffer loads straight into a ring of four LDS stages of 32 k (each
 // load a contiguous kilobyte: read from rows a stage apart in K-major
@@ -567,14 +570,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t gm_rsrc(const void *p, int64_t
 //
 // The sums leave through LDS, 64 rows at a time in two buffers, so that the
 // epilogue reads and writes whole row segments.
-template <int MI, bool GATED>
+template <int MI, int NJ, bool GATED>
 __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
-    constexpr int BM = 64 * MI, BN = 256, NBUF = 4;
+    constexpr int BM = 64 * MI, BN = 64 * NJ, NBUF = 4;
     constexpr int NSIDE = BN * GK * 2, STAGE = NSIDE + BM * GK * 2;   // bytes
-    constexpr int NDMA = 4, MDMA = MI;                                // loads per wave and stage
+    constexpr int NDMA = NJ, MDMA = MI;                               // loads per wave and stage
     constexpr int PER_STAGE = NDMA + MDMA;
-    constexpr int COLS = GATED ? 128 : 256;                           // columns n of one layer
-    constexpr int EROW = 256 + 4;                                     // floats of an epilogue row (padded)
+    constexpr int COLS = GATED ? BN / 2 : BN;                         // columns n of one layer
+    constexpr int EROW = BN + 4;                                      // floats of an epilogue row (padded)
     __shared__ __attribute__((aligned(16))) char lds[std::max(NBUF * STAGE, 2 * 64 * EROW * 4)];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -603,7 +606,7 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
     // hold only reaches results that are never stored)
     const uint16_t *abase = p.A + (m0 >> 8) * (p.lda / GK) * TILE_STAGE + (m0 & 255) * GK;
     // the gated pair: waves 2 and 3 move the up layer's rows
-    const int64_t bskip = GATED ? (wave >> 1) * pad_tile(p.n) * p.ldb - (wave >> 1) * 128 * GK : 0;
+    const int64_t bskip = GATED ? (wave >> 1) * pad_tile(p.n) * p.ldb - (wave >> 1) * (BN / 2) * GK : 0;
     const uint16_t *bbase = p.B + (n0 >> 8) * (p.ldb / GK) * TILE_STAGE + (n0 & 255) * GK + bskip;
     const __amdgpu_buffer_rsrc_t arsrc = gm_rsrc(abase, p.lda / GK * TILE_STAGE * 2);
     const __amdgpu_buffer_rsrc_t brsrc = gm_rsrc(bbase, p.ldb / GK * TILE_STAGE * 2);
@@ -629,24 +632,25 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
     const int sw = swz(li);
     int brow[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) brow[j] = (GATED ? (j >> 1) * 128 + wn * 64 + (j & 1) * 32 : wn * 128 + 32 * j) + li;
+    for (int j = 0; j < NJ; ++j)
+        brow[j] = (GATED ? j / (NJ / 2) * (BN / 2) + wn * (BN / 4) + j % (NJ / 2) * 32 : wn * (BN / 2) + 32 * j) + li;
     const int arow = wm * 32 * MI + li;
-    auto frags = [&](int st, int ks, f16x8 (&fb)[4], f16x8 (&fa)[MI]) {
+    auto frags = [&](int st, int ks, f16x8 (&fb)[NJ], f16x8 (&fa)[MI]) {
         const char *buf = lds + (st % NBUF) * STAGE;
         const int piece = 16 * ((2 * ks + h) ^ sw);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) fb[j] = *(const f16x8 *)(buf + brow[j] * GK * 2 + piece);
+        for (int j = 0; j < NJ; ++j) fb[j] = *(const f16x8 *)(buf + brow[j] * GK * 2 + piece);
 #pragma unroll
         for (int i = 0; i < MI; ++i) fa[i] = *(const f16x8 *)(buf + NSIDE + (arow + 32 * i) * GK * 2 + piece);
     };
-    f32x16 acc[4][MI];
+    f32x16 acc[NJ][MI];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int i = 0; i < MI; ++i) acc[j][i] = f32x16{};
-    auto products = [&](const f16x8 (&fb)[4], const f16x8 (&fa)[MI]) {
+    auto products = [&](const f16x8 (&fb)[NJ], const f16x8 (&fa)[MI]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int i = 0; i < MI; ++i)
                 acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[j], fa[i], acc[j][i], 0, 0, 0);
@@ -656,17 +660,17 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
     auto spread = [] {
         constexpr int MFMA = 0x008, VMEM = 0x010, DSR = 0x100;
 #pragma unroll
-        for (int i = 0; i < 4 + MI; ++i) {
+        for (int i = 0; i < NJ + MI; ++i) {
             __builtin_amdgcn_sched_group_barrier(DSR, 1, 0);
             __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
         }
 #pragma unroll
         for (int i = 0; i < PER_STAGE / 2; ++i) {
             __builtin_amdgcn_sched_group_barrier(VMEM, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(MFMA, MI == 4 ? 2 : 1, 0);
+            __builtin_amdgcn_sched_group_barrier(MFMA, MI * NJ == 16 ? 2 : 1, 0);
         }
     };
-    f16x8 fb0[4], fa0[MI], fb1[4], fa1[MI];
+    f16x8 fb0[NJ], fa0[MI], fb1[NJ], fa1[MI];
     for (int st = 0; st < NBUF - 1; ++st) {
         issue(st, 0);
         issue(st, 1);
@@ -702,7 +706,7 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
     for (int i = 0; i < MI; ++i) {
         float *out = (float *)lds + (i & 1) * 64 * EROW;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int col = brow[j] - li + 8 * q + 4 * h;
@@ -716,20 +720,11 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
             if (row >= p.m || n >= p.n) continue;
             const f32x4 z = *(const f32x4 *)(out + rr * EROW + c);
             f32x4 u = {0.f, 0.f, 0.f, 0.f};
-            if (GATED) u = *(const f32x4 *)(out + rr * EROW + 128 + c);
+            if (GATED) u = *(const f32x4 *)(out + rr * EROW + BN / 2 + c);
             if (p.nsplit > 1) {
-                float *part = p.part + ((int64_t)split * p.layers * p.m + row) * p.n + n;
-                if (p.vec) {
-                    *(f32x4 *)part = z;
-                    if (GATED) *(f32x4 *)(part + p.m * p.n) = u;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < p.n) {
-                            part[e] = z[e];
-                            if (GATED) part[p.m * p.n + e] = u[e];
-                        }
-                }
+                float *part = p.part + (((int64_t)split * p.layers * p.m) + row) * p.np + n;
+                *(f32x4 *)part = z;
+                if (GATED) *(f32x4 *)(part + p.m * p.np) = u;
             } else {
                 epilogue4<GATED>(p, row, n, p.fa[row], z, u);
             }
@@ -740,43 +735,35 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
 // the splits' sums in split order, and the epilogue: four columns per thread
 template <bool GATED>
 __global__ __launch_bounds__(256) void split_reduce_kernel(Gemm p) {
-    const int64_t quads = (p.n + 3) / 4;
+    const int64_t quads = p.np / 4;
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (t >= p.m * quads) return;
     const int64_t i = t / quads, n = 4 * (t - i * quads);
     f32x4 z = {0.f, 0.f, 0.f, 0.f}, u = z;
     for (int s = 0; s < p.nsplit; ++s) {
-        const float *z0 = p.part + ((int64_t)s * p.layers * p.m + i) * p.n + n;
-        const float *u0 = z0 + p.m * p.n;
-        if (p.vec) {
-            z += *(const f32x4 *)z0;
-            if (GATED) u += *(const f32x4 *)u0;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (n + e < p.n) {
-                    z[e] += z0[e];
-                    if (GATED) u[e] += u0[e];
-                }
-        }
+        const float *z0 = p.part + ((int64_t)s * p.layers * p.m + i) * p.np + n;
+        z += *(const f32x4 *)z0;
+        if (GATED) u += *(const f32x4 *)(z0 + p.m * p.np);
     }
     epilogue4<GATED>(p, i, n, p.fa[i], z, u);
 }
 
 int64_t pad_stage(int64_t k) { return cdiv(k, GK) * GK; }
+int64_t pad_quad(int64_t n) { return cdiv(n, 4) * 4; }
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-struct Plan {
-    int mi, mt, nt, nsplit;
-};
-// Tiles of 256 rows unless half as many would do; k splits for grids that
+// Tiles of 256 x 256, or of 128 x 128 where fewer than 32 large ones would do
+// (509 x 251 fp32: 23 us a call against 31; 2048 x 4096, 128 large tiles with
+// two k splits: 263 us against 294 with 128 x 128).  k splits for grids that
 // leave CUs idle, each of at least eight stages.
+struct Plan {
+    int mi, nj, mt, nt, nsplit;   // tile of 64 mi rows by 64 nj columns
+};
 Plan plan_gemm(int64_t m, int64_t n, int layers, int stages) {
     Plan p;
-    const int cols = layers == 2 ? 128 : 256;
-    p.nt = (int)cdiv(n, cols);
-    p.mi = m > 128 ? 4 : 2;
+    p.mi = p.nj = cdiv(m, 256) * cdiv(layers * n, 256) >= 32 ? 4 : 2;
     p.mt = (int)cdiv(m, 64 * p.mi);
+    p.nt = (int)cdiv(n, (layers == 2 ? 32 : 64) * p.nj);
     const int64_t tiles = (int64_t)p.mt * p.nt;
     p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, (int64_t)stages / 8, (int64_t)16}));
     return p;
@@ -814,10 +801,14 @@ ForwardWs forward_layout(const FusedShape &s, char *base) {
     w.fa = l.take<float>(w.rows);
     w.W16 = l.take<uint16_t>(s.layers * pad_tile(s.d_out) * w.planes_w * w.kp);
     w.A16 = l.take<uint16_t>(pad_tile(w.rows) * w.planes_a * w.kp);
-    w.part = l.take<float>(w.plan.nsplit > 1 ? w.plan.nsplit * s.layers * w.rows * s.d_out : 0);
+    w.part = l.take<float>(w.plan.nsplit > 1 ? w.plan.nsplit * s.layers * w.rows * pad_quad(s.d_out) : 0);
     w.bytes = l.bytes;
     return w;
 }
+
+// Few rows: enough work groups; many rows with a bias gradient: fewer partial
+// sums per column
+int dz_rows(int64_t m, bool bias) { return bias && m > 1024 ? BIAS_ROWS : DZ_ROWS; }
 
 struct BackwardWs {
     float *fw, *fg, *fa, *part, *bias;
@@ -840,24 +831,27 @@ BackwardWs backward_layout(const FusedShape &s, char *base) {
     w.fa = l.take<float>(2 * w.rows);
     w.W16 = l.take<uint16_t>(pad_tile(s.d_in) * w.planes_w * s.layers * w.kp);
     w.D16 = l.take<uint16_t>(pad_tile(w.rows) * w.planes_a * s.layers * w.kp);
-    w.bias = l.take<float>(cdiv(w.rows, BIAS_ROWS) * s.layers * s.d_out);
-    w.part = l.take<float>(w.plan.nsplit > 1 ? w.plan.nsplit * w.rows * s.d_in : 0);
+    w.bias = l.take<float>(cdiv(w.rows, dz_rows(w.rows, true)) * s.layers * s.d_out);
+    w.part = l.take<float>(w.plan.nsplit > 1 ? w.plan.nsplit * w.rows * pad_quad(s.d_in) : 0);
     w.bytes = l.bytes;
     return w;
 }
 
-template <int MI, bool GATED>
+template <int MI, int NJ, bool GATED>
 hipError_t launch_gemm_k(const Gemm &g, hipStream_t st) {
-    fused_gemm_kernel<MI, GATED><<<(unsigned)(g.mt * g.nt * g.nsplit), 256, 0, st>>>(g);
+    fused_gemm_kernel<MI, NJ, GATED><<<(unsigned)(g.mt * g.nt * g.nsplit), 256, 0, st>>>(g);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || g.nsplit == 1) return e;
-    split_reduce_kernel<GATED><<<(unsigned)cdiv(g.m * cdiv(g.n, 4), 256), 256, 0, st>>>(g);
+    split_reduce_kernel<GATED><<<(unsigned)cdiv(g.m * (g.np / 4), 256), 256, 0, st>>>(g);
     return hipGetLastError();
 }
 
-hipError_t launch_gemm(const Gemm &g, int mi, hipStream_t st) {
-    if (g.layers == 2) return mi == 4 ? launch_gemm_k<4, true>(g, st) : launch_gemm_k<2, true>(g, st);
-    return mi == 4 ? launch_gemm_k<4, false>(g, st) : launch_gemm_k<2, false>(g, st);
+template <bool GATED>
+hipError_t launch_gemm(const Gemm &g, const Plan &p, hipStream_t st) {
+    return p.mi == 4 ? launch_gemm_k<4, 4, GATED>(g, st) : launch_gemm_k<2, 2, GATED>(g, st);
+}
+hipError_t launch_gemm(const Gemm &g, const Plan &p, hipStream_t st) {
+    return g.layers == 2 ? launch_gemm<true>(g, p, st) : launch_gemm<false>(g, p, st);
 }
 
 constexpr size_t PREP_LDS_MAX = 128 * 1024;   // bytes of an activation row staged for its gather
@@ -946,10 +940,11 @@ hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st) {
         g.Y = (void *)at(a.Y, o, s.out_bf16);
         g.out_bf16 = s.out_bf16;
         g.part = w.part;
+        g.np = pad_quad(g.n);
         g.nsplit = w.plan.nsplit;
         g.mt = (int)cdiv(m, 64 * w.plan.mi);   // (the last rows may be fewer)
         g.nt = w.plan.nt;
-        e = launch_gemm(g, w.plan.mi, st);
+        e = launch_gemm(g, w.plan, st);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -994,7 +989,8 @@ hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st) {
         p.planes_w = w.planes_w;
         p.fw = w.fw;
         p.dz_cols = cdiv(w.kp, 256);
-        const int64_t row_blocks = cdiv(m, BIAS_ROWS);
+        p.dz_rows = dz_rows(m, bias);
+        const int64_t row_blocks = cdiv(m, p.dz_rows);
         p.dz_blocks = p.dz_cols * row_blocks;
         // the groups' ranges and the weights once, with the first rows
         backward_range_kernel<<<(unsigned)(m + (i0 == 0 ? s.ngroups : 0)), 256, 0, st>>>(p);
@@ -1033,10 +1029,11 @@ hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st) {
         g.out_bf16 = s.out_bf16;
         g.vec = s.d_in % 4 == 0 && aligned(a.dA, 16);
         g.part = w.part;
+        g.np = pad_quad(g.n);
         g.nsplit = w.plan.nsplit;
         g.mt = (int)cdiv(m, 64 * w.plan.mi);
         g.nt = w.plan.nt;
-        e = launch_gemm(g, w.plan.mi, st);
+        e = launch_gemm(g, w.plan, st);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

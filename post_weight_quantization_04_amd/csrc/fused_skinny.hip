@@ -16,7 +16,7 @@ __device__ __forceinline__ int xcd_run(int b, int total) {
 }
 
 // ---------------------------------------------------------------------------
-// Forward, m <= 64: Z = A_p (q - z)^T per group on 16 x 16 x 32 bf16 MFMAs.
+// Forward, few rows (up to 64 per work group): Z = A_p (q - z)^T per group on 16 x 16 x 32 bf16 MFMAs.
 // q - z is an integer in [-255, 255], exact in bf16, and a group's products
 // sum in fp32 before its scale: the same arithmetic for every output type.
 // fp32 activations enter as three bf16 terms (24 bits), one MFMA each.
@@ -32,6 +32,7 @@ __device__ __forceinline__ int xcd_run(int b, int total) {
 // the last ones, units past a wave's run its last unit.
 // ---------------------------------------------------------------------------
 constexpr int SK_NW = 8;
+constexpr int SK_MAX_M = 128;   // bf16 rows, in blocks of up to 64
 
 struct SkinnyForward {
     FusedForward f;
@@ -62,42 +63,32 @@ __device__ __forceinline__ bf16x8 int_weights(const Codes8<BITS> &c, float z) {
     return w;
 }
 
-// HALF: groups may end between the halves of a unit (g not a multiple of 32)
-template <int BITS, int V, int MT, int NL, bool A32, bool HALF>
+// CH: units of a chunk (1 or 4) that lies in one group; 0: chunks of one unit
+// whose halves may belong to two groups (g not a multiple of 32)
+template <int BITS, int V, int MT, int NL, bool A32, int CH>
 __global__ __launch_bounds__(64 * SK_NW) void skinny_forward_kernel(SkinnyForward p) {
+    constexpr bool HALF = CH == 0;
+    constexpr int C = HALF ? 1 : CH;                            // units of a chunk
     constexpr int ROWS = 16 * V, NWD = fz_two_words<BITS>() ? 2 : 1;
-    constexpr int PF = MT > 1 ? 2 : (V * NL == 1 ? 8 : 4);      // units in flight
     constexpr int AP = A32 ? 3 : 1, AL = A32 ? 2 : 1, ES = A32 ? 4 : 2;   // bf16 terms, loads and bytes of activations
+    // chunks in flight
+    constexpr int PF = C == 4 ? (MT > 1 || NL * V * NWD > 2 || A32 ? 1 : 3) : (MT > 1 ? 2 : (V * NL == 1 ? 8 : 4));
     __shared__ float red[SK_NW * NL * 16 * ROWS];
     const FusedShape &s = p.f.s;
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t r0 = (int64_t)xcd_run(blockIdx.x, p.tiles) * ROWS;
-    const int u0 = __builtin_amdgcn_readfirstlane((int)((int64_t)p.nunits * wave / SK_NW));
-    const int u1 = __builtin_amdgcn_readfirstlane((int)((int64_t)p.nunits * (wave + 1) / SK_NW));
+    const int m0 = MT > 1 ? 16 * MT * (int)blockIdx.y : 0;      // first activation row
+    const int nch = p.nunits / C;                               // (whole chunks: see the launch)
+    const int c0 = __builtin_amdgcn_readfirstlane((int)((int64_t)nch * wave / SK_NW));
+    const int c1 = __builtin_amdgcn_readfirstlane((int)((int64_t)nch * (wave + 1) / SK_NW));
 
     struct Slot {
-        unsigned w[NL][NWD][V], z[NL][V], s0[NL][V], s1[NL][HALF ? V : 1];   // (s1: the second half's scale)
-        u32x4 a[MT][AL];
+        unsigned w[C][NL][NWD][V], z[NL][V], s0[NL][V], s1[NL][HALF ? V : 1];   // (s1: the second half's scale)
+        u32x4 a[C][MT][AL];
     };
-    // group of a unit's first half, and that half's place in the group
-    struct Place {
-        int g, at;
-        __device__ __forceinline__ void next(int gs) {
-            at += 2;
-            g += at >= gs;
-            at -= at >= gs ? gs : 0;
-            if (HALF) {   // (two groups a unit for g of 16)
-                g += at >= gs;
-                at -= at >= gs ? gs : 0;
-            }
-        }
-    };
-    Place ahead, here;
-    ahead.g = here.g = __builtin_amdgcn_readfirstlane(2 * u0 / p.gs);
-    ahead.at = here.at = __builtin_amdgcn_readfirstlane(2 * u0 - here.g * p.gs);
 
-    // Units are fetched in order: scalar pointers move along, the lanes'
+    // Chunks are fetched in order: scalar pointers move along, the lanes'
     // offsets stay.
     const unsigned stride = (unsigned)s.d_out * 4;   // bytes of a word row, of a group's scales
     const unsigned ro = (unsigned)std::min<int64_t>(r0 + V * li, s.d_out - V) * 4;
@@ -110,137 +101,159 @@ __global__ __launch_bounds__(64 * SK_NW) void skinny_forward_kernel(SkinnyForwar
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
-        ao[t] = (unsigned)((std::min(16 * t + li, (int)s.m - 1) * (int)p.lda + 8 * kg) * ES);
-    int at = std::min(u0, p.nunits - 1);             // the next unit to fetch
-    const char *qp[NL], *ap = (const char *)p.A + (int64_t)at * 32 * ES;
+        ao[t] = (unsigned)((std::min(m0 + 16 * t + li, (int)s.m - 1) * (int)p.lda + 8 * kg) * ES);
+    int at = std::min(c0, nch - 1);                  // the next chunk to fetch
+    const char *ap = (const char *)p.A + (int64_t)at * C * 32 * ES;
+    const char *qp[NL], *zp[NL], *sp[NL];
+    // the chunk's group (its first half's, and that half's place in it), or
+    // the chunks left in it
+    int g = 0, place = 0;
+    if constexpr (HALF) {
+        g = __builtin_amdgcn_readfirstlane(2 * at / p.gs);
+        place = __builtin_amdgcn_readfirstlane(2 * at - g * p.gs);
+    } else {
+        const int per = p.gs / (2 * C);              // chunks of a group
+        g = __builtin_amdgcn_readfirstlane(at / per);
+        place = per - __builtin_amdgcn_readfirstlane(at - g * per);
+    }
 #pragma unroll
-    for (int l = 0; l < NL; ++l) qp[l] = (const char *)p.f.w[l].Q + (int64_t)at * BITS * stride;
+    for (int l = 0; l < NL; ++l) {
+        qp[l] = (const char *)p.f.w[l].Q + (int64_t)at * C * BITS * stride;
+        zp[l] = (const char *)p.f.w[l].zeros + (int64_t)g * stride;
+        sp[l] = (const char *)p.f.w[l].scales + (int64_t)g * stride;
+    }
     auto fetch = [&](Slot &sl) {
-        const bool last = at == p.nunits - 1;
-        const int64_t go = (int64_t)std::min(ahead.g, s.ngroups - 1) * stride;
-        const bool between = HALF && ahead.at + 1 >= p.gs && ahead.g + 1 < s.ngroups;
+        const bool last = at == nch - 1;
+        // (past the end the last group's parameters stand in)
+        const bool between = HALF && place + 1 >= p.gs && g + 1 < s.ngroups;
         const unsigned second = between ? stride : 0u;
 #pragma unroll
         for (int l = 0; l < NL; ++l) {
 #pragma unroll
-            for (int d = 0; d < NWD; ++d) load_rows<V>(qp[l], last ? qlast[d] : qo[d], sl.w[l][d]);
-            load_rows<V>((const char *)p.f.w[l].zeros + go, ro + (HALF && kg >= 2 ? second : 0u), sl.z[l]);
-            load_rows<V>((const char *)p.f.w[l].scales + go, ro, sl.s0[l]);
-            if constexpr (HALF) load_rows<V>((const char *)p.f.w[l].scales + go, ro + second, sl.s1[l]);
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int d = 0; d < NWD; ++d)
+                    load_rows<V>(qp[l] + c * BITS * stride, last && c == C - 1 ? qlast[d] : qo[d], sl.w[c][l][d]);
+            load_rows<V>(zp[l], ro + (HALF && kg >= 2 ? second : 0u), sl.z[l]);
+            load_rows<V>(sp[l], ro, sl.s0[l]);
+            if constexpr (HALF) load_rows<V>(sp[l], ro + second, sl.s1[l]);
         }
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int h = 0; h < AL; ++h) sl.a[t][h] = *(const u32x4 *)(ap + ao[t] + 16 * h);
-        const bool more = at + 1 < u1;
-        ap += more ? 32 * ES : 0;
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int l = 0; l < NL; ++l) qp[l] += more ? BITS * stride : 0u;
-        at += more;
-        if (more) ahead.next(p.gs);
+                for (int h = 0; h < AL; ++h) sl.a[c][t][h] = *(const u32x4 *)(ap + ao[t] + 32 * ES * c + 16 * h);
+        if (at + 1 < c1) {
+            ++at;
+            ap += C * 32 * ES;
+            int on;   // groups to move on
+            if constexpr (HALF) {
+                place += 2;
+                on = place >= p.gs;
+                place -= on ? p.gs : 0;
+                const int again = place >= p.gs;   // (two groups a unit for g of 16)
+                place -= again ? p.gs : 0;
+                on = std::min(on + again, s.ngroups - 1 - g);
+                g += on;
+            } else {
+                on = --place == 0;
+                place += on ? p.gs / (2 * C) : 0;
+            }
+#pragma unroll
+            for (int l = 0; l < NL; ++l) {
+                qp[l] += C * BITS * stride;
+                zp[l] += on * stride;
+                sp[l] += on * stride;
+            }
+        }
     };
 
-    f32x4 acc[NL][V][MT], dg[NL][V][MT];
+    f32x4 acc[NL][V][MT];
 #pragma unroll
     for (int l = 0; l < NL; ++l)
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int t = 0; t < MT; ++t) acc[l][j][t] = dg[l][j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float scale[NL][V];   // of the group that dg belongs to
-    auto fold = [&] {
-#pragma unroll
-        for (int l = 0; l < NL; ++l)
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[l][j][t][e] = fmaf(scale[l][j], dg[l][j][t][e], acc[l][j][t][e]);
-                    dg[l][j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
-    };
+            for (int t = 0; t < MT; ++t) acc[l][j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // a chunk's products in fp32, then its scale
     auto use = [&](const Slot &sl) {
         const int sh = (BITS * 8 * kg) & 31;   // (a unit starts on a word)
-        bf16x8 w[NL][V], a[MT][AP];
+        bf16x8 a[C][MT][AP];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                if constexpr (A32) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const unsigned bits = sl.a[c][t][e >> 2 & (AL - 1)][e & 3];
+                        const float x = __builtin_bit_cast(float, bits);
+                        const bool finite = fabsf(x) < __builtin_inff();   // (others only in the first term)
+                        const __bf16 b0 = (__bf16)x;
+                        const float x1 = finite ? x - (float)b0 : 0.f;
+                        const __bf16 b1 = (__bf16)x1;
+                        a[c][t][0][e] = b0;
+                        a[c][t][AP > 1 ? 1 : 0][e] = AP > 1 ? b1 : b0;
+                        a[c][t][AP - 1][e] = AP > 1 ? (__bf16)(x1 - (float)b1) : b0;
+                    }
+                } else {
+                    a[c][t][0] = __builtin_bit_cast(bf16x8, sl.a[c][t][0]);
+                }
+            }
 #pragma unroll
         for (int l = 0; l < NL; ++l)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const unsigned zb = sl.z[l][j], sb = sl.s0[l][j];
-                w[l][j] = int_weights<BITS>(fz_codes8<BITS>(sl.w[l][0][j], sl.w[l][NWD - 1][j], sh),
-                                            __builtin_bit_cast(float, zb));
-                scale[l][j] = __builtin_bit_cast(float, sb);
+                const unsigned zb = sl.z[l][j], s0 = sl.s0[l][j], s1 = sl.s1[l][HALF ? j : 0];
+                f32x4 dg[MT], dh[MT];
+#pragma unroll
+                for (int t = 0; t < MT; ++t) dg[t] = dh[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const bf16x8 w = int_weights<BITS>(fz_codes8<BITS>(sl.w[c][l][0][j], sl.w[c][l][NWD - 1][j], sh),
+                                                       __builtin_bit_cast(float, zb));
+                    const bf16x8 w0 = HALF && kg >= 2 ? bf16x8{} : w, w1 = kg < 2 ? bf16x8{} : w;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int q = AP - 1; q >= 0; --q) {
+                            if constexpr (HALF) {   // (lanes of the other half: no activations either, see inf)
+                                const bf16x8 x0 = kg >= 2 ? bf16x8{} : a[c][t][q], x1 = kg < 2 ? bf16x8{} : a[c][t][q];
+                                dg[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x0, w0, dg[t], 0, 0, 0);
+                                dh[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x1, w1, dh[t], 0, 0, 0);
+                            } else {
+                                dg[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[c][t][q], w, dg[t], 0, 0, 0);
+                            }
+                        }
+                }
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc[l][j][t][e] = fmaf(__builtin_bit_cast(float, s0), dg[t][e], acc[l][j][t][e]);
+                        if (HALF) acc[l][j][t][e] = fmaf(__builtin_bit_cast(float, s1), dh[t][e], acc[l][j][t][e]);
+                    }
             }
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            if constexpr (A32) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const unsigned bits = sl.a[t][e >> 2 & (AL - 1)][e & 3];
-                    const float x = __builtin_bit_cast(float, bits);
-                    const bool finite = fabsf(x) < __builtin_inff();   // (others only in the first term)
-                    const __bf16 b0 = (__bf16)x;
-                    const float x1 = finite ? x - (float)b0 : 0.f;
-                    const __bf16 b1 = (__bf16)x1;
-                    a[t][0][e] = b0;
-                    a[t][AP > 1 ? 1 : 0][e] = AP > 1 ? b1 : b0;
-                    a[t][AP - 1][e] = AP > 1 ? (__bf16)(x1 - (float)b1) : b0;
-                }
-            } else {
-                a[t][0] = __builtin_bit_cast(bf16x8, sl.a[t][0]);
-            }
-        }
-        auto multiply = [&](bool keep) {   // keep: this lane's codes take part
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int q = AP - 1; q >= 0; --q) {
-                    const bf16x8 x = keep ? a[t][q] : bf16x8{};
-#pragma unroll
-                    for (int l = 0; l < NL; ++l)
-#pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            dg[l][j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[l][j], dg[l][j][t], 0, 0, 0);
-                }
-        };
-        if (!HALF || here.at + 1 < p.gs) {   // both halves in one group
-            multiply(true);
-            if (here.at + 2 == p.gs) fold();
-        } else {                             // a group ends between them
-            multiply(kg < 2);
-            fold();
-#pragma unroll
-            for (int l = 0; l < NL; ++l)
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const unsigned sb = sl.s1[l][HALF ? j : 0];
-                    scale[l][j] = __builtin_bit_cast(float, sb);
-                }
-            multiply(kg >= 2);
-            if (p.gs == 1) fold();
-        }
-        here.next(p.gs);
     };
 
     Slot sl[PF];
 #pragma unroll
     for (int q = 0; q < PF; ++q) fetch(sl[q]);
-    for (int u = u0; u < u1; u += PF) {
+    for (int c = c0; c < c1; c += PF) {
 #pragma unroll
         for (int q = 0; q < PF; ++q) {
-            if (u + q < u1) use(sl[q]);
-            fetch(sl[q]);
+            if (c + q < c1) use(sl[q]);
+            if (c + q + PF < c1) fetch(sl[q]);
         }
     }
-    if (u1 > u0) fold();
 
-    // lane, register e of (j, t) <-> token 16 t + 4 kg + e, output row + j
+    // lane, register e of (j, t) <-> row m0 + 16 t + 4 kg + e of A, output r0 + V li + j
     const void *bias0 = p.f.bias[0], *bias1 = p.f.bias[1];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         if (t > 0) __syncthreads();
-        if (16 * t >= s.m) break;
+        if (m0 + 16 * t >= s.m) break;
 #pragma unroll
         for (int l = 0; l < NL; ++l)
 #pragma unroll
@@ -250,7 +263,7 @@ __global__ __launch_bounds__(64 * SK_NW) void skinny_forward_kernel(SkinnyForwar
                     red[((wave * NL + l) * 16 + 4 * kg + e) * ROWS + V * li + j] = acc[l][j][t][e];
         __syncthreads();
         for (int x = tid; x < 16 * ROWS; x += 64 * SK_NW) {
-            const int64_t i = 16 * t + x / ROWS, n = r0 + x % ROWS;
+            const int64_t i = m0 + 16 * t + x / ROWS, n = r0 + x % ROWS;
             if (i >= s.m || n >= s.d_out) continue;
             float z[NL];
 #pragma unroll
@@ -292,17 +305,21 @@ __global__ __launch_bounds__(256) void gather_rows_kernel(const T *A, const int3
 // f16's range; they are taken over the work group's own outputs and undone
 // before its sums leave.
 //
-// A work group (4 waves) owns 128 columns and up to BK_RANGE outputs of one
+// A work group (4 waves) owns 128 columns and a range of outputs of one
 // layer.  A lane's words of eight outputs hold an 8 x 8 block of codes: eight
 // MFMA operands (columns 8 li + j, j = 0..7) without any exchange.  dZ of the
-// range is formed once per group in LDS, from dY and the saved
-// pre-activations.  The groups' sums are added in range order by a second
+// range enters LDS once per group (formed from dY and the saved
+// pre-activations by a kernel before, where there is an activation).  The groups' sums are added in range order by a second
 // kernel, which also moves the columns back to their original order.
 // ---------------------------------------------------------------------------
-constexpr int BK_RANGE = 512, BK_COLS = 128, BK_ROWS = 16;
+constexpr int BK_COLS = 128, BK_RANGE = 512;   // columns, and outputs at most, of a work group
+constexpr int BK_MAX_M = 16;
 
 struct SkinnyBackward {
     FusedBackward f;
+    const void *dz[2];      // dZ of each layer [m][d_out]: dY itself, or formed in the workspace
+    int dz_bf16;
+    float *dzw;             // room for it: [layers][m][d_out] fp32
     float *part;            // [layers * splits][m][d_in]; NULL: one range, straight to dA
     int splits, range;      // ranges per layer, outputs per range (a multiple of 32)
     int64_t nwords;
@@ -326,12 +343,52 @@ __device__ __forceinline__ float finite_abs(float v) {
     return a < __builtin_inff() ? a : 0.f;
 }
 
+// dZ of every layer in fp32, and the bias gradients: 64 outputs per work
+// group, a wave every fourth row
+__global__ __launch_bounds__(256) void skinny_dz_kernel(SkinnyBackward p, int write) {
+    __shared__ float red[2][4][64];
+    const FusedShape &s = p.f.s;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t r = (int64_t)blockIdx.x * 64 + lane, rc = std::min(r, s.d_out - 1);
+    float sum[2] = {0.f, 0.f};
+    for (int ib = wave; ib < s.m; ib += 16) {
+        float dy[4], z[4], u[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int64_t o = std::min<int64_t>(ib + 4 * b, s.m - 1) * s.d_out + rc;
+            dy[b] = fz_ld(p.f.dY, o, s.in_bf16);
+            z[b] = p.f.pre[0] ? fz_ld(p.f.pre[0], o, s.in_bf16) : 0.f;
+            u[b] = s.layers == 2 ? fz_ld(p.f.pre[1], o, s.in_bf16) : 1.f;
+        }
+        fz_with_act(p.f.act, [&](auto act) {
+            constexpr int ACT = decltype(act)::value;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const float d0 = dy[b] * u[b] * fz_slope<ACT>(z[b]), d1 = dy[b] * fz_act<ACT>(z[b]);
+                const int64_t i = ib + 4 * b;
+                if (i >= s.m) break;
+                sum[0] += d0;
+                sum[1] += d1;
+                if (write && r < s.d_out) {
+                    p.dzw[i * s.d_out + r] = d0;
+                    if (s.layers == 2) p.dzw[(s.m + i) * s.d_out + r] = d1;
+                }
+            }
+        });
+    }
+    red[0][wave][lane] = sum[0];
+    red[1][wave][lane] = sum[1];
+    __syncthreads();
+    float *db = wave < s.layers ? p.f.dbias[wave & 1] : nullptr;
+    if (db && r < s.d_out) db[r] = red[wave & 1][0][lane] + red[wave & 1][1][lane] + red[wave & 1][2][lane] + red[wave & 1][3][lane];
+}
+
 template <int BITS, bool HI>
 __global__ __launch_bounds__(256) void skinny_backward_kernel(SkinnyBackward p) {
-    constexpr int AP = HI ? 2 : 1, LD = BK_RANGE + 8;
-    __shared__ __attribute__((aligned(16))) _Float16 dz[AP][BK_ROWS][LD];
-    __shared__ float red[4 * BK_ROWS * BK_COLS];   // also the bias sums' [4][BK_RANGE]
-    __shared__ float rowinv[BK_ROWS], gmax[8];
+    constexpr int AP = HI ? 2 : 1, LD = BK_RANGE + 8, PER = BK_RANGE / 64;
+    __shared__ __attribute__((aligned(16))) _Float16 dz[AP][16][LD];
+    __shared__ float red[4 * 16 * BK_COLS];
+    __shared__ float rowinv[16], gmax[8];
     const FusedShape &s = p.f.s;
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -342,119 +399,114 @@ __global__ __launch_bounds__(256) void skinny_backward_kernel(SkinnyBackward p) 
     const PackedLayer w = p.f.w[l];
     const int steps = (int)((rend - rb + 31) / 32);
 
-    // dZ of the range: wave w forms rows w, w + 4, ...
-    float bsum[BK_RANGE / 64] = {};
-    for (int i = wave; i < s.m; i += 4) {
-        float v[BK_RANGE / 64];
-        float mx = 0.f;
-#pragma unroll
-        for (int c = 0; c < BK_RANGE / 64; ++c) {
-            const int64_t r = rb + 64 * c + lane, o = i * s.d_out + r;
-            v[c] = 0.f;
-            if (r < rend) {
-                const float dy = fz_ld(p.f.dY, o, s.in_bf16);
-                const float z = p.f.pre[0] ? fz_ld(p.f.pre[0], o, s.in_bf16) : 0.f;
-                const float u = s.layers == 2 && l == 0 ? fz_ld(p.f.pre[1], o, s.in_bf16) : 1.f;
-                fz_with_act(p.f.act, [&](auto act) {
-                    constexpr int ACT = decltype(act)::value;
-                    v[c] = dy * u * (l == 1 ? fz_act<ACT>(z) : fz_slope<ACT>(z));
-                });
-            }
-            mx = fmaxf(mx, finite_abs(v[c]));
-            bsum[c] += v[c];
-        }
-        float mul, inv;
-        f16_scale(wave_max(mx), mul, inv);
-        if (lane == 0) rowinv[i] = inv;
-#pragma unroll
-        for (int c = 0; c < BK_RANGE / 64; ++c) {
-            float x = v[c] * mul;
-            asm("" : "+v"(x));   // (rounded to f16 from this value alone, both times)
-            const bool finite = fabsf(x) < __builtin_inff();   // (others only in the last part: see put_planes)
-            const _Float16 h = (_Float16)(finite || !HI ? x : 0.f);
-            dz[0][i][64 * c + lane] = h;
-            if (HI) dz[AP - 1][i][64 * c + lane] = (_Float16)(finite ? x - (float)h : x);
-        }
-    }
-    const bool bias = blockIdx.x == 0 && p.f.dbias[l];
-    if (bias) {
-#pragma unroll
-        for (int c = 0; c < BK_RANGE / 64; ++c) red[wave * BK_RANGE + 64 * c + lane] = bsum[c];
-    }
-    // the largest scale of each of the columns' groups, over the range
-    const int g0 = (int)(c0 / s.group), g1 = (int)(std::min<int64_t>(c0 + BK_COLS, s.d_in) - 1) / s.group;
-    for (int gi = g0 + wave; gi <= g1; gi += 4) {
-        float mx = 0.f;
-        for (int64_t r = rb + lane; r < rend; r += 64)
-            mx = fmaxf(mx, finite_abs(w.scales[(int64_t)gi * s.d_out + r]));
-        mx = wave_max(mx);
-        if (lane == 0) gmax[gi - g0] = mx;
-    }
-    __syncthreads();
-    if (bias) {
-        for (int x = tid; rb + x < rend; x += 256)
-            p.f.dbias[l][rb + x] = red[x] + red[BK_RANGE + x] + red[2 * BK_RANGE + x] + red[3 * BK_RANGE + x];
-    }
+    // this lane's columns k0 .. k0 + 7, their group and words
+    const int g0 = (int)(c0 / s.group), g1 = (int)((std::min<int64_t>(c0 + BK_COLS, s.d_in) - 1) / s.group);
     const int64_t k0 = c0 + 8 * li;
-    const int gi = std::min<int>((int)(k0 / s.group), g1);
-    float mul, inv;
-    f16_scale(gmax[gi - g0] * (float)((1 << BITS) - 1), mul, inv);
+    const int gi = std::min((int)(k0 / s.group), g1);
     const int64_t j0 = std::min((BITS * k0) >> 5, p.nwords - 1), j1 = std::min(j0 + 1, p.nwords - 1);
     const int sh = (int)((BITS * k0) & 31);
-
+    const unsigned *ql = w.Q + j0 * s.d_out + rb + 8 * kg, *qh = w.Q + j1 * s.d_out + rb + 8 * kg;
+    const float *sp = w.scales + (int64_t)gi * s.d_out + rb + 8 * kg, *zp = w.zeros + (int64_t)gi * s.d_out + rb + 8 * kg;
     struct Slot {
-        unsigned lo[8], hi[8];
-        float s[8], z[8];
+        u32x4 lo[2], hi[fz_two_words<BITS>() ? 2 : 1];
+        f32x4 s[2], z[2];
     };
     auto fetch = [&](int step, Slot &sl) {
-        const int64_t r = rb + 32 * step + 8 * kg;
-        if (p.wvec && r + 8 <= s.d_out) {
+        const int at = 32 * step;
+        if (p.wvec && rb + at + 32 <= s.d_out) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t at = r + 4 * h;
-                const u32x4 a = *(const u32x4 *)(w.Q + j0 * s.d_out + at);
-                const u32x4 b = fz_two_words<BITS>() ? *(const u32x4 *)(w.Q + j1 * s.d_out + at) : u32x4{0u, 0u, 0u, 0u};
-                const f32x4 sc = *(const f32x4 *)(w.scales + (int64_t)gi * s.d_out + at);
-                const f32x4 zp = *(const f32x4 *)(w.zeros + (int64_t)gi * s.d_out + at);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sl.lo[4 * h + e] = a[e];
-                    sl.hi[4 * h + e] = b[e];
-                    sl.s[4 * h + e] = sc[e];
-                    sl.z[4 * h + e] = zp[e];
-                }
+                sl.lo[h] = *(const u32x4 *)(ql + at + 4 * h);
+                if constexpr (fz_two_words<BITS>()) sl.hi[h] = *(const u32x4 *)(qh + at + 4 * h);
+                sl.s[h] = *(const f32x4 *)(sp + at + 4 * h);
+                sl.z[h] = *(const f32x4 *)(zp + at + 4 * h);
             }
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {   // (outputs past the end: dZ is 0)
-                const int64_t at = std::min<int64_t>(r + e, s.d_out - 1);
-                sl.lo[e] = w.Q[j0 * s.d_out + at];
-                sl.hi[e] = fz_two_words<BITS>() ? w.Q[j1 * s.d_out + at] : 0u;
-                sl.s[e] = w.scales[(int64_t)gi * s.d_out + at];
-                sl.z[e] = w.zeros[(int64_t)gi * s.d_out + at];
+                const int o = (int)(std::min<int64_t>(rb + at + 8 * kg + e, s.d_out - 1) - rb) - 8 * kg;
+                sl.lo[e >> 2][e & 3] = ql[o];
+                if constexpr (fz_two_words<BITS>()) sl.hi[e >> 2][e & 3] = qh[o];
+                sl.s[e >> 2][e & 3] = sp[o];
+                sl.z[e >> 2][e & 3] = zp[o];
             }
         }
     };
+    // the first steps' words travel while dZ is formed
+    Slot sl[2];
+    fetch(std::min(wave, steps - 1), sl[0]);
+    fetch(std::min(wave + 4, steps - 1), sl[1]);
+
+    // dZ of the range in f16: wave w takes rows w, w + 4, ... , all loads in
+    // flight together
+    {
+        float v[4][PER];
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int c = 0; c < PER; ++c) {
+                const int64_t r = std::min<int64_t>(rb + 64 * c + lane, s.d_out - 1);
+                v[b][c] = fz_ld(p.dz[l], std::min<int64_t>(wave + 4 * b, s.m - 1) * s.d_out + r, p.dz_bf16);
+            }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int i = wave + 4 * b;
+            if (i >= s.m) break;
+            float mx = 0.f;
+#pragma unroll
+            for (int c = 0; c < PER; ++c) {
+                if (rb + 64 * c + lane >= rend) v[b][c] = 0.f;
+                mx = fmaxf(mx, finite_abs(v[b][c]));
+            }
+            float mul, inv;
+            f16_scale(wave_max(mx), mul, inv);
+            if (lane == 0) rowinv[i] = inv;
+#pragma unroll
+            for (int c = 0; c < PER; ++c) {
+                float x = v[b][c] * mul;
+                asm("" : "+v"(x));   // (rounded to f16 from this value alone, both times)
+                const bool finite = fabsf(x) < __builtin_inff();   // (others only in the last part: see put_planes)
+                const _Float16 h = (_Float16)(finite || !HI ? x : 0.f);
+                dz[0][i][64 * c + lane] = h;
+                if (HI) dz[AP - 1][i][64 * c + lane] = (_Float16)(finite ? x - (float)h : x);
+            }
+        }
+    }
+    // the largest scale of each of the columns' groups, over the range
+    for (int gq = g0 + wave; gq <= g1; gq += 4) {
+        float mx = 0.f;
+#pragma unroll
+        for (int c = 0; c < PER; ++c) {
+            const int64_t r = std::min<int64_t>(rb + 64 * c + lane, rend - 1);
+            mx = fmaxf(mx, finite_abs(w.scales[(int64_t)gq * s.d_out + r]));
+        }
+        mx = wave_max(mx);
+        if (lane == 0) gmax[gq - g0] = mx;
+    }
+    __syncthreads();
+    float mul, inv;
+    f16_scale(gmax[gi - g0] * (float)((1 << BITS) - 1), mul, inv);
+
     f32x4 acc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto use = [&](int step, const Slot &sl) {
         const f16x8 a0 = *(const f16x8 *)&dz[0][li][32 * step + 8 * kg];
-        f16x8 a1 = a0;
-        if (HI) a1 = *(const f16x8 *)&dz[AP - 1][li][32 * step + 8 * kg];
+        const f16x8 a1 = *(const f16x8 *)&dz[AP - 1][li][32 * step + 8 * kg];
         Codes8<BITS> c[8];
         float sc[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            c[e] = fz_codes8<BITS>(sl.lo[e], sl.hi[e], sh);
-            sc[e] = sl.s[e] * mul;
+            constexpr int H = fz_two_words<BITS>() ? 1 : 0;
+            c[e] = fz_codes8<BITS>(sl.lo[e >> 2][e & 3], H ? sl.hi[(e >> 2) & H][e & 3] : 0u, sh);
+            sc[e] = sl.s[e >> 2][e & 3] * mul;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             f16x8 h, r;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float x = (c[e].at(j) - sl.z[e]) * sc[e];
+                float x = (c[e].at(j) - sl.z[e >> 2][e & 3]) * sc[e];
                 if (HI) asm("" : "+v"(x));
                 h[e] = (_Float16)x;
                 if (HI) r[e] = (_Float16)(x - (float)h[e]);
@@ -466,9 +518,6 @@ __global__ __launch_bounds__(256) void skinny_backward_kernel(SkinnyBackward p) 
             acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, h, acc[j], 0, 0, 0);
         }
     };
-    Slot sl[2];
-    if (wave < steps) fetch(wave, sl[0]);
-    if (wave + 4 < steps) fetch(wave + 4, sl[1]);
     for (int step = wave; step < steps; step += 8) {
         use(step, sl[0]);
         if (step + 8 < steps) fetch(step + 8, sl[0]);
@@ -477,23 +526,19 @@ __global__ __launch_bounds__(256) void skinny_backward_kernel(SkinnyBackward p) 
             if (step + 12 < steps) fetch(step + 12, sl[1]);
         }
     }
-    __syncthreads();   // (the bias sums have been read)
     // lane, register e of j <-> row 4 kg + e, column k0 + j
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int i = 4 * kg + e;
-        if (i < s.m) {
-            const float f = rowinv[i];
+        const float f = i < s.m ? rowinv[i] : 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) red[(wave * BK_ROWS + i) * BK_COLS + 8 * li + j] = acc[j][e] * f * inv;
-        }
+        for (int j = 0; j < 8; ++j) red[(wave * 16 + i) * BK_COLS + 8 * li + j] = acc[j][e] * f * inv;
     }
     __syncthreads();
     for (int x = tid; x < (int)s.m * BK_COLS; x += 256) {
         const int64_t i = x / BK_COLS, k = c0 + x % BK_COLS;
         if (k >= s.d_in) continue;
-        const float v = red[x] + red[BK_ROWS * BK_COLS + x] + red[2 * BK_ROWS * BK_COLS + x] +
-                        red[3 * BK_ROWS * BK_COLS + x];
+        const float v = red[x] + red[16 * BK_COLS + x] + red[2 * 16 * BK_COLS + x] + red[3 * 16 * BK_COLS + x];
         if (p.part)
             p.part[(blockIdx.y * s.m + i) * s.d_in + k] = v;
         else
@@ -527,26 +572,28 @@ void backward_ranges(const FusedShape &s, int &splits, int &range) {
 
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-template <int BITS, int V, int NL, bool HALF>
+template <int BITS, int V, int NL, int CH>
 void launch_forward_k(const SkinnyForward &p, hipStream_t st) {
-    const dim3 grid((unsigned)p.tiles), block(64 * SK_NW);
+    const dim3 grid((unsigned)p.tiles, p.f.s.m > 16 ? (unsigned)cdiv(p.f.s.m, 64) : 1u), block(64 * SK_NW);
     if (p.f.s.m > 16) {
-        if constexpr (V * NL <= 2) skinny_forward_kernel<BITS, V, 4, NL, false, HALF><<<grid, block, 0, st>>>(p);
+        if constexpr (V * NL <= 2) skinny_forward_kernel<BITS, V, 4, NL, false, CH><<<grid, block, 0, st>>>(p);
     } else if (p.f.s.in_bf16) {
-        skinny_forward_kernel<BITS, V, 1, NL, false, HALF><<<grid, block, 0, st>>>(p);
+        skinny_forward_kernel<BITS, V, 1, NL, false, CH><<<grid, block, 0, st>>>(p);
     } else {
-        if constexpr (V == 1) skinny_forward_kernel<BITS, V, 1, NL, true, HALF><<<grid, block, 0, st>>>(p);
+        if constexpr (V == 1) skinny_forward_kernel<BITS, V, 1, NL, true, CH><<<grid, block, 0, st>>>(p);
     }
 }
 
 template <int BITS, int NL>
 hipError_t launch_forward(const SkinnyForward &p, int v, hipStream_t st) {
+    // whole chunks of four units, each in one group
+    const bool four = p.gs % 8 == 0 && p.nunits % 4 == 0;
     if (p.gs % 2 == 1)
-        launch_forward_k<BITS, 1, NL, true>(p, st);
+        launch_forward_k<BITS, 1, NL, 0>(p, st);
     else if (v == 2)
-        launch_forward_k<BITS, 2, NL, false>(p, st);
+        four ? launch_forward_k<BITS, 2, NL, 4>(p, st) : launch_forward_k<BITS, 2, NL, 1>(p, st);
     else
-        launch_forward_k<BITS, 1, NL, false>(p, st);
+        four ? launch_forward_k<BITS, 1, NL, 4>(p, st) : launch_forward_k<BITS, 1, NL, 1>(p, st);
     return hipGetLastError();
 }
 template <int BITS>
@@ -565,7 +612,7 @@ void launch_backward(const SkinnyBackward &p, hipStream_t st) {
 
 }  // namespace
 
-bool skinny_forward_takes(const FusedShape &s) { return s.m <= (s.in_bf16 ? 64 : 16); }
+bool skinny_forward_takes(const FusedShape &s) { return s.m <= (s.in_bf16 ? SK_MAX_M : 16); }
 
 size_t skinny_forward_ws(const FusedShape &s) {
     return align256((size_t)(s.m * cdiv(s.d_in, 32) * 32) * (s.in_bf16 ? 2 : 4));   // gathered rows
@@ -610,32 +657,52 @@ hipError_t skinny_forward_launch(const FusedForward &a, hipStream_t st) {
     return hipErrorInvalidValue;
 }
 
-bool skinny_backward_takes(const FusedShape &s) { return s.m <= BK_ROWS; }
+// (at 17 rows the dense form takes 35 us at 4096 x 4096, a second row tile here 33, a third 39)
+bool skinny_backward_takes(const FusedShape &s) { return s.m <= BK_MAX_M; }
 
-size_t skinny_backward_ws(const FusedShape &s) {
+struct SkinnyBackwardWs {
+    size_t part, bytes;   // offset of the ranges' sums behind dZ
+};
+SkinnyBackwardWs skinny_backward_layout(const FusedShape &s) {
     int splits, range;
     backward_ranges(s, splits, range);
-    return splits * s.layers > 1 ? align256((size_t)(splits * s.layers) * s.m * s.d_in * sizeof(float)) : 0;
+    SkinnyBackwardWs w;
+    w.part = align256((size_t)(s.layers * s.m * s.d_out) * sizeof(float));
+    w.bytes = w.part + (splits * s.layers > 1 ? align256((size_t)(splits * s.layers) * s.m * s.d_in * sizeof(float)) : 0);
+    return w;
 }
+size_t skinny_backward_ws(const FusedShape &s) { return skinny_backward_layout(s).bytes; }
 
 hipError_t skinny_backward_launch(const FusedBackward &a, hipStream_t st) {
     const FusedShape &s = a.s;
+    const SkinnyBackwardWs wl = skinny_backward_layout(s);
     SkinnyBackward p{};
     p.f = a;
-    if (s.layers == 1 && a.act == 0) p.f.pre[0] = nullptr;
+    const bool form = s.layers == 2 || a.act != 0;
+    if (!form) p.f.pre[0] = nullptr;
+    p.dzw = (float *)a.ws;
+    p.dz[0] = form ? (const void *)p.dzw : a.dY;
+    p.dz[1] = p.dzw + s.m * s.d_out;
+    p.dz_bf16 = !form && s.in_bf16;
     backward_ranges(s, p.splits, p.range);
-    p.part = p.splits * s.layers > 1 ? (float *)a.ws : nullptr;
+    p.part = p.splits * s.layers > 1 ? (float *)(a.ws + wl.part) : nullptr;
     p.nwords = cdiv(s.bits * s.d_in, 32);
     p.wvec = s.d_out % 4 == 0;
     for (int l = 0; l < s.layers; ++l)
         p.wvec = p.wvec && aligned(a.w[l].Q, 16) && aligned(a.w[l].scales, 16) && aligned(a.w[l].zeros, 16);
+    hipError_t e = hipSuccess;
+    if (form || a.dbias[0] || a.dbias[1]) {
+        skinny_dz_kernel<<<(unsigned)cdiv(s.d_out, 64), 256, 0, st>>>(p, form);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     switch (s.bits) {
         case 2: launch_backward<2>(p, st); break;
         case 3: launch_backward<3>(p, st); break;
         case 4: launch_backward<4>(p, st); break;
         case 8: launch_backward<8>(p, st); break;
     }
-    const hipError_t e = hipGetLastError();
+    e = hipGetLastError();
     if (e != hipSuccess || !p.part) return e;
     skinny_backward_reduce_kernel<<<dim3((unsigned)cdiv(s.d_in, 256), (unsigned)s.m), 256, 0, st>>>(p);
     return hipGetLastError();
