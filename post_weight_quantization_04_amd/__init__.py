@@ -166,9 +166,15 @@ def _check(status: int) -> None:
         raise GptqError(status, _lib().gptq_last_error().decode(errors="replace"))
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch  # memory and streams only
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch  # memory and streams only
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream_ptr(stream=None) -> int:
@@ -442,14 +448,15 @@ class _FusedCall:
             self.stream = stream.cuda_stream
             self.guard = torch.cuda.stream(stream)
         else:
-            self.stream = torch.cuda.current_stream(device).cuda_stream
+            # (the current stream's handle without a Stream object around it)
+            self.stream = torch._C._cuda_getCurrentRawStream(device.index)
             if device.index != torch.cuda.current_device():
                 self.guard = torch.cuda.device(device)
         self.given_ws = workspace
         if workspace is not None:
             _operand(workspace, "workspace", workspace.dtype, workspace.shape, device)
-        if torch.is_grad_enabled():
-            self.no_grad(x, q.scales, q.zeros)
+        if torch.is_grad_enabled() and (x.requires_grad or q.scales.requires_grad or q.zeros.requires_grad):
+            self.no_grad()
 
     def layer(self, q):
         """A packed layer's pointers (codes, scales, zero points)."""
@@ -464,22 +471,21 @@ class _FusedCall:
             raise ValueError("the layers must have the same sizes, bits and group_size")
         if up.act_order != gate.act_order or (up.act_order and up.perm.data_ptr() != self.perm):
             raise ValueError("the layers must share one perm (quantize_layers gives them one)")
-        if _torch().is_grad_enabled():
-            self.no_grad(up.scales, up.zeros)
+        if _torch().is_grad_enabled() and (up.scales.requires_grad or up.zeros.requires_grad):
+            self.no_grad()
 
     def take(self, t, name, dtype, shape):
         """An optional operand's pointer."""
         if t is None:
             return None
-        if _torch().is_grad_enabled():
-            self.no_grad(t)
+        if _torch().is_grad_enabled() and getattr(t, "requires_grad", False):
+            self.no_grad()
         return _operand(t, name, dtype, shape, self.device)
 
     @staticmethod
-    def no_grad(*tensors):
-        if any(t.requires_grad for t in tensors):
-            raise ValueError("autograd does not see through the fused products: call them under torch.no_grad() (or "
-                             "inside a torch.autograd.Function) and their _backward calls for the gradients")
+    def no_grad():
+        raise ValueError("autograd does not see through the fused products: call them under torch.no_grad() (or "
+                         "inside a torch.autograd.Function) and their _backward calls for the gradients")
 
     def empty(self, shape, dtype=None):
         return _torch().empty(shape, dtype=dtype or self.out_dtype, device=self.device)

@@ -27,6 +27,30 @@ __device__ __forceinline__ f32x4 fz_ld4(const void *p, int64_t i, int bf16) {
     return f32x4{__builtin_bit_cast(float, u[0] << 16), __builtin_bit_cast(float, u[0] & 0xffff0000u),
                  __builtin_bit_cast(float, u[1] << 16), __builtin_bit_cast(float, u[1] & 0xffff0000u)};
 }
+// eight consecutive values, element 0 aligned to eight
+__device__ __forceinline__ void fz_ld8(const void *p, int64_t i, int bf16, float (&v)[8]) {
+    if (bf16) {
+        const u32x4 u = *(const u32x4 *)((const uint16_t *)p + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __builtin_bit_cast(float, u[e] << 16);
+            v[2 * e + 1] = __builtin_bit_cast(float, u[e] & 0xffff0000u);
+        }
+    } else {
+        const f32x4 a = *(const f32x4 *)((const float *)p + i), b = *(const f32x4 *)((const float *)p + i + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = a[e];
+            v[4 + e] = b[e];
+        }
+    }
+}
+// k / g for k < 2^24, with inv = 1.f / g
+__device__ __forceinline__ int fz_div(int k, int g, float inv) {
+    int q = (int)((float)k * inv);
+    q -= q * g > k;
+    return q + ((q + 1) * g <= k);
+}
 __device__ __forceinline__ unsigned fz_pack_bf16(float a, float b) {
     const fz_bf16x2 p = {(__bf16)a, (__bf16)b};
     return __builtin_bit_cast(unsigned, p);

@@ -31,8 +31,7 @@ namespace {
 
 constexpr int GK = 32;                    // contraction elements per stage
 constexpr int64_t DENSE_ROWS = 16384;     // activation rows per pass (bounds the workspace)
-constexpr int DZ_ROWS = 16;                // rows of dZ formed by one work group
-constexpr int BIAS_ROWS = 64;             // ... when it also sums them for a bias gradient of many rows
+constexpr int DZ_ROWS = 16, DZ_ROWS_MANY = 64;   // rows of dZ formed (and summed) by one work group
 
 // 2^-e for a positive finite v in [2^e, 2^(e+1)) times 2^14, as a factor and
 // its inverse (both normal); 1 for 0
@@ -98,13 +97,6 @@ __device__ __forceinline__ void put_planes(uint16_t *out, int64_t plane, int pla
 // ---------------------------------------------------------------------------
 // forward operands: rows of A (gathered into processing order), weights [n][k]
 // ---------------------------------------------------------------------------
-// Work group b's row: two rows that share a 128-byte line of the operand go to
-// groups of one XCD (groups go round the 8 XCDs in turn), so that its L2
-// writes whole lines.
-__device__ __forceinline__ int64_t paired_row(int64_t b, int64_t m) {
-    return b < m / 16 * 16 ? b / 16 * 16 + b % 8 * 2 + b / 8 % 2 : b;
-}
-
 struct ForwardPrep {
     const void *A;
     int a_bf16, vec;            // vec: whole aligned 16-byte pieces
@@ -113,7 +105,7 @@ struct ForwardPrep {
     uint16_t *A16;              // rows [m], contraction [planes_a][kp]
     int planes_a;
     float *fa;                  // [m] inverse row factors
-    int in_lds;                 // the row fits the launch's LDS
+    int pairs;                  // gather from two bf16 rows staged in the launch's LDS
     PackedLayer w[2];
     int64_t d_out, nwords;
     int g, ngroups, layers;
@@ -124,46 +116,72 @@ struct ForwardPrep {
     int kchunks;
 };
 
-__device__ void prep_row(const ForwardPrep &p, int64_t i, char *lds) {
-    const int tid = threadIdx.x;
-    const int esize = p.a_bf16 ? 2 : 4;
-    const char *row = (const char *)p.A + i * p.d_in * esize;
-    float mx = 0.f;
+// Two rows i, i + 1 (which share 128-byte lines of the operand).
+__device__ void prep_rows(const ForwardPrep &p, int64_t i, char *lds) {
+    const int tid = threadIdx.x, rows = i + 1 < p.m ? 2 : 1;
+    const int d = (int)p.d_in, kp = (int)p.kp, es = p.a_bf16 ? 2 : 4;
+    const int64_t ktot = (int64_t)p.planes_a * p.kp;
+    const char *row[2] = {(const char *)p.A + i * d * es, (const char *)p.A + (i + rows - 1) * d * es};
+    float mx[2] = {0.f, 0.f}, mul[2], inv[2];
     if (p.vec) {
-        const int np = (int)(p.d_in * esize / 16);
-        for (int q = tid; q < np; q += 256) {
-            const u32x4 u = ((const u32x4 *)row)[q];
-            if (p.in_lds) ((u32x4 *)lds)[q] = u;
+        for (int k = 8 * tid; k < d; k += 8 * 256) {
+            float v[2][8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const unsigned x = u[e];   // (the compiler's bit cast of a vector element itself takes element 0)
-                if (p.a_bf16) {
-                    mx = fmaxf(mx, finite_abs(__builtin_bit_cast(float, x << 16)));
-                    mx = fmaxf(mx, finite_abs(__builtin_bit_cast(float, x & 0xffff0000u)));
-                } else {
-                    mx = fmaxf(mx, finite_abs(__builtin_bit_cast(float, x)));
-                }
+            for (int r = 0; r < 2; ++r) fz_ld8(row[r], k, p.a_bf16, v[r]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mx[r] = fmaxf(mx[r], finite_abs(v[r][e]));
+            if (p.pairs) {   // both rows' bf16 values of a column in one word
+                u32x4 w[2];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    w[e >> 2][e & 3] = (__builtin_bit_cast(unsigned, +v[0][e]) >> 16) |
+                                       (__builtin_bit_cast(unsigned, +v[1][e]) & 0xffff0000u);
+                *(u32x4 *)(lds + 4 * k) = w[0];
+                *(u32x4 *)(lds + 4 * k + 16) = w[1];
             }
         }
     } else {
-        for (int64_t k = tid; k < p.d_in; k += 256) {
-            const float v = fz_ld(row, k, p.a_bf16);
-            if (p.in_lds) fz_st(lds, k, v, p.a_bf16);
-            mx = fmaxf(mx, finite_abs(v));
-        }
-    }
-    float mul, inv;
-    pow2_scale(block_max(mx), mul, inv);   // (its barriers also cover the staged row)
-    if (tid == 0) p.fa[i] = inv;
-    const void *src = p.in_lds ? (const void *)lds : (const void *)row;
-    for (int64_t k0 = 8 * tid; k0 < p.kp; k0 += 8 * 256) {
-        float v[8];
+        for (int k = tid; k < d; k += 256)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t k = k0 + e;
-            v[e] = k < p.d_in ? fz_ld(src, p.perm ? (int64_t)p.perm[k] : k, p.a_bf16) * mul : 0.f;
+            for (int r = 0; r < 2; ++r) mx[r] = fmaxf(mx[r], finite_abs(fz_ld(row[r], k, p.a_bf16)));
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        pow2_scale(block_max(mx[r]), mul[r], inv[r]);   // (its barriers also cover the staged rows)
+        if (tid == 0 && r < rows) p.fa[i + r] = inv[r];
+    }
+    for (int k0 = 8 * tid; k0 < kp; k0 += 8 * 256) {
+        float v[2][8];
+        if (p.pairs && k0 < d) {
+            int c[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c[e] = p.perm[k0 + e];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const unsigned w = *(const unsigned *)(lds + 4 * c[e]);
+                v[0][e] = fz_bf16((uint16_t)w);
+                v[1][e] = fz_bf16((uint16_t)(w >> 16));
+            }
+        } else if (p.vec && !p.perm && k0 < d) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) fz_ld8(row[r], k0, p.a_bf16, v[r]);   // (from the cache)
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int k = k0 + e, c = k < d ? (p.perm ? p.perm[k] : k) : -1;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) v[r][e] = c < 0 ? 0.f : fz_ld(row[r], c, p.a_bf16);
+            }
         }
-        put_planes(p.A16 + operand_at(i, k0, p.planes_a * p.kp), p.kp * 256, p.planes_a, p.a_bf16, v);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            if (r >= rows) break;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[r][e] *= mul[r];
+            put_planes(p.A16 + operand_at(i + r, k0, ktot), p.kp * 256, p.planes_a, p.a_bf16, v[r]);
+        }
     }
 }
 
@@ -172,50 +190,60 @@ __device__ void prep_row(const ForwardPrep &p, int64_t i, char *lds) {
 // side by side and writes whole 128-byte lines.
 constexpr int FW_ROWS = 32, FW_K = 1024;
 template <int BITS>
-__device__ void prep_weights(const ForwardPrep &p, int64_t b, float *lds) {
-    const int tid = threadIdx.x;
-    const int64_t tiles = cdiv(p.d_out, FW_ROWS);
-    const int kc = (int)(b % p.kchunks);
-    const int64_t t = b / p.kchunks;
-    const int l = (int)(t / tiles);
-    const int64_t r0 = (t % tiles) * FW_ROWS;
+__device__ void prep_weights(const ForwardPrep &p, unsigned b, float *lds) {
+    const int tid = threadIdx.x, d_out = (int)p.d_out, d_in = (int)p.d_in;
+    const unsigned tiles = (unsigned)((d_out + FW_ROWS - 1) / FW_ROWS), t = b / (unsigned)p.kchunks;
+    const int kc = (int)(b - t * (unsigned)p.kchunks), l = t >= tiles;
+    const int r0 = (int)(t - l * tiles) * FW_ROWS;
     const PackedLayer w = p.w[l];
     // the rows' largest scales, over all groups
     float mx = 0.f;
     {
-        const int64_t r = std::min<int64_t>(r0 + (tid & 31), p.d_out - 1);
-        for (int gi = tid >> 5; gi < p.ngroups; gi += 8) mx = fmaxf(mx, finite_abs(w.scales[(int64_t)gi * p.d_out + r]));
+        const float *sc = w.scales + std::min(r0 + (tid & 31), d_out - 1);
+        for (int gi = tid >> 5; gi < p.ngroups; gi += 8) mx = fmaxf(mx, finite_abs(sc[(int64_t)gi * d_out]));
         lds[tid] = mx;
     }
     __syncthreads();
     const int wave = tid >> 6, lane = tid & 63;
     const int rl = 8 * wave + (lane & 7);       // row within the tile
-    const int64_t r = std::min<int64_t>(r0 + rl, p.d_out - 1);
+    const int r = std::min(r0 + rl, d_out - 1);
     mx = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) mx = fmaxf(mx, lds[32 * e + rl]);
     float mul, inv;
     pow2_scale(mx * (float)((1 << BITS) - 1), mul, inv);
-    if (kc == 0 && lane < 8 && r0 + rl < p.d_out) p.fw[l * p.d_out + r] = inv;
-    if (r0 + rl >= p.d_out) return;
-    uint16_t *out = p.W16 + l * pad_tile(p.d_out) * p.planes_w * p.kp;
-    const int64_t kend = std::min<int64_t>(p.kp, (int64_t)(kc + 1) * FW_K);
-    for (int64_t k0 = (int64_t)kc * FW_K + 8 * (lane >> 3); k0 < kend; k0 += 64) {
+    if (kc == 0 && lane < 8 && r0 + rl < d_out) p.fw[l * d_out + r] = inv;
+    if (r0 + rl >= d_out) return;
+    const float ginv = 1.f / (float)p.g;
+    uint16_t *out = p.W16 + (int64_t)l * pad_tile(d_out) * p.planes_w * p.kp;
+    const int kend = std::min((int)p.kp, (kc + 1) * FW_K);
+    struct Block {
+        unsigned lo, hi;
+        float s, z;
+    };
+    auto load = [&](int k0) {   // (past d_in: the last words again, not used)
+        k0 = std::min(k0, (d_in - 1) & ~7);
+        const int64_t j = (BITS * k0) >> 5;
+        const int64_t gi = fz_div(k0, p.g, ginv);
+        Block x;
+        x.lo = w.Q[j * d_out + r];
+        x.hi = fz_two_words<BITS>() ? w.Q[std::min(j + 1, p.nwords - 1) * d_out + r] : 0u;
+        x.s = w.scales[gi * d_out + r] * mul;
+        x.z = w.zeros[gi * d_out + r];
+        return x;
+    };
+    // two blocks ahead of the one that is written
+    const int first = kc * FW_K + 8 * (lane >> 3);
+    Block x0 = load(first), x1 = load(first + 64);
+    for (int k0 = first; k0 < kend; k0 += 64) {
+        const Block x2 = load(k0 + 128);
         float v[8];
-        if (k0 < p.d_in) {
-            const int64_t pos = BITS * k0, j = pos >> 5;
-            const unsigned lo = w.Q[j * p.d_out + r];
-            const unsigned hi = fz_two_words<BITS>() ? w.Q[std::min<int64_t>(j + 1, p.nwords - 1) * p.d_out + r] : 0u;
-            const Codes8<BITS> c = fz_codes8<BITS>(lo, hi, (int)(pos & 31));
-            const int64_t gi = k0 / p.g;
-            const float s = w.scales[gi * p.d_out + r] * mul, z = w.zeros[gi * p.d_out + r];
+        const Codes8<BITS> c = fz_codes8<BITS>(x0.lo, x0.hi, (BITS * k0) & 31);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = k0 + e < p.d_in ? (c.at(e) - z) * s : 0.f;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        }
+        for (int e = 0; e < 8; ++e) v[e] = k0 + e < d_in ? (c.at(e) - x0.z) * x0.s : 0.f;
         put_planes(out + operand_at(r, k0, p.planes_w * p.kp), p.kp * 256, p.planes_w, 0, v);
+        x0 = x1;
+        x1 = x2;
     }
 }
 
@@ -223,9 +251,9 @@ template <int BITS>
 __global__ __launch_bounds__(256) void forward_prep_kernel(ForwardPrep p) {
     extern __shared__ __attribute__((aligned(16))) char dyn[];
     if ((int64_t)blockIdx.x < p.row_blocks)
-        prep_row(p, paired_row(blockIdx.x, p.m), dyn);
+        prep_rows(p, 2 * (int64_t)blockIdx.x, dyn);
     else
-        prep_weights<BITS>(p, (int64_t)blockIdx.x - p.row_blocks, (float *)dyn);
+        prep_weights<BITS>(p, (unsigned)((int64_t)blockIdx.x - p.row_blocks), (float *)dyn);
 }
 
 // ---------------------------------------------------------------------------
@@ -241,7 +269,7 @@ struct BackwardPrep {
     uint16_t *D16;              // rows [m], contraction [planes_a][layers][kp]
     int planes_a;
     float *fa;                  // [m] row factors (mul), then [m] their inverses
-    float *bias_part;           // [row blocks][layers][d_out], or NULL
+    float *bias_part;           // [row blocks][layers][d_out], or NULL: no bias gradients
     PackedLayer w[2];
     const int32_t *perm;
     int64_t d_in, nwords;
@@ -250,46 +278,117 @@ struct BackwardPrep {
     uint16_t *W16;              // rows [d_in], contraction [planes_w][layers][kp]
     int planes_w;
     float *fw;                  // [d_in] inverse factors, original order
-    int dz_rows;                // rows of a dZ tile
+    int dz_rows;                // rows of a dZ tile (bias gradients)
     int64_t dz_blocks, dz_cols; // dZ tiles, then weight tiles
 };
 
-// First pass: a bound on every row's |dZ| (one work group per row: |act'| and
-// |act(z) / z| are below 1.13 and 1), and every group's largest scale
-__global__ __launch_bounds__(256) void backward_range_kernel(BackwardPrep p) {
-    const int tid = threadIdx.x;
-    float mul, inv;
-    if ((int64_t)blockIdx.x < p.m) {
-        const int64_t i = blockIdx.x, o = i * p.d_out;
-        float md = 0.f, mg = 0.f, mu = 0.f;
-        auto fold = [&](float &mx, const void *x) {
-            if (p.vec) {
-                for (int64_t r = 4 * tid; r < p.d_out; r += 4 * 256) {
-                    const f32x4 v = fz_ld4(x, o + r, p.bf16);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mx = fmaxf(mx, finite_abs(v[e]));
-                }
-            } else {
-                for (int64_t r = tid; r < p.d_out; r += 256) mx = fmaxf(mx, finite_abs(fz_ld(x, o + r, p.bf16)));
+// What bounds a row's |dZ| (|act'| and |act(z) / z| are below 1.13 and 1),
+// from its largest finite |dY|, |G| and |U|
+__device__ __forceinline__ void row_scale(const BackwardPrep &p, int64_t i, float &mul, float &inv) {
+    const int64_t o = i * p.d_out;
+    float md = 0.f, mg = 0.f, mu = 0.f;
+    if (p.vec) {
+        for (int r = 8 * threadIdx.x; r < p.d_out; r += 8 * 256) {
+            float d[8], g[8], u[8];
+            fz_ld8(p.dY, o + r, p.bf16, d);
+            if (p.layers == 2) {
+                fz_ld8(p.pre[0], o + r, p.bf16, g);
+                fz_ld8(p.pre[1], o + r, p.bf16, u);
             }
-        };
-        fold(md, p.dY);
-        if (p.layers == 2) {
-            fold(mg, p.pre[0]);
-            fold(mu, p.pre[1]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                md = fmaxf(md, finite_abs(d[e]));
+                if (p.layers == 2) {
+                    mg = fmaxf(mg, finite_abs(g[e]));
+                    mu = fmaxf(mu, finite_abs(u[e]));
+                }
+            }
         }
-        md = block_max(md);
-        if (p.layers == 2) {
-            mg = block_max(mg);
-            mu = block_max(mu);
+    } else {
+        for (int r = threadIdx.x; r < p.d_out; r += 256) {
+            md = fmaxf(md, finite_abs(fz_ld(p.dY, o + r, p.bf16)));
+            if (p.layers == 2) {
+                mg = fmaxf(mg, finite_abs(fz_ld(p.pre[0], o + r, p.bf16)));
+                mu = fmaxf(mu, finite_abs(fz_ld(p.pre[1], o + r, p.bf16)));
+            }
         }
-        const float f = p.layers == 2 ? fmaxf(mg, 1.13f * mu) : (p.pre[0] ? 1.13f : 1.f);
-        // (an overflowing bound: the largest finite one)
-        pow2_scale(fminf(md * f, 3.0e38f), mul, inv);
+    }
+    md = block_max(md);
+    if (p.layers == 2) {
+        mg = block_max(mg);
+        mu = block_max(mu);
+    }
+    const float f = p.layers == 2 ? fmaxf(mg, 1.13f * mu) : (p.pre[0] ? 1.13f : 1.f);
+    // (an overflowing bound: the largest finite one)
+    pow2_scale(fminf(md * f, 3.0e38f), mul, inv);
+}
+
+// eight values of a row's inputs, zeros past the end
+__device__ __forceinline__ void load_row8(const BackwardPrep &p, const void *x, int64_t i, int64_t r0, float (&v)[8]) {
+    const int64_t o = i * p.d_out + r0;
+    if (p.vec && r0 < p.d_out) {
+        fz_ld8(x, o, p.bf16, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = r0 + e < p.d_out ? fz_ld(x, o + e, p.bf16) : 0.f;
+    }
+}
+
+// outputs r0 .. r0 + 7 of row i of dZ (of dG and dU), as operand planes; the
+// values themselves in d0 (and d1)
+__device__ __forceinline__ void form_dz8(const BackwardPrep &p, int64_t i, int64_t r0, float mul, float (&d0)[8],
+                                         float (&d1)[8]) {
+    const int64_t ktot = (int64_t)p.planes_a * p.layers * p.kp;
+    float d[8], z[8], u[8];
+    load_row8(p, p.dY, i, r0, d);
+    auto put = [&](int l, const float (&x)[8]) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = r0 + e < p.d_out ? x[e] * mul : 0.f;
+        put_planes(p.D16 + operand_at(i, l * p.kp + r0, ktot), p.layers * p.kp * 256, p.planes_a, 0, v);
+    };
+    if (p.layers == 2) {
+        load_row8(p, p.pre[0], i, r0, z);
+        load_row8(p, p.pre[1], i, r0, u);
+        fz_with_act(p.act, [&](auto act) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                d0[e] = d[e] * u[e] * fz_slope<decltype(act)::value>(z[e]);
+                d1[e] = d[e] * fz_act<decltype(act)::value>(z[e]);
+            }
+        });
+        put(1, d1);
+    } else if (p.act != 0) {
+        load_row8(p, p.pre[0], i, r0, z);
+        fz_with_act(p.act, [&](auto act) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d0[e] = d[e] * fz_slope<decltype(act)::value>(z[e]);
+        });
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d0[e] = d[e];
+    }
+    put(0, d0);
+}
+
+// First pass: every group's largest scale, and either whole rows of dZ (the
+// second sweep over a row finds it in the caches), or, where the second pass
+// also sums columns for bias gradients, the rows' factors alone.  (Gated pair
+// of 11008, 4096 rows: 88 us for the factors and 187 with the weights for a
+// second pass that reads everything again.)
+__global__ __launch_bounds__(256) void backward_rows_kernel(BackwardPrep p) {
+    const int tid = threadIdx.x;
+    if ((int64_t)blockIdx.x < p.m) {
+        const int64_t i = blockIdx.x;
+        float mul, inv;
+        row_scale(p, i, mul, inv);
         if (tid == 0) {
             p.fa[i] = mul;
             p.fa[p.m + i] = inv;
         }
+        if (p.bias_part) return;
+        float d0[8], d1[8];
+        for (int64_t r0 = 8 * tid; r0 < p.kp; r0 += 8 * 256) form_dz8(p, i, r0, mul, d0, d1);
     } else {
         const int gi = (int)((int64_t)blockIdx.x - p.m);
         float mx = 0.f;
@@ -301,78 +400,29 @@ __global__ __launch_bounds__(256) void backward_range_kernel(BackwardPrep p) {
     }
 }
 
-// dz_rows rows by 256 columns of dZ (of dG and dU): rounded to f16 planes, and the
-// columns' sums over the tile's rows when bias gradients are wanted
-__device__ void prep_dz(const BackwardPrep &p, int64_t b, float *lds) {
+// dz_rows rows by 256 columns of dZ (of dG and dU) with their columns' sums
+__device__ void prep_dz(const BackwardPrep &p, unsigned b, float *lds) {
     const int tid = threadIdx.x;
-    const int64_t cb = b % p.dz_cols, rb = b / p.dz_cols;
+    const unsigned rbu = b / (unsigned)p.dz_cols;
+    const int64_t rb = rbu, cb = b - rbu * (unsigned)p.dz_cols;
     const int64_t r0 = cb * 256 + 8 * (tid & 31);
     const int64_t ilast = std::min<int64_t>(p.m, (rb + 1) * p.dz_rows);
     float sum[2][8] = {};
-    auto load8 = [&](const void *x, int64_t o, float (&v)[8]) {
-        if (p.vec) {
-            if (r0 < p.d_out) {
-                const f32x4 a = fz_ld4(x, o, p.bf16), c = fz_ld4(x, o + 4, p.bf16);
+    if (r0 < p.kp)
+        for (int64_t i = rb * p.dz_rows + (tid >> 5); i < ilast; i += 8) {
+            float d0[8], d1[8] = {};
+            form_dz8(p, i, r0, p.fa[i], d0, d1);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = a[e];
-                    v[4 + e] = c[e];
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = 0.f;
+            for (int e = 0; e < 8; ++e) {
+                sum[0][e] += d0[e];
+                sum[1][e] += d1[e];
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = r0 + e < p.d_out ? fz_ld(x, o + e, p.bf16) : 0.f;
         }
-    };
-    auto put = [&](int l, int64_t i, const float (&d)[8], float mul) {
-        if (r0 >= p.kp) return;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[e] = r0 + e < p.d_out ? d[e] * mul : 0.f;
-            if (r0 + e < p.d_out) sum[l][e] += d[e];
-        }
-        put_planes(p.D16 + operand_at(i, l * p.kp + r0, p.planes_a * p.layers * p.kp), p.layers * p.kp * 256, p.planes_a,
-                   0, v);
-    };
-    for (int64_t i = rb * p.dz_rows + (tid >> 5); i < ilast; i += 8) {
-        const int64_t o = i * p.d_out + r0;
-        const float mul = p.fa[i];
-        float d[8], z[8], u[8];
-        load8(p.dY, o, d);
-        if (p.layers == 2) {
-            load8(p.pre[0], o, z);
-            load8(p.pre[1], o, u);
-            float dg[8], du[8];
-            fz_with_act(p.act, [&](auto act) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    dg[e] = d[e] * u[e] * fz_slope<decltype(act)::value>(z[e]);
-                    du[e] = d[e] * fz_act<decltype(act)::value>(z[e]);
-                }
-            });
-            put(0, i, dg, mul);
-            put(1, i, du, mul);
-        } else {
-            if (p.act != 0) {
-                load8(p.pre[0], o, z);
-                fz_with_act(p.act, [&](auto act) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) d[e] *= fz_slope<decltype(act)::value>(z[e]);
-                });
-            }
-            put(0, i, d, mul);
-        }
-    }
-    if (!p.bias_part) return;
     // the eight row lanes of a column, added in their order
     for (int l = 0; l < p.layers; ++l) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) lds[(tid >> 5) * 256 + 8 * (tid & 31) + e] = sum[l][e];
+        for (int e = 0; e < 8; ++e) lds[(tid >> 5) * 256 + 8 * (tid & 31) + e] = l ? sum[1][e] : sum[0][e];
         __syncthreads();
         float v = 0.f;
 #pragma unroll
@@ -387,17 +437,17 @@ __device__ void prep_dz(const BackwardPrep &p, int64_t b, float *lds) {
 // 128-byte lines, and eight consecutive columns are 512 contiguous bytes.
 constexpr int BW_ROWS = 128, BW_COLS = 128;
 template <int BITS>
-__device__ void prep_weights_t(const BackwardPrep &p, int64_t b) {
+__device__ void prep_weights_t(const BackwardPrep &p, unsigned b) {
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int64_t rtiles = cdiv(p.kp, BW_ROWS);
-    const int64_t ctiles = cdiv(p.d_in, BW_COLS);
-    const int l = (int)(b / (rtiles * ctiles));
-    const int64_t t = b % (rtiles * ctiles);
-    const int64_t r0 = (t % rtiles) * BW_ROWS + 32 * wave + 8 * (lane & 3);
-    const int64_t k0 = (t / rtiles) * BW_COLS + 8 * (lane >> 2);
+    const unsigned rtiles = (unsigned)((p.kp + BW_ROWS - 1) / BW_ROWS);
+    const unsigned ctiles = (unsigned)((p.d_in + BW_COLS - 1) / BW_COLS);
+    const unsigned tc = b / rtiles;
+    const int l = tc >= ctiles;
+    const int64_t r0 = (int64_t)(b - tc * rtiles) * BW_ROWS + 32 * wave + 8 * (lane & 3);
+    const int64_t k0 = (int64_t)(tc - l * ctiles) * BW_COLS + 8 * (lane >> 2);
     if (r0 >= p.kp || k0 >= p.d_in) return;
     const PackedLayer w = p.w[l];
-    const int64_t gi = k0 / p.g;
+    const int64_t gi = fz_div((int)k0, p.g, 1.f / (float)p.g);
     float mul, inv;
     pow2_scale(p.fg[gi] * (float)((1 << BITS) - 1), mul, inv);
     const int64_t pos = BITS * k0, j = pos >> 5, j1 = std::min<int64_t>(j + 1, p.nwords - 1);
@@ -454,7 +504,7 @@ __global__ __launch_bounds__(256) void backward_prep_kernel(BackwardPrep p) {
     if ((int64_t)blockIdx.x < p.dz_blocks)
         prep_dz(p, blockIdx.x, lds);
     else
-        prep_weights_t<BITS>(p, (int64_t)blockIdx.x - p.dz_blocks);
+        prep_weights_t<BITS>(p, (unsigned)((int64_t)blockIdx.x - p.dz_blocks));
 }
 
 // a bias gradient from its row blocks' sums, in their order; more: added to
@@ -806,9 +856,8 @@ ForwardWs forward_layout(const FusedShape &s, char *base) {
     return w;
 }
 
-// Few rows: enough work groups; many rows with a bias gradient: fewer partial
-// sums per column
-int dz_rows(int64_t m, bool bias) { return bias && m > 1024 ? BIAS_ROWS : DZ_ROWS; }
+// Few rows: enough work groups; many rows: fewer partial sums per column
+int dz_rows(int64_t m) { return m > 1024 ? DZ_ROWS_MANY : DZ_ROWS; }
 
 struct BackwardWs {
     float *fw, *fg, *fa, *part, *bias;
@@ -831,7 +880,7 @@ BackwardWs backward_layout(const FusedShape &s, char *base) {
     w.fa = l.take<float>(2 * w.rows);
     w.W16 = l.take<uint16_t>(pad_tile(s.d_in) * w.planes_w * s.layers * w.kp);
     w.D16 = l.take<uint16_t>(pad_tile(w.rows) * w.planes_a * s.layers * w.kp);
-    w.bias = l.take<float>(cdiv(w.rows, dz_rows(w.rows, true)) * s.layers * s.d_out);
+    w.bias = l.take<float>(cdiv(w.rows, dz_rows(w.rows)) * s.layers * s.d_out);
     w.part = l.take<float>(w.plan.nsplit > 1 ? w.plan.nsplit * w.rows * pad_quad(s.d_in) : 0);
     w.bytes = l.bytes;
     return w;
@@ -854,16 +903,30 @@ hipError_t launch_gemm(const Gemm &g, const Plan &p, hipStream_t st) {
     return g.layers == 2 ? launch_gemm<true>(g, p, st) : launch_gemm<false>(g, p, st);
 }
 
-constexpr size_t PREP_LDS_MAX = 128 * 1024;   // bytes of an activation row staged for its gather
+constexpr size_t PREP_LDS_MAX = 128 * 1024;   // bytes of two activation rows staged for their gather
 
 template <int BITS>
-hipError_t launch_forward_prep(const ForwardPrep &p, int64_t blocks, hipStream_t st) {
-    const size_t row = (size_t)p.d_in * (p.a_bf16 ? 2 : 4);
-    const size_t lds = std::max<size_t>(p.in_lds ? (row + 15) / 16 * 16 : 0, 1024);
-    if (lds > 64 * 1024) {   // above the default limit a launch needs the kernel's attribute
-        const hipError_t e = hipFuncSetAttribute((const void *)forward_prep_kernel<BITS>,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)PREP_LDS_MAX);
-        if (e != hipSuccess) return e;
+hipError_t launch_forward_prep(ForwardPrep p, int64_t blocks, hipStream_t st) {
+    // The rows' staging would take LDS from the weights' groups too (fewer of
+    // them per CU): beyond 16 KB they go in a launch of their own.
+    size_t lds = 1024;
+    if (p.pairs) {
+        const size_t rows = (size_t)p.d_in * 4;
+        if (rows > 16 * 1024) {
+            if (rows > 64 * 1024) {   // above the default limit a launch needs the kernel's attribute
+                const hipError_t e = hipFuncSetAttribute((const void *)forward_prep_kernel<BITS>,
+                                                         hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                         (int)PREP_LDS_MAX);
+                if (e != hipSuccess) return e;
+            }
+            forward_prep_kernel<BITS><<<(unsigned)p.row_blocks, 256, rows, st>>>(p);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess || blocks == p.row_blocks) return e;
+            blocks -= p.row_blocks;
+            p.row_blocks = 0;
+        } else {
+            lds = std::max(lds, rows);
+        }
     }
     forward_prep_kernel<BITS><<<(unsigned)blocks, 256, lds, st>>>(p);
     return hipGetLastError();
@@ -892,7 +955,7 @@ hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st) {
         p.A16 = w.A16;
         p.planes_a = w.planes_a;
         p.fa = w.fa;
-        p.in_lds = (size_t)s.d_in * (s.in_bf16 ? 2 : 4) <= PREP_LDS_MAX;
+        p.pairs = p.perm && p.vec && s.in_bf16 && (size_t)s.d_in * 4 <= PREP_LDS_MAX;
         for (int l = 0; l < s.layers; ++l) p.w[l] = a.w[l];
         p.d_out = s.d_out;
         p.nwords = cdiv(s.bits * s.d_in, 32);
@@ -902,10 +965,10 @@ hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st) {
         p.W16 = w.W16;
         p.planes_w = w.planes_w;
         p.fw = w.fw;
-        p.row_blocks = m;
+        p.row_blocks = cdiv(m, 2);
         p.kchunks = (int)cdiv(w.kp, FW_K);
         // the weights once, with the first rows
-        const int64_t blocks = m + (i0 == 0 ? s.layers * cdiv(s.d_out, FW_ROWS) * p.kchunks : 0);
+        const int64_t blocks = p.row_blocks + (i0 == 0 ? s.layers * cdiv(s.d_out, FW_ROWS) * p.kchunks : 0);
         hipError_t e = hipErrorInvalidValue;
         switch (s.bits) {
             case 2: e = launch_forward_prep<2>(p, blocks, st); break;
@@ -989,23 +1052,25 @@ hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st) {
         p.planes_w = w.planes_w;
         p.fw = w.fw;
         p.dz_cols = cdiv(w.kp, 256);
-        p.dz_rows = dz_rows(m, bias);
+        p.dz_rows = dz_rows(m);
         const int64_t row_blocks = cdiv(m, p.dz_rows);
-        p.dz_blocks = p.dz_cols * row_blocks;
+        p.dz_blocks = bias ? p.dz_cols * row_blocks : 0;
         // the groups' ranges and the weights once, with the first rows
-        backward_range_kernel<<<(unsigned)(m + (i0 == 0 ? s.ngroups : 0)), 256, 0, st>>>(p);
+        backward_rows_kernel<<<(unsigned)(m + (i0 == 0 ? s.ngroups : 0)), 256, 0, st>>>(p);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const int64_t blocks =
             p.dz_blocks + (i0 == 0 ? s.layers * cdiv(w.kp, BW_ROWS) * cdiv(s.d_in, BW_COLS) : 0);
-        switch (s.bits) {
-            case 2: backward_prep_kernel<2><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-            case 3: backward_prep_kernel<3><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-            case 4: backward_prep_kernel<4><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-            case 8: backward_prep_kernel<8><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+        if (blocks > 0) {
+            switch (s.bits) {
+                case 2: backward_prep_kernel<2><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+                case 3: backward_prep_kernel<3><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+                case 4: backward_prep_kernel<4><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+                case 8: backward_prep_kernel<8><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+            }
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
         }
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
         if (bias) {
             bias_reduce_kernel<<<dim3((unsigned)cdiv(s.d_out, 256), (unsigned)s.layers), 256, 0, st>>>(
                 w.bias, row_blocks, s.layers, s.d_out, a.dbias[0], a.dbias[1], i0 > 0);
