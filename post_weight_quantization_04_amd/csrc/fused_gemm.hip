@@ -48,15 +48,18 @@ __device__ __forceinline__ float finite_abs(float v) {
     return a < __builtin_inff() ? a : 0.f;   // NaN and infinities do not count
 }
 
-// largest of v over the work group's 256 threads
+// largest of v over the work group's NW waves
+template <int NW = 4>
 __device__ __forceinline__ float block_max(float v) {
-    __shared__ float red[4];
+    __shared__ float red[NW];
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v = fmaxf(v, red[w]);
+    return v;
 }
 
 // Operand layout: tiles of 256 rows, inside a tile stages of GK contraction
@@ -282,8 +285,14 @@ struct BackwardPrep {
     int64_t dz_blocks, dz_cols; // dZ tiles, then weight tiles
 };
 
-// What bounds a row's |dZ| (|act'| and |act(z) / z| are below 1.13 and 1),
-// from its largest finite |dY|, |G| and |U|
+// The factors of a row from a bound on its |dZ| (|act'| and |act(z) / z| are
+// below 1.13 and 1): its largest finite |dY|, |G| and |U|
+__device__ __forceinline__ void bound_scale(const BackwardPrep &p, float md, float mg, float mu, float &mul,
+                                            float &inv) {
+    const float f = p.layers == 2 ? fmaxf(mg, 1.13f * mu) : (p.pre[0] ? 1.13f : 1.f);
+    // (an overflowing bound: the largest finite one)
+    pow2_scale(fminf(md * f, 3.0e38f), mul, inv);
+}
 __device__ __forceinline__ void row_scale(const BackwardPrep &p, int64_t i, float &mul, float &inv) {
     const int64_t o = i * p.d_out;
     float md = 0.f, mg = 0.f, mu = 0.f;
@@ -318,9 +327,7 @@ __device__ __forceinline__ void row_scale(const BackwardPrep &p, int64_t i, floa
         mg = block_max(mg);
         mu = block_max(mu);
     }
-    const float f = p.layers == 2 ? fmaxf(mg, 1.13f * mu) : (p.pre[0] ? 1.13f : 1.f);
-    // (an overflowing bound: the largest finite one)
-    pow2_scale(fminf(md * f, 3.0e38f), mul, inv);
+    bound_scale(p, md, mg, mu, mul, inv);
 }
 
 // eight values of a row's inputs, zeros past the end
@@ -334,70 +341,130 @@ __device__ __forceinline__ void load_row8(const BackwardPrep &p, const void *x, 
     }
 }
 
-// outputs r0 .. r0 + 7 of row i of dZ (of dG and dU), as operand planes; the
-// values themselves in d0 (and d1)
-__device__ __forceinline__ void form_dz8(const BackwardPrep &p, int64_t i, int64_t r0, float mul, float (&d0)[8],
-                                         float (&d1)[8]) {
+// outputs r0 .. r0 + 7 of row i of dZ (of dG and dU) from dY and what was
+// saved, as operand planes; the values themselves in d0 (and d1)
+__device__ __forceinline__ void put_dz8(const BackwardPrep &p, int64_t i, int64_t r0, float mul, const float (&d)[8],
+                                        const float (&z)[8], const float (&u)[8], float (&d0)[8], float (&d1)[8]) {
     const int64_t ktot = (int64_t)p.planes_a * p.layers * p.kp;
-    float d[8], z[8], u[8];
-    load_row8(p, p.dY, i, r0, d);
     auto put = [&](int l, const float (&x)[8]) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = r0 + e < p.d_out ? x[e] * mul : 0.f;
         put_planes(p.D16 + operand_at(i, l * p.kp + r0, ktot), p.layers * p.kp * 256, p.planes_a, 0, v);
     };
-    if (p.layers == 2) {
-        load_row8(p, p.pre[0], i, r0, z);
-        load_row8(p, p.pre[1], i, r0, u);
-        fz_with_act(p.act, [&](auto act) {
+    fz_with_act(p.act, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        if (p.layers == 2) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                d0[e] = d[e] * u[e] * fz_slope<decltype(act)::value>(z[e]);
-                d1[e] = d[e] * fz_act<decltype(act)::value>(z[e]);
+                d0[e] = d[e] * u[e] * fz_slope<ACT>(z[e]);
+                d1[e] = d[e] * fz_act<ACT>(z[e]);
             }
-        });
-        put(1, d1);
-    } else if (p.act != 0) {
-        load_row8(p, p.pre[0], i, r0, z);
-        fz_with_act(p.act, [&](auto act) {
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d0[e] = d[e] * fz_slope<decltype(act)::value>(z[e]);
-        });
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d0[e] = d[e];
-    }
+            for (int e = 0; e < 8; ++e) d0[e] = ACT ? d[e] * fz_slope<ACT>(z[e]) : d[e];
+        }
+    });
     put(0, d0);
+    if (p.layers == 2) put(1, d1);
+}
+__device__ __forceinline__ void form_dz8(const BackwardPrep &p, int64_t i, int64_t r0, float mul, float (&d0)[8],
+                                         float (&d1)[8]) {
+    float d[8], z[8], u[8];
+    load_row8(p, p.dY, i, r0, d);
+    if (p.pre[0]) load_row8(p, p.pre[0], i, r0, z);
+    if (p.layers == 2) load_row8(p, p.pre[1], i, r0, u);
+    put_dz8(p, i, r0, mul, d, z, u, d0, d1);
 }
 
-// First pass: every group's largest scale, and either whole rows of dZ (the
-// second sweep over a row finds it in the caches), or, where the second pass
-// also sums columns for bias gradients, the rows' factors alone.  (Gated pair
-// of 11008, 4096 rows: 88 us for the factors and 187 with the weights for a
-// second pass that reads everything again.)
-__global__ __launch_bounds__(256) void backward_rows_kernel(BackwardPrep p) {
-    const int tid = threadIdx.x;
-    if ((int64_t)blockIdx.x < p.m) {
-        const int64_t i = blockIdx.x;
-        float mul, inv;
-        row_scale(p, i, mul, inv);
-        if (tid == 0) {
-            p.fa[i] = mul;
-            p.fa[p.m + i] = inv;
-        }
-        if (p.bias_part) return;
-        float d0[8], d1[8];
-        for (int64_t r0 = 8 * tid; r0 < p.kp; r0 += 8 * 256) form_dz8(p, i, r0, mul, d0, d1);
-    } else {
-        const int gi = (int)((int64_t)blockIdx.x - p.m);
-        float mx = 0.f;
-        for (int l = 0; l < p.layers; ++l)
-            for (int64_t r = tid; r < p.d_out; r += 256)
-                mx = fmaxf(mx, finite_abs(p.w[l].scales[(int64_t)gi * p.d_out + r]));
-        mx = block_max(mx);
-        if (tid == 0) p.fg[gi] = mx;
+// a group's largest scale, over all outputs (and both layers)
+template <int NW>
+__device__ __forceinline__ void group_range(const BackwardPrep &p, int gi) {
+    float mx = 0.f;
+    for (int l = 0; l < p.layers; ++l)
+        for (int64_t r = threadIdx.x; r < p.d_out; r += 64 * NW)
+            mx = fmaxf(mx, finite_abs(p.w[l].scales[(int64_t)gi * p.d_out + r]));
+    mx = block_max<NW>(mx);
+    if (threadIdx.x == 0) p.fg[gi] = mx;
+}
+
+// First pass, rows of bf16 that fit NC eight-element pieces per thread (512
+// threads), no bias gradients: a row is read once into registers, its factor
+// found, and dZ written.  (Gated pair of 11008, 4096 rows: read twice, which
+// the L2 does not hold, the pass moved 750 MB in 180 us.)
+// NS: dY alone, with Z, or with G and U
+constexpr int ROW_NW = 8, ROW_PIECES = 4;
+template <int NC, int NS>
+__global__ __launch_bounds__(64 * ROW_NW, 4) void backward_row_kernel(BackwardPrep p) {
+    if ((int64_t)blockIdx.x >= p.m) {
+        group_range<ROW_NW>(p, (int)((int64_t)blockIdx.x - p.m));
+        return;
     }
+    constexpr int STEP = 8 * 64 * ROW_NW;
+    const int64_t i = blockIdx.x, o = i * p.d_out;
+    const int r0 = 8 * threadIdx.x;
+    const uint16_t *src[3] = {(const uint16_t *)p.dY + o, (const uint16_t *)p.pre[0] + o, (const uint16_t *)p.pre[1] + o};
+    u32x4 raw[NS][NC];
+#pragma unroll
+    for (int a = 0; a < NS; ++a)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            raw[a][c] = r0 + c * STEP < p.d_out ? *(const u32x4 *)(src[a] + r0 + c * STEP) : u32x4{0u, 0u, 0u, 0u};
+    auto unpack = [](const u32x4 &w, float (&v)[8]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __builtin_bit_cast(float, w[e] << 16);
+            v[2 * e + 1] = __builtin_bit_cast(float, w[e] & 0xffff0000u);
+        }
+    };
+    float mx[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int a = 0; a < NS; ++a) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float v[8];
+            unpack(raw[a][c], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx[a] = fmaxf(mx[a], finite_abs(v[e]));
+        }
+        mx[a] = block_max<ROW_NW>(mx[a]);
+    }
+    float mul, inv;
+    bound_scale(p, mx[0], mx[1], mx[2], mul, inv);
+    if (threadIdx.x == 0) {
+        p.fa[i] = mul;
+        p.fa[p.m + i] = inv;
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int r = r0 + c * STEP;
+        if (r < p.kp) {
+            float d[8], z[8], u[8], d0[8], d1[8];
+            unpack(raw[0][c], d);
+            unpack(raw[NS > 1 ? 1 : 0][c], z);
+            unpack(raw[NS > 2 ? 2 : 0][c], u);
+            put_dz8(p, i, r, mul, d, z, u, d0, d1);
+        }
+    }
+}
+
+// First pass otherwise: whole rows of dZ in two sweeps, or, where the second
+// pass also sums columns for bias gradients, the rows' factors alone
+__global__ __launch_bounds__(256) void backward_rows_kernel(BackwardPrep p) {
+    if ((int64_t)blockIdx.x >= p.m) {
+        group_range<4>(p, (int)((int64_t)blockIdx.x - p.m));
+        return;
+    }
+    const int64_t i = blockIdx.x;
+    float mul, inv;
+    row_scale(p, i, mul, inv);
+    if (threadIdx.x == 0) {
+        p.fa[i] = mul;
+        p.fa[p.m + i] = inv;
+    }
+    if (p.bias_part) return;
+    float d0[8], d1[8];
+    for (int64_t r0 = 8 * threadIdx.x; r0 < p.kp; r0 += 8 * 256) form_dz8(p, i, r0, mul, d0, d1);
 }
 
 // dz_rows rows by 256 columns of dZ (of dG and dU) with their columns' sums
@@ -932,6 +999,14 @@ hipError_t launch_forward_prep(ForwardPrep p, int64_t blocks, hipStream_t st) {
     return hipGetLastError();
 }
 
+void launch_row(const BackwardPrep &p, int npre, unsigned blocks, hipStream_t st) {
+    switch (npre) {
+        case 0: backward_row_kernel<ROW_PIECES, 1><<<blocks, 64 * ROW_NW, 0, st>>>(p); break;
+        case 1: backward_row_kernel<ROW_PIECES, 2><<<blocks, 64 * ROW_NW, 0, st>>>(p); break;
+        default: backward_row_kernel<ROW_PIECES, 3><<<blocks, 64 * ROW_NW, 0, st>>>(p); break;
+    }
+}
+
 const char *at(const void *p, int64_t elements, int bf16) { return (const char *)p + elements * (bf16 ? 2 : 4); }
 
 }  // namespace
@@ -1056,7 +1131,12 @@ hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st) {
         const int64_t row_blocks = cdiv(m, p.dz_rows);
         p.dz_blocks = bias ? p.dz_cols * row_blocks : 0;
         // the groups' ranges and the weights once, with the first rows
-        backward_rows_kernel<<<(unsigned)(m + (i0 == 0 ? s.ngroups : 0)), 256, 0, st>>>(p);
+        const unsigned firsts = (unsigned)(m + (i0 == 0 ? s.ngroups : 0));
+        const int64_t pieces = cdiv(w.kp, 8 * 64 * ROW_NW);
+        if (p.vec && p.bf16 && !bias && pieces <= ROW_PIECES)
+            launch_row(p, npre, firsts, st);
+        else
+            backward_rows_kernel<<<firsts, 256, 0, st>>>(p);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const int64_t blocks =

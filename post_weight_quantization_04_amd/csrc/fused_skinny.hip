@@ -437,51 +437,64 @@ __global__ __launch_bounds__(256) void skinny_backward_kernel(SkinnyBackward p) 
     fetch(std::min(wave, steps - 1), sl[0]);
     fetch(std::min(wave + 4, steps - 1), sl[1]);
 
-    // dZ of the range in f16: wave w takes rows w, w + 4, ... , all loads in
-    // flight together
+    // dZ of the range in f16 (wave w takes rows w, w + 4, ...), and the largest
+    // scale of each of the columns' groups over the range: all loads in flight
+    // together, the maxima's exchanges side by side
     {
-        float v[4][PER];
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int c = 0; c < PER; ++c) {
-                const int64_t r = std::min<int64_t>(rb + 64 * c + lane, s.d_out - 1);
-                v[b][c] = fz_ld(p.dz[l], std::min<int64_t>(wave + 4 * b, s.m - 1) * s.d_out + r, p.dz_bf16);
-            }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int i = wave + 4 * b;
-            if (i >= s.m) break;
-            float mx = 0.f;
-#pragma unroll
-            for (int c = 0; c < PER; ++c) {
-                if (rb + 64 * c + lane >= rend) v[b][c] = 0.f;
-                mx = fmaxf(mx, finite_abs(v[b][c]));
-            }
-            float mul, inv;
-            f16_scale(wave_max(mx), mul, inv);
-            if (lane == 0) rowinv[i] = inv;
-#pragma unroll
-            for (int c = 0; c < PER; ++c) {
-                float x = v[b][c] * mul;
-                asm("" : "+v"(x));   // (rounded to f16 from this value alone, both times)
-                const bool finite = fabsf(x) < __builtin_inff();   // (others only in the last part: see put_planes)
-                const _Float16 h = (_Float16)(finite || !HI ? x : 0.f);
-                dz[0][i][64 * c + lane] = h;
-                if (HI) dz[AP - 1][i][64 * c + lane] = (_Float16)(finite ? x - (float)h : x);
-            }
-        }
-    }
-    // the largest scale of each of the columns' groups, over the range
-    for (int gq = g0 + wave; gq <= g1; gq += 4) {
-        float mx = 0.f;
+        float v[4][PER], sc[PER], mx[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < PER; ++c) {
             const int64_t r = std::min<int64_t>(rb + 64 * c + lane, rend - 1);
-            mx = fmaxf(mx, finite_abs(w.scales[(int64_t)gq * s.d_out + r]));
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                v[b][c] = fz_ld(p.dz[l], std::min<int64_t>(wave + 4 * b, s.m - 1) * s.d_out + r, p.dz_bf16);
+            sc[c] = w.scales[(int64_t)std::min(g0 + wave, g1) * s.d_out + r];
         }
-        mx = wave_max(mx);
-        if (lane == 0) gmax[gq - g0] = mx;
+#pragma unroll
+        for (int c = 0; c < PER; ++c) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (rb + 64 * c + lane >= rend) v[b][c] = 0.f;
+                mx[b] = fmaxf(mx[b], finite_abs(v[b][c]));
+            }
+            mx[4] = fmaxf(mx[4], finite_abs(sc[c]));
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            float t[5];
+#pragma unroll
+            for (int b = 0; b < 5; ++b) t[b] = __shfl_xor(mx[b], o);
+#pragma unroll
+            for (int b = 0; b < 5; ++b) mx[b] = fmaxf(mx[b], t[b]);
+        }
+        if (lane == 0 && g0 + wave <= g1) gmax[wave] = mx[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int i = wave + 4 * b;
+            if (i < s.m) {
+                float mul, inv;
+                f16_scale(mx[b], mul, inv);
+                if (lane == 0) rowinv[i] = inv;
+#pragma unroll
+                for (int c = 0; c < PER; ++c) {
+                    float x = v[b][c] * mul;
+                    asm("" : "+v"(x));   // (rounded to f16 from this value alone, both times)
+                    const bool finite = fabsf(x) < __builtin_inff();   // (others only in the last part: see put_planes)
+                    const _Float16 h = (_Float16)(finite || !HI ? x : 0.f);
+                    dz[0][i][64 * c + lane] = h;
+                    if (HI) dz[AP - 1][i][64 * c + lane] = (_Float16)(finite ? x - (float)h : x);
+                }
+            }
+        }
+        for (int gq = g0 + wave + 4; gq <= g1; gq += 4) {
+            float m2 = 0.f;
+#pragma unroll
+            for (int c = 0; c < PER; ++c)
+                m2 = fmaxf(m2, finite_abs(w.scales[(int64_t)gq * s.d_out +
+                                                   std::min<int64_t>(rb + 64 * c + lane, rend - 1)]));
+            m2 = wave_max(m2);
+            if (lane == 0) gmax[gq - g0] = m2;
+        }
     }
     __syncthreads();
     float mul, inv;
