@@ -605,51 +605,54 @@ struct Gemm {
     const void *residual;
     void *Y;
     void *pre[2];
-    int out_bf16, vec;          // vec: four consecutive outputs load and store together
+    int out_bf16, vec;          // vec: four consecutive outputs load and store together (n % 4 == 0)
     float *part;                // [nsplit][layers][m][np] when nsplit > 1
     int64_t np;                 // n padded to whole quads
     int nsplit;
     int mt, nt;                 // tiles
 };
 
-// The epilogue of four consecutive columns n .. n + 3 of row i (of both
-// layers, when gated), from their sums
-template <bool GATED>
-__device__ __forceinline__ void epilogue4(const Gemm &p, int64_t i, int64_t n, float fa, f32x4 z, f32x4 u) {
-    const int64_t o = i * p.n + n;
-    const int count = (int)std::min<int64_t>(4, p.n - n);
-    auto load = [&](const void *x, int64_t at, int bf16) {
-        if (p.vec) return fz_ld4(x, at, bf16);   // the four exist together
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+// The epilogue of W (four, where p.vec allows; else one) consecutive columns,
+// of both layers when gated: what depends on the columns alone ...
+template <bool GATED, int W>
+struct Columns {
+    f32x4 fw[GATED ? 2 : 1], bias[GATED ? 2 : 1];
+    __device__ __forceinline__ static f32x4 load(const void *x, int64_t at, int bf16) {
+        if constexpr (W == 4) return fz_ld4(x, at, bf16);
+        return f32x4{fz_ld(x, at, bf16), 0.f, 0.f, 0.f};
+    }
+    __device__ __forceinline__ Columns(const Gemm &p, int64_t n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < count) v[e] = fz_ld(x, at + e, bf16);
-        return v;
-    };
-    auto store = [&](void *x, f32x4 v) {
-        if (p.vec) {
-            fz_st4(x, o, v, p.out_bf16);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < count) fz_st(x, o + e, v[e], p.out_bf16);
+        for (int l = 0; l < (GATED ? 2 : 1); ++l) {
+            fw[l] = load(p.fw, l * p.n + n, 0);
+            bias[l] = p.bias[l] ? load(p.bias[l], n, p.bias_bf16) : f32x4{0.f, 0.f, 0.f, 0.f};
         }
+    }
+};
+// ... and row i's outputs at columns n .. from their sums
+template <bool GATED, int W>
+__device__ __forceinline__ void epilogue(const Gemm &p, const Columns<GATED, W> &col, int64_t i, int64_t n, float fa,
+                                         f32x4 z, f32x4 u) {
+    const int64_t o = i * p.n + n;
+    auto store = [&](void *x, f32x4 v) {
+        if constexpr (W == 4)
+            fz_st4(x, o, v, p.out_bf16);
+        else
+            fz_st(x, o, v[0], p.out_bf16);
     };
-    z = z * fa * load(p.fw, n, 0);
-    if (p.bias[0]) z += load(p.bias[0], n, p.bias_bf16);
+    z = z * fa * col.fw[0] + col.bias[0];
     if (p.pre[0]) store(p.pre[0], z);
-    f32x4 y;
+    f32x4 y = z;
     fz_with_act(p.act, [&](auto act) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = fz_act<decltype(act)::value>(z[e]);
+        for (int e = 0; e < W; ++e) y[e] = fz_act<decltype(act)::value>(z[e]);
     });
     if constexpr (GATED) {
-        u = u * fa * load(p.fw, p.n + n, 0);
-        if (p.bias[1]) u += load(p.bias[1], n, p.bias_bf16);
+        u = u * fa * col.fw[1] + col.bias[1];
         if (p.pre[1]) store(p.pre[1], u);
         y *= u;
     }
-    if (p.residual) y += load(p.residual, o, p.out_bf16);
+    if (p.residual) y += col.load(p.residual, o, p.out_bf16);
     store(p.Y, y);
 }
 
@@ -695,7 +698,7 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
     constexpr int PER_STAGE = NDMA + MDMA;
     constexpr int COLS = GATED ? BN / 2 : BN;                         // columns n of one layer
     constexpr int EROW = BN + 4;                                      // floats of an epilogue row (padded)
-    __shared__ __attribute__((aligned(16))) char lds[std::max(NBUF * STAGE, 2 * 64 * EROW * 4)];
+    __shared__ __attribute__((aligned(16))) char lds[std::max(NBUF * STAGE, (2 * 64 * EROW + BM) * 4)];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave >> 1, wm = wave & 1;
@@ -818,7 +821,41 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
     gm_barrier();
 
     // lane (h, li), register 4 q + e of tile (j, i) <-> column 8 q + 4 h + e, row li
-    constexpr int TPR = COLS / 4;   // threads per row of outputs
+    const int tid = threadIdx.x;
+    float *fas = (float *)lds + 2 * 64 * EROW;
+    auto leave = [&](auto width, const float *out, int i) {
+        constexpr int W = decltype(width)::value, TPR = COLS / W;   // threads per row of outputs
+        const int c = W * (tid % TPR);
+        const int64_t n = n0 + c;
+        if (n >= p.n) return;
+        const int64_t first = m0 + 32 * i;
+        if (p.nsplit > 1) {
+            for (int rr = tid / TPR; rr < 64; rr += 256 / TPR) {
+                const int64_t row = first + (rr >> 5) * 32 * MI + (rr & 31);
+                if (row >= p.m) continue;
+                float *part = p.part + (((int64_t)split * p.layers * p.m) + row) * p.np + n;
+                *(f32x4 *)part = *(const f32x4 *)(out + rr * EROW + c);   // (W is 4: see below)
+                if (GATED) *(f32x4 *)(part + p.m * p.np) = *(const f32x4 *)(out + rr * EROW + BN / 2 + c);
+            }
+            return;
+        }
+        const Columns<GATED, W> col(p, n);
+#pragma unroll 4
+        for (int rr = tid / TPR; rr < 64; rr += 256 / TPR) {
+            const int64_t row = first + (rr >> 5) * 32 * MI + (rr & 31);
+            if (row < p.m) {
+                f32x4 z = {0.f, 0.f, 0.f, 0.f}, u = z;
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    z[e] = out[rr * EROW + c + e];
+                    if (GATED) u[e] = out[rr * EROW + BN / 2 + c + e];
+                }
+                epilogue<GATED, W>(p, col, row, n, fas[row - m0], z, u);
+            }
+        }
+    };
+    // the tile's row factors (visible behind the first barrier below)
+    for (int r = tid; r < BM; r += 256) fas[r] = m0 + r < p.m ? p.fa[m0 + r] : 0.f;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
         float *out = (float *)lds + (i & 1) * 64 * EROW;
@@ -831,58 +868,57 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
                     f32x4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
             }
         gm_barrier();   // (the buffer two passes back was read before the previous barrier)
-        const int c = 4 * ((int)threadIdx.x % TPR);
-        for (int rr = (int)threadIdx.x / TPR; rr < 64; rr += 256 / TPR) {
-            const int64_t row = m0 + (rr >> 5) * 32 * MI + 32 * i + (rr & 31), n = n0 + c;
-            if (row >= p.m || n >= p.n) continue;
-            const f32x4 z = *(const f32x4 *)(out + rr * EROW + c);
-            f32x4 u = {0.f, 0.f, 0.f, 0.f};
-            if (GATED) u = *(const f32x4 *)(out + rr * EROW + BN / 2 + c);
-            if (p.nsplit > 1) {
-                float *part = p.part + (((int64_t)split * p.layers * p.m) + row) * p.np + n;
-                *(f32x4 *)part = z;
-                if (GATED) *(f32x4 *)(part + p.m * p.np) = u;
-            } else {
-                epilogue4<GATED>(p, row, n, p.fa[row], z, u);
-            }
-        }
+        if (p.vec || p.nsplit > 1)
+            leave(std::integral_constant<int, 4>{}, out, i);
+        else
+            leave(std::integral_constant<int, 1>{}, out, i);
     }
 }
 
-// the splits' sums in split order, and the epilogue: four columns per thread
-template <bool GATED>
+// the splits' sums in split order, and the epilogue: W columns per thread
+template <bool GATED, int W>
 __global__ __launch_bounds__(256) void split_reduce_kernel(Gemm p) {
-    const int64_t quads = p.np / 4;
+    const int64_t per = (p.n + W - 1) / W;
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (t >= p.m * quads) return;
-    const int64_t i = t / quads, n = 4 * (t - i * quads);
+    if (t >= p.m * per) return;
+    const int64_t i = t / per, n = W * (t - i * per);
     f32x4 z = {0.f, 0.f, 0.f, 0.f}, u = z;
     for (int s = 0; s < p.nsplit; ++s) {
         const float *z0 = p.part + ((int64_t)s * p.layers * p.m + i) * p.np + n;
-        z += *(const f32x4 *)z0;
-        if (GATED) u += *(const f32x4 *)(z0 + p.m * p.np);
+        const float *u0 = z0 + p.m * p.np;
+        if constexpr (W == 4) {
+            z += *(const f32x4 *)z0;
+            if (GATED) u += *(const f32x4 *)u0;
+        } else {
+            z[0] += z0[0];
+            if (GATED) u[0] += u0[0];
+        }
     }
-    epilogue4<GATED>(p, i, n, p.fa[i], z, u);
+    epilogue<GATED, W>(p, Columns<GATED, W>(p, n), i, n, p.fa[i], z, u);
 }
 
 int64_t pad_stage(int64_t k) { return cdiv(k, GK) * GK; }
 int64_t pad_quad(int64_t n) { return cdiv(n, 4) * 4; }
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// Tiles of 256 x 256, or of 128 x 128 where fewer than 32 large ones would do
-// (509 x 251 fp32: 23 us a call against 31; 2048 x 4096, 128 large tiles with
-// two k splits: 263 us against 294 with 128 x 128).  k splits for grids that
-// leave CUs idle, each of at least eight stages.
+// Tiles of 256 x 256 where at least 32 of them, with their k splits, fill half
+// the CUs; otherwise of 128 x 128 (509 x 251 fp32: 23 us a call against 31;
+// 2048 x 4096 of 11008, 128 large tiles with two splits: 263 us against 294
+// with small ones).  k splits for grids that leave CUs idle, each of at least
+// eight stages.
 struct Plan {
     int mi, nj, mt, nt, nsplit;   // tile of 64 mi rows by 64 nj columns
 };
 Plan plan_gemm(int64_t m, int64_t n, int layers, int stages) {
     Plan p;
-    p.mi = p.nj = cdiv(m, 256) * cdiv(layers * n, 256) >= 32 ? 4 : 2;
-    p.mt = (int)cdiv(m, 64 * p.mi);
-    p.nt = (int)cdiv(n, (layers == 2 ? 32 : 64) * p.nj);
-    const int64_t tiles = (int64_t)p.mt * p.nt;
-    p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, (int64_t)stages / 8, (int64_t)16}));
+    for (int size = 4; size >= 2; size -= 2) {
+        p.mi = p.nj = size;
+        p.mt = (int)cdiv(m, 64 * p.mi);
+        p.nt = (int)cdiv(n, (layers == 2 ? 32 : 64) * p.nj);
+        const int64_t tiles = (int64_t)p.mt * p.nt;
+        p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, (int64_t)stages / 8, (int64_t)16}));
+        if (tiles >= 32 && tiles * p.nsplit >= 128) break;
+    }
     return p;
 }
 
@@ -958,7 +994,10 @@ hipError_t launch_gemm_k(const Gemm &g, hipStream_t st) {
     fused_gemm_kernel<MI, NJ, GATED><<<(unsigned)(g.mt * g.nt * g.nsplit), 256, 0, st>>>(g);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || g.nsplit == 1) return e;
-    split_reduce_kernel<GATED><<<(unsigned)cdiv(g.m * (g.np / 4), 256), 256, 0, st>>>(g);
+    if (g.vec)
+        split_reduce_kernel<GATED, 4><<<(unsigned)cdiv(g.m * cdiv(g.n, 4), 256), 256, 0, st>>>(g);
+    else
+        split_reduce_kernel<GATED, 1><<<(unsigned)cdiv(g.m * g.n, 256), 256, 0, st>>>(g);
     return hipGetLastError();
 }
 
