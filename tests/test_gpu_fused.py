@@ -196,6 +196,11 @@ EXACT = [
     (200, 480, 4, 48, 65, True), (300, 992, 3, 32, 129, True), (333, 1000, 2, 16, 300, True),
     (1024, 520, 4, 128, 257, False), (516, 260, 3, 80, 8, False), (1030, 2052, 4, 32, 5, True),
     (260, 300, 4, 16, 512, True), (2050, 130, 2, 32, 700, False),
+    # pairs of outputs per lane, whole chunks of four units or not, one and two blocks of rows
+    (8200, 512, 4, 128, 3, True), (8210, 256, 2, -1, 70, False), (8202, 192, 3, 64, 20, True),
+    (8196, 128, 8, 128, 100, False), (8300, 160, 8, 32, 2, False),
+    # wide rows of dZ: held in registers (up to 16384), read twice beyond
+    (9000, 48, 4, 16, 20, True), (16400, 40, 3, 16, 33, False), (4104, 72, 2, 32, 130, True),
 ]
 
 
@@ -259,6 +264,29 @@ def test_backward_exact(case, in_dt, out_dt):
     dg, du = d * u * on, d * z * on
     assert torch.equal(dA, (mm(dg, gate.w) + mm(du, up.w)).to(DT[out_dt]))
     assert torch.equal(dbg, dg.sum(0).float()) and torch.equal(dbu, du.sum(0).float())
+
+
+def test_more_rows_than_one_pass():
+    """More activation rows than the dense form takes at once (16384): later
+    passes use the same weights, and bias gradients add up over them."""
+    rng = np.random.default_rng(16)
+    m, d_out, d_in = 16384 + 300, 72, 64
+    gate = Layer(rng, d_out, d_in, 4, 32, True, True)
+    up = Layer(rng, d_out, d_in, 4, 32, True, True, gate.perm)
+    A, res = values(rng, (m, d_in), "bf16", True), values(rng, (m, d_out), "bf16", True)
+    dY, Z, U = (values(rng, (m, d_out), "bf16", True) for _ in range(3))
+    Y = P.dequant_linear(A, gate.q, residual=res)
+    assert torch.equal(Y, (mm(A, gate.w.t()) + res.to(F64)).to(torch.bfloat16))
+    H, G, _ = P.dequant_gated(A, gate.q, up.q, "relu", save_preact=True)
+    assert torch.equal(G, mm(A, gate.w.t()).to(torch.bfloat16))
+    assert torch.equal(H, (mm(A, gate.w.t()).clamp(min=0) * mm(A, up.w.t())).float().to(torch.bfloat16))
+    d, z, u = dY.to(F64), Z.to(F64), U.to(F64)
+    on = (z > 0).to(F64)
+    for bias in (True, False):
+        dA, dbg, dbu = P.dequant_gated_backward(dY, gate.q, up.q, Z, U, "relu", bias)
+        assert torch.equal(dA, (mm(d * u * on, gate.w) + mm(d * z * on, up.w)).to(torch.bfloat16))
+        if bias:
+            assert torch.equal(dbg, (d * u * on).sum(0).float()) and torch.equal(dbu, (d * z * on).sum(0).float())
 
 
 # ---------------------------------------------------------------------------
