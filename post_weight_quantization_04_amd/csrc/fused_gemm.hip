@@ -730,14 +730,20 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
     const uint16_t *bbase = p.B + (n0 >> 8) * (p.ldb / GK) * TILE_STAGE + (n0 & 255) * GK + bskip;
     const __amdgpu_buffer_rsrc_t arsrc = gm_rsrc(abase, p.lda / GK * TILE_STAGE * 2);
     const __amdgpu_buffer_rsrc_t brsrc = gm_rsrc(bbase, p.ldb / GK * TILE_STAGE * 2);
-    // first (part 0) or second half of this wave's loads of stage st; stages
-    // past the end re-read the last one, unused
-    auto issue = [&](int st, int part) {
-        char *buf = lds + (st % NBUF) * STAGE;
-        const int s = st0 + std::min(st, nst - 1);
-        const int pass = (s >= spp) + (s >= 2 * spp), kk = (s - pass * spp) * (int)TILE_STAGE * 2;
-        const int bk = __builtin_amdgcn_readfirstlane(kk + (pass == 1 ? (int)(p.b_plane / GK * TILE_STAGE) * 2 : 0));
-        const int ak = __builtin_amdgcn_readfirstlane(kk + (pass == (p.exact ? 0 : 2) ? (int)(p.a_plane / GK * TILE_STAGE) * 2 : 0));
+    // Stages are issued in order, each in two parts (part 0, then 1) of this
+    // wave's loads: offsets of the one in turn into both operands, and the
+    // stages left of its pass; past the end the last stage again, unused.
+    int turn = 0;                                     // the next stage's ring slot is turn % NBUF
+    const int pass0 = st0 / spp;
+    int pass = __builtin_amdgcn_readfirstlane(pass0);
+    int left = __builtin_amdgcn_readfirstlane(spp - (st0 - pass0 * spp));
+    constexpr int BYTES = (int)TILE_STAGE * 2;
+    const int bsecond = (int)(p.b_plane / GK) * BYTES, asecond = (int)(p.a_plane / GK) * BYTES;
+    const int apass = p.exact ? 0 : 2;                // the pass that reads A's second plane
+    int bk = (st0 - pass0 * spp) * BYTES + (pass0 == 1 ? bsecond : 0);
+    int ak = (st0 - pass0 * spp) * BYTES + (pass0 == apass ? asecond : 0);
+    auto issue = [&](int part) {
+        char *buf = lds + (turn % NBUF) * STAGE;
 #pragma unroll
         for (int q = NDMA / 2 * part; q < NDMA / 2 * (part + 1); ++q)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(brsrc, (gm_lds_void *)(buf + (NDMA * wave + q) * 1024), 16,
@@ -746,6 +752,16 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
         for (int q = MDMA / 2 * part; q < MDMA / 2 * (part + 1); ++q)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(arsrc, (gm_lds_void *)(buf + NSIDE + (MDMA * wave + q) * 1024),
                                                      16, (MDMA * wave + q) * 1024 + lane * 16, ak, 0, 0);
+    };
+    // on to the next stage (after both parts; selects only, so that the
+    // products around it stay one scheduling region)
+    auto advance = [&] {
+        ++turn;
+        const bool more = turn < nst, wrap = left == 1;
+        pass += more && wrap;
+        left = more ? (wrap ? spp : left - 1) : left;
+        bk = more ? (wrap ? (pass == 1 ? bsecond : 0) : bk + BYTES) : bk;
+        ak = more ? (wrap ? (pass == apass ? asecond : 0) : ak + BYTES) : ak;
     };
 
     // operand reads: lane l supplies row l % 32 of a 32-row tile, k 8 (l / 32) .. +7
@@ -775,14 +791,15 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
             for (int i = 0; i < MI; ++i)
                 acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[j], fa[i], acc[j][i], 0, 0, 0);
     };
-    // the half stage's instruction order: operand reads one per MFMA, then
-    // its loads, spread over the rest
+    // the half stage's instruction order: operand reads one behind each MFMA
+    // (the first MFMA waits for every read before it), then its loads, spread
+    // over the rest
     auto spread = [] {
         constexpr int MFMA = 0x008, VMEM = 0x010, DSR = 0x100;
 #pragma unroll
         for (int i = 0; i < NJ + MI; ++i) {
-            __builtin_amdgcn_sched_group_barrier(DSR, 1, 0);
             __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(DSR, 1, 0);
         }
 #pragma unroll
         for (int i = 0; i < PER_STAGE / 2; ++i) {
@@ -792,24 +809,26 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
     };
     f16x8 fb0[NJ], fa0[MI], fb1[NJ], fa1[MI];
     for (int st = 0; st < NBUF - 1; ++st) {
-        issue(st, 0);
-        issue(st, 1);
+        issue(0);
+        issue(1);
+        advance();
     }
     gm_wait<(NBUF - 2) * PER_STAGE>();     // stage 0 landed
     gm_barrier();
-    issue(NBUF - 1, 0);
+    issue(0);
     frags(0, 0, fb0, fa0);
     for (int st = 0; st < nst - 1; ++st) {
         frags(st, 1, fb1, fa1);
-        issue(st - 1 + NBUF, 1);
+        issue(1);
         products(fb0, fa0);
         spread();
         __builtin_amdgcn_sched_barrier(0);
+        advance();
         gm_wait<(NBUF - 2) * PER_STAGE>(); // stage st + 1 landed
         gm_barrier();                      // every wave has read stage st: its buffer is free
         __builtin_amdgcn_sched_barrier(0);
         frags(st + 1, 0, fb0, fa0);
-        issue(st + NBUF, 0);
+        issue(0);
         products(fb1, fa1);
         spread();
         __builtin_amdgcn_sched_barrier(0);
