@@ -278,11 +278,16 @@ GPTQ_API gptq_status gptq_dequant_matmul(const void *A, gptq_dtype a_dtype, int6
  *   dbias*     fp32 outputs, overwritten (not accumulated); NULL: not formed.
  *   residual   NULL: none.
  * Numerics: fp32 sums, one rounding of each output to its dtype.  With an F32
- * output every product keeps fp32 accuracy; with a BF16 output the weights may
- * be rounded to 11 significand bits on the way (an eighth of the output's own
- * rounding).  In a forward call's such rounding a row's groups share one
- * power-of-two range of 2^29, in a backward call's a group's rows do; values
- * below it lose precision gradually.  All results are deterministic.
+ * output every product keeps fp32 accuracy (operands of 22 significand bits at
+ * least); with a BF16 output the weights, and in the backward calls dZ, may be
+ * rounded to 11 significand bits on the way (an eighth of the output's own
+ * rounding each).  What is rounded so shares a power-of-two range of 2^29: a
+ * row of activations or of dZ (in the gated pair's backward call measured from
+ * max|dH| max(max|G|, max|U|) of the row), the weights of a layer's row in a
+ * forward call, those of a group of columns in a backward one; values below
+ * the range lose precision gradually.  Values of A, dY, dH, Z, G and U that
+ * are not finite reach the results of their own row only.  All results are
+ * deterministic.
  * workspace  device scratch of the matching size query's bytes (may be NULL
  *            when that is 0), 256-byte aligned.  Its contents need not be
  *            prepared and are not kept: calls of any sizes may share one as

@@ -517,7 +517,7 @@ def dequant_linear(A, q: "QuantizedLayer", bias=None, activation="none", residua
     A: [m, d_in] bfloat16/float32; bias: [d_out] bfloat16/float32; residual:
     [m, d_out] of out_dtype (A's dtype by default); activation: one of
     ACTIVATIONS.  Returns Y, or (Y, Z) with the pre-activation Z = A W_hat^T +
-    bias when save_preact.  workspace: any device tensor of at least
+    bias when save_preact.  workspace: any 256-byte aligned device tensor of at least
     dequant_linear_workspace_size bytes (allocated when absent or too small).
     Not differentiable by autograd: see dequant_linear_backward."""
     f = _FusedCall(A, "A", q, activation, out_dtype, workspace, stream)

@@ -10,7 +10,13 @@
 // A layer's dequantization costs d_out d_in elements of traffic, the product
 // m times as many multiplications: from about a hundred rows on the products
 // dominate, and the inner loop then carries neither code extraction nor group
-// scales.
+// scales.  Measured: the product 1.19 PFLOP/s for the pair 28672 x 8192 with
+// 2048 rows (1.62 ms), 1.2-1.27 for K = 22016 and 4096 x 4096 outputs (0.58-0.62
+// ms), 1.0 where the last tiles leave CUs idle (pair 11008 x 4096, 4096 rows:
+// 0.74 ms); matrix cores busy 62-63% of cycles at a clock of 1.4-1.7 GHz, no
+// LDS conflicts.  A large library product reaches 1.31-1.42 on the same card.
+// The dequantized weights are written at 2.6-4.0 TB/s (pair 28672 x 8192: 940
+// MB in 287 us).
 //
 // f16 operands.  Every row of A16 / D16 is scaled by a power of two that
 // brings its largest finite magnitude to [2^14, 2^15), every row n of W16 by
@@ -190,7 +196,8 @@ __device__ void prep_rows(const ForwardPrep &p, int64_t i, char *lds) {
 
 // One work group: 32 rows of the layer(s) and FW_K of their columns.  A wave
 // takes 8 rows by 64 columns at a time, so that it reads words of eight rows
-// side by side and writes whole 128-byte lines.
+// side by side and writes 512 contiguous bytes.  Bound by the write of W16;
+// 1024 columns measured best (4096 x 11008: 35 us; 512: 39, 2048: 46).
 constexpr int FW_ROWS = 32, FW_K = 1024;
 template <int BITS>
 __device__ void prep_weights(const ForwardPrep &p, unsigned b, float *lds) {
@@ -681,7 +688,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t gm_rsrc(const void *p, int64_t
 // four consecutive columns of one activation row.  Both operands move by
 // 16-byte buffer loads straight into a ring of four LDS stages of 32 k (each
 // load a contiguous kilobyte: read from rows a stage apart in K-major
-// matrices, 64 bytes each, the same loop reached 55% of the matrix cores);
+// matrices, 64 bytes each, the same loop took 1.86 ms against 1.65 for the pair
+// 28672 x 8192 with 2048 rows);
 // the permuted 16-byte pieces put the operand reads of a wave on distinct
 // banks.  Each half stage's MFMAs run
 // between the reads of the next half's operands and half of a refill; the
