@@ -6,6 +6,7 @@
 
 namespace gptq {
 
+typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(2))) __bf16 fz_bf16x2;
 
@@ -61,6 +62,19 @@ __device__ __forceinline__ void fz_st4(void *p, int64_t i, f32x4 v, int bf16) {
     else
         *(f32x4 *)((float *)p + i) = v;
 }
+
+// The factor 2^t that brings v, positive and finite, to [2^14, 2^15) (f16's
+// range), and the exponent -t that undoes it; 1 and 0 for 0.  A sum of scaled
+// products returns by ldexpf with both operands' exponents added: the sums are
+// of order 2^32, the exponents up to 126 each, and one factor at a time would
+// overflow (or vanish) on the way to results that fp32 holds.
+__device__ __forceinline__ void fz_pow2_scale(float v, float &mul, int &undo) {
+    int e = (int)((__builtin_bit_cast(unsigned, v) >> 23) & 255u) - 127;   // (subnormals: -127)
+    if (v == 0.f) e = 14;
+    undo = max(-126, min(126, e - 14));
+    mul = __builtin_bit_cast(float, (unsigned)(127 - undo) << 23);
+}
+__device__ __forceinline__ float fz_ldexp(float v, int e) { return __builtin_amdgcn_ldexpf(v, e); }
 
 // ---------------------------------------------------------------------------
 // activations and their slopes (fp32)

@@ -39,16 +39,6 @@ constexpr int GK = 32;                    // contraction elements per stage
 constexpr int64_t DENSE_ROWS = 16384;     // activation rows per pass (bounds the workspace)
 constexpr int DZ_ROWS = 16, DZ_ROWS_MANY = 64;   // rows of dZ formed (and summed) by one work group
 
-// 2^-e for a positive finite v in [2^e, 2^(e+1)) times 2^14, as a factor and
-// its inverse (both normal); 1 for 0
-__device__ __forceinline__ void pow2_scale(float v, float &mul, float &inv) {
-    int e = (int)((__builtin_bit_cast(unsigned, v) >> 23) & 255u) - 127;   // (subnormals: -127)
-    if (v == 0.f) e = 14;
-    const int t = max(-126, min(126, 14 - e));
-    mul = __builtin_bit_cast(float, (unsigned)(127 + t) << 23);
-    inv = __builtin_bit_cast(float, (unsigned)(127 - t) << 23);
-}
-
 __device__ __forceinline__ float finite_abs(float v) {
     const float a = fabsf(v);
     return a < __builtin_inff() ? a : 0.f;   // NaN and infinities do not count
@@ -113,14 +103,14 @@ struct ForwardPrep {
     int64_t m, d_in, kp;        // kp: d_in padded to whole stages
     uint16_t *A16;              // rows [m], contraction [planes_a][kp]
     int planes_a;
-    float *fa;                  // [m] inverse row factors
+    int *ea;                    // [m] exponents that undo the rows' factors
     int pairs;                  // gather from two bf16 rows staged in the launch's LDS
     PackedLayer w[2];
     int64_t d_out, nwords;
     int g, ngroups, layers;
     uint16_t *W16;              // per layer: rows [d_out], contraction [planes_w][kp]
     int planes_w;
-    float *fw;                  // [layers][d_out] inverse factors
+    int *ew;                    // [layers][d_out] exponents
     int64_t row_blocks;         // work groups of the activation rows, then those of the weights
     int kchunks;
 };
@@ -131,7 +121,7 @@ __device__ void prep_rows(const ForwardPrep &p, int64_t i, char *lds) {
     const int d = (int)p.d_in, kp = (int)p.kp, es = p.a_bf16 ? 2 : 4;
     const int64_t ktot = (int64_t)p.planes_a * p.kp;
     const char *row[2] = {(const char *)p.A + i * d * es, (const char *)p.A + (i + rows - 1) * d * es};
-    float mx[2] = {0.f, 0.f}, mul[2], inv[2];
+    float mx[2] = {0.f, 0.f}, mul[2];
     if (p.vec) {
         for (int k = 8 * tid; k < d; k += 8 * 256) {
             float v[2][8];
@@ -158,8 +148,9 @@ __device__ void prep_rows(const ForwardPrep &p, int64_t i, char *lds) {
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        pow2_scale(block_max(mx[r]), mul[r], inv[r]);   // (its barriers also cover the staged rows)
-        if (tid == 0 && r < rows) p.fa[i + r] = inv[r];
+        int undo;
+        fz_pow2_scale(block_max(mx[r]), mul[r], undo);   // (its barriers also cover the staged rows)
+        if (tid == 0 && r < rows) p.ea[i + r] = undo;
     }
     for (int k0 = 8 * tid; k0 < kp; k0 += 8 * 256) {
         float v[2][8];
@@ -220,9 +211,10 @@ __device__ void prep_weights(const ForwardPrep &p, unsigned b, float *lds) {
     mx = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) mx = fmaxf(mx, lds[32 * e + rl]);
-    float mul, inv;
-    pow2_scale(mx * (float)((1 << BITS) - 1), mul, inv);
-    if (kc == 0 && lane < 8 && r0 + rl < d_out) p.fw[l * d_out + r] = inv;
+    float mul;
+    int undo;
+    fz_pow2_scale(mx * (float)((1 << BITS) - 1), mul, undo);
+    if (kc == 0 && lane < 8 && r0 + rl < d_out) p.ew[l * d_out + r] = undo;
     if (r0 + rl >= d_out) return;
     const float ginv = 1.f / (float)p.g;
     uint16_t *out = p.W16 + (int64_t)l * pad_tile(d_out) * p.planes_w * p.kp;
@@ -278,16 +270,17 @@ struct BackwardPrep {
     int layers;
     uint16_t *D16;              // rows [m], contraction [planes_a][layers][kp]
     int planes_a;
-    float *fa;                  // [m] row factors (mul), then [m] their inverses
+    float *fa;                  // [m] row factors
+    int *ea;                    // [m] exponents that undo them
     float *bias_part;           // [row blocks][layers][d_out], or NULL: no bias gradients
     PackedLayer w[2];
     const int32_t *perm;
     int64_t d_in, nwords;
     int g, ngroups, wvec;       // wvec: four rows' words load together
-    float *fg;                  // [ngroups] weight factors (mul), then their inverses
+    float *fg;                  // [ngroups] largest scales
     uint16_t *W16;              // rows [d_in], contraction [planes_w][layers][kp]
     int planes_w;
-    float *fw;                  // [d_in] inverse factors, original order
+    int *ew;                    // [d_in] exponents that undo the weights' factors, original order
     int dz_rows;                // rows of a dZ tile (bias gradients)
     int64_t dz_blocks, dz_cols; // dZ tiles, then weight tiles
 };
@@ -295,12 +288,12 @@ struct BackwardPrep {
 // The factors of a row from a bound on its |dZ| (|act'| and |act(z) / z| are
 // below 1.13 and 1): its largest finite |dY|, |G| and |U|
 __device__ __forceinline__ void bound_scale(const BackwardPrep &p, float md, float mg, float mu, float &mul,
-                                            float &inv) {
+                                            int &undo) {
     const float f = p.layers == 2 ? fmaxf(mg, 1.13f * mu) : (p.pre[0] ? 1.13f : 1.f);
     // (an overflowing bound: the largest finite one)
-    pow2_scale(fminf(md * f, 3.0e38f), mul, inv);
+    fz_pow2_scale(fminf(md * f, 3.0e38f), mul, undo);
 }
-__device__ __forceinline__ void row_scale(const BackwardPrep &p, int64_t i, float &mul, float &inv) {
+__device__ __forceinline__ void row_scale(const BackwardPrep &p, int64_t i, float &mul, int &undo) {
     const int64_t o = i * p.d_out;
     float md = 0.f, mg = 0.f, mu = 0.f;
     if (p.vec) {
@@ -334,7 +327,7 @@ __device__ __forceinline__ void row_scale(const BackwardPrep &p, int64_t i, floa
         mg = block_max(mg);
         mu = block_max(mu);
     }
-    bound_scale(p, md, mg, mu, mul, inv);
+    bound_scale(p, md, mg, mu, mul, undo);
 }
 
 // eight values of a row's inputs, zeros past the end
@@ -436,11 +429,12 @@ __global__ __launch_bounds__(64 * ROW_NW, 4) void backward_row_kernel(BackwardPr
         }
         mx[a] = block_max<ROW_NW>(mx[a]);
     }
-    float mul, inv;
-    bound_scale(p, mx[0], mx[1], mx[2], mul, inv);
+    float mul;
+    int undo;
+    bound_scale(p, mx[0], mx[1], mx[2], mul, undo);
     if (threadIdx.x == 0) {
         p.fa[i] = mul;
-        p.fa[p.m + i] = inv;
+        p.ea[i] = undo;
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -463,11 +457,12 @@ __global__ __launch_bounds__(256) void backward_rows_kernel(BackwardPrep p) {
         return;
     }
     const int64_t i = blockIdx.x;
-    float mul, inv;
-    row_scale(p, i, mul, inv);
+    float mul;
+    int undo;
+    row_scale(p, i, mul, undo);
     if (threadIdx.x == 0) {
         p.fa[i] = mul;
-        p.fa[p.m + i] = inv;
+        p.ea[i] = undo;
     }
     if (p.bias_part) return;
     float d0[8], d1[8];
@@ -522,8 +517,9 @@ __device__ void prep_weights_t(const BackwardPrep &p, unsigned b) {
     if (r0 >= p.kp || k0 >= p.d_in) return;
     const PackedLayer w = p.w[l];
     const int64_t gi = fz_div((int)k0, p.g, 1.f / (float)p.g);
-    float mul, inv;
-    pow2_scale(p.fg[gi] * (float)((1 << BITS) - 1), mul, inv);
+    float mul;
+    int undo;
+    fz_pow2_scale(p.fg[gi] * (float)((1 << BITS) - 1), mul, undo);
     const int64_t pos = BITS * k0, j = pos >> 5, j1 = std::min<int64_t>(j + 1, p.nwords - 1);
     const int sh = (int)(pos & 31);
     float s[8], z[8];
@@ -568,7 +564,7 @@ __device__ void prep_weights_t(const BackwardPrep &p, unsigned b) {
         for (int e = 0; e < 8; ++e) v[e] = (c[e].at(k) - z[e]) * s[e];
         put_planes(p.W16 + operand_at(col, l * p.kp + r0, p.planes_w * p.layers * p.kp), p.layers * p.kp * 256,
                    p.planes_w, 0, v);
-        if (l == 0 && r0 == 0) p.fw[col] = inv;
+        if (l == 0 && r0 == 0) p.ew[col] = undo;
     }
 }
 
@@ -606,7 +602,7 @@ struct Gemm {
     int64_t a_plane, b_plane;   // elements between the planes of a row
     int64_t m, n;
     int layers;                 // 2: the gated pair's forward product
-    const float *fa, *fw;       // inverse factors [m], [layers * n]
+    const int *ea, *ew;         // exponents that undo the operands' factors [m], [layers * n]
     const void *bias[2];
     int bias_bf16, act;
     const void *residual;
@@ -623,7 +619,8 @@ struct Gemm {
 // of both layers when gated: what depends on the columns alone ...
 template <bool GATED, int W>
 struct Columns {
-    f32x4 fw[GATED ? 2 : 1], bias[GATED ? 2 : 1];
+    i32x4 ew[GATED ? 2 : 1];
+    f32x4 bias[GATED ? 2 : 1];
     __device__ __forceinline__ static f32x4 load(const void *x, int64_t at, int bf16) {
         if constexpr (W == 4) return fz_ld4(x, at, bf16);
         return f32x4{fz_ld(x, at, bf16), 0.f, 0.f, 0.f};
@@ -631,14 +628,17 @@ struct Columns {
     __device__ __forceinline__ Columns(const Gemm &p, int64_t n) {
 #pragma unroll
         for (int l = 0; l < (GATED ? 2 : 1); ++l) {
-            fw[l] = load(p.fw, l * p.n + n, 0);
+            if constexpr (W == 4)
+                ew[l] = *(const i32x4 *)(p.ew + l * p.n + n);
+            else
+                ew[l] = i32x4{p.ew[l * p.n + n], 0, 0, 0};
             bias[l] = p.bias[l] ? load(p.bias[l], n, p.bias_bf16) : f32x4{0.f, 0.f, 0.f, 0.f};
         }
     }
 };
 // ... and row i's outputs at columns n .. from their sums
 template <bool GATED, int W>
-__device__ __forceinline__ void epilogue(const Gemm &p, const Columns<GATED, W> &col, int64_t i, int64_t n, float fa,
+__device__ __forceinline__ void epilogue(const Gemm &p, const Columns<GATED, W> &col, int64_t i, int64_t n, int ea,
                                          f32x4 z, f32x4 u) {
     const int64_t o = i * p.n + n;
     auto store = [&](void *x, f32x4 v) {
@@ -647,7 +647,8 @@ __device__ __forceinline__ void epilogue(const Gemm &p, const Columns<GATED, W> 
         else
             fz_st(x, o, v[0], p.out_bf16);
     };
-    z = z * fa * col.fw[0] + col.bias[0];
+#pragma unroll
+    for (int e = 0; e < W; ++e) z[e] = fz_ldexp(z[e], ea + col.ew[0][e]) + col.bias[0][e];
     if (p.pre[0]) store(p.pre[0], z);
     f32x4 y = z;
     fz_with_act(p.act, [&](auto act) {
@@ -655,7 +656,8 @@ __device__ __forceinline__ void epilogue(const Gemm &p, const Columns<GATED, W> 
         for (int e = 0; e < W; ++e) y[e] = fz_act<decltype(act)::value>(z[e]);
     });
     if constexpr (GATED) {
-        u = u * fa * col.fw[1] + col.bias[1];
+#pragma unroll
+        for (int e = 0; e < W; ++e) u[e] = fz_ldexp(u[e], ea + col.ew[GATED][e]) + col.bias[GATED][e];
         if (p.pre[1]) store(p.pre[1], u);
         y *= u;
     }
@@ -849,7 +851,7 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
 
     // lane (h, li), register 4 q + e of tile (j, i) <-> column 8 q + 4 h + e, row li
     const int tid = threadIdx.x;
-    float *fas = (float *)lds + 2 * 64 * EROW;
+    int *eas = (int *)lds + 2 * 64 * EROW;
     auto leave = [&](auto width, const float *out, int i) {
         constexpr int W = decltype(width)::value, TPR = COLS / W;   // threads per row of outputs
         const int c = W * (tid % TPR);
@@ -877,12 +879,12 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
                     z[e] = out[rr * EROW + c + e];
                     if (GATED) u[e] = out[rr * EROW + BN / 2 + c + e];
                 }
-                epilogue<GATED, W>(p, col, row, n, fas[row - m0], z, u);
+                epilogue<GATED, W>(p, col, row, n, eas[row - m0], z, u);
             }
         }
     };
-    // the tile's row factors (visible behind the first barrier below)
-    for (int r = tid; r < BM; r += 256) fas[r] = m0 + r < p.m ? p.fa[m0 + r] : 0.f;
+    // the tile's row exponents (visible behind the first barrier below)
+    for (int r = tid; r < BM; r += 256) eas[r] = m0 + r < p.m ? p.ea[m0 + r] : 0;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
         float *out = (float *)lds + (i & 1) * 64 * EROW;
@@ -921,7 +923,7 @@ __global__ __launch_bounds__(256) void split_reduce_kernel(Gemm p) {
             if (GATED) u[0] += u0[0];
         }
     }
-    epilogue<GATED, W>(p, Columns<GATED, W>(p, n), i, n, p.fa[i], z, u);
+    epilogue<GATED, W>(p, Columns<GATED, W>(p, n), i, n, p.ea[i], z, u);
 }
 
 int64_t pad_stage(int64_t k) { return cdiv(k, GK) * GK; }
@@ -962,7 +964,8 @@ struct Layout {
 };
 
 struct ForwardWs {
-    float *fw, *fa, *part;
+    int *ew, *ea;
+    float *part;
     uint16_t *W16, *A16;
     size_t bytes;
     int planes_a, planes_w, passes;
@@ -977,8 +980,8 @@ ForwardWs forward_layout(const FusedShape &s, char *base) {
     w.rows = std::min(s.m, DENSE_ROWS);
     w.plan = plan_gemm(w.rows, s.d_out, s.layers, (int)(w.kp / GK) * w.passes);
     Layout l(base);
-    w.fw = l.take<float>(s.layers * s.d_out);
-    w.fa = l.take<float>(w.rows);
+    w.ew = l.take<int>(s.layers * s.d_out);
+    w.ea = l.take<int>(w.rows);
     w.W16 = l.take<uint16_t>(s.layers * pad_tile(s.d_out) * w.planes_w * w.kp);
     w.A16 = l.take<uint16_t>(pad_tile(w.rows) * w.planes_a * w.kp);
     w.part = l.take<float>(w.plan.nsplit > 1 ? w.plan.nsplit * s.layers * w.rows * pad_quad(s.d_out) : 0);
@@ -990,7 +993,8 @@ ForwardWs forward_layout(const FusedShape &s, char *base) {
 int dz_rows(int64_t m) { return m > 1024 ? DZ_ROWS_MANY : DZ_ROWS; }
 
 struct BackwardWs {
-    float *fw, *fg, *fa, *part, *bias;
+    int *ew, *ea;
+    float *fg, *fa, *part, *bias;
     uint16_t *W16, *D16;
     size_t bytes;
     int planes_a, planes_w, passes;
@@ -1005,9 +1009,10 @@ BackwardWs backward_layout(const FusedShape &s, char *base) {
     w.rows = std::min(s.m, DENSE_ROWS);
     w.plan = plan_gemm(w.rows, s.d_in, 1, (int)(w.kp / GK) * s.layers * w.passes);
     Layout l(base);
-    w.fw = l.take<float>(s.d_in);
+    w.ew = l.take<int>(s.d_in);
     w.fg = l.take<float>(s.ngroups);
-    w.fa = l.take<float>(2 * w.rows);
+    w.fa = l.take<float>(w.rows);
+    w.ea = l.take<int>(w.rows);
     w.W16 = l.take<uint16_t>(pad_tile(s.d_in) * w.planes_w * s.layers * w.kp);
     w.D16 = l.take<uint16_t>(pad_tile(w.rows) * w.planes_a * s.layers * w.kp);
     w.bias = l.take<float>(cdiv(w.rows, dz_rows(w.rows)) * s.layers * s.d_out);
@@ -1095,7 +1100,7 @@ hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st) {
         p.kp = w.kp;
         p.A16 = w.A16;
         p.planes_a = w.planes_a;
-        p.fa = w.fa;
+        p.ea = w.ea;
         p.pairs = p.perm && p.vec && s.in_bf16 && (size_t)s.d_in * 4 <= PREP_LDS_MAX;
         for (int l = 0; l < s.layers; ++l) p.w[l] = a.w[l];
         p.d_out = s.d_out;
@@ -1105,7 +1110,7 @@ hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st) {
         p.layers = s.layers;
         p.W16 = w.W16;
         p.planes_w = w.planes_w;
-        p.fw = w.fw;
+        p.ew = w.ew;
         p.row_blocks = cdiv(m, 2);
         p.kchunks = (int)cdiv(w.kp, FW_K);
         // the weights once, with the first rows
@@ -1129,8 +1134,8 @@ hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st) {
         g.m = m;
         g.n = s.d_out;
         g.layers = s.layers;
-        g.fa = w.fa;
-        g.fw = w.fw;
+        g.ea = w.ea;
+        g.ew = w.ew;
         g.bias_bf16 = a.bias_bf16;
         g.act = a.act;
         const int64_t o = i0 * s.d_out;
@@ -1177,6 +1182,7 @@ hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st) {
         p.D16 = w.D16;
         p.planes_a = w.planes_a;
         p.fa = w.fa;
+        p.ea = w.ea;
         p.bias_part = bias ? w.bias : nullptr;
         p.perm = a.perm;
         p.d_in = s.d_in;
@@ -1191,7 +1197,7 @@ hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st) {
         p.fg = w.fg;
         p.W16 = w.W16;
         p.planes_w = w.planes_w;
-        p.fw = w.fw;
+        p.ew = w.ew;
         p.dz_cols = cdiv(w.kp, 256);
         p.dz_rows = dz_rows(m);
         const int64_t row_blocks = cdiv(m, p.dz_rows);
@@ -1234,8 +1240,8 @@ hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st) {
         g.m = m;
         g.n = s.d_in;
         g.layers = 1;
-        g.fa = w.fa + m;
-        g.fw = w.fw;
+        g.ea = w.ea;
+        g.ew = w.ew;
         g.Y = (void *)at(a.dA, i0 * s.d_in, s.out_bf16);
         g.out_bf16 = s.out_bf16;
         g.vec = s.d_in % 4 == 0 && aligned(a.dA, 16);

@@ -1,0 +1,74 @@
+"""GPU tests of the fused products with packed layers at the ends of their
+range: values near the largest of their type, slopes of far arguments, operands
+of very different sizes, rows wider than the LDS, and calls around their edges.
+
+Tolerances as in test_gpu_fused.py unless a test states its own.
+"""
+import numpy as np
+import pytest
+
+import oracle as O
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_fused import (DEV, DT, F64, Layer, P, check, mm, product_error, ref_backward, ref_gated,  # noqa: E402
+                            ref_linear, say, slope64, values)
+
+
+def scaled(layer, f):
+    """The layer with its scales times f, a power of two."""
+    for t in (layer.q.scales, layer.w, layer.mag):
+        t *= f
+    return layer
+
+
+def large_rows(rng, m, n, dt, lo, hi):
+    """Rows of normal values times channel factors, each row times 10^lo .. 10^hi."""
+    size = torch.from_numpy(10.0 ** rng.uniform(lo, hi, size=(m, 1))).to(DEV)
+    x = (values(rng, (m, n), "f32").to(F64) * size).to(DT[dt])
+    assert torch.isfinite(x).all()
+    return x
+
+
+# ---------------------------------------------------------------------------
+# large finite values: results that fp32 holds are finite, and as exact as any
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_large_rows_dense(dt):
+    rng = np.random.default_rng(1)
+    m, d_out, d_in = 200, 400, 1024
+    gate = Layer(rng, d_out, d_in, 4, 32, False, True)
+    up = Layer(rng, d_out, d_in, 4, 32, False, True, gate.perm)
+    A = large_rows(rng, m, d_in, dt, 29, 34)
+    (y, ey), _ = ref_linear(A, gate, None, "none", None, dt)
+    check(P.dequant_linear(A, gate.q), y, ey, "Y")
+    for layer in (gate, up):   # (so that H stays finite)
+        scaled(layer, 2.0 ** -60)
+    (h, eh), (g, eg), (u, eu) = ref_gated(A, gate, up, None, None, "silu", dt)
+    H, G, U = P.dequant_gated(A, gate.q, up.q, save_preact=True)
+    check(G, g, eg, "G")
+    check(U, u, eu, "U")
+    check(H, h, eh, "H")
+    dY = large_rows(rng, m, d_out, dt, 29, 33)
+    Z = values(rng, (m, d_out), dt)
+    (da, ea), _ = ref_backward(dY, [gate], [Z], "gelu", dt, dt)
+    check(P.dequant_linear_backward(dY, gate.q, "gelu", Z)[0], da, ea, "dA")
+    (da, ea), _ = ref_backward(dY, [gate, up], [Z, Z], "silu", dt, dt)
+    check(P.dequant_gated_backward(dY, gate.q, up.q, Z, Z)[0], da, ea, "dA gated")
+
+
+FACTORS = [(2.0 ** 110, 2.0 ** -115), (2.0 ** -110, 2.0 ** 115), (2.0 ** -70, 2.0 ** -56)]   # of weights, of rows
+
+
+def test_factors_out_of_fp32_dense():
+    """Rows and weights whose scale factors multiply to less or more than fp32
+    holds, with results that it does hold."""
+    rng = np.random.default_rng(2)
+    for weight, size in FACTORS:
+        l = scaled(Layer(rng, 96, 256, 4, 64, False, False), weight)
+        A, dY = (values(rng, (150, n), "f32") * size for n in (256, 96))
+        for got, ref, x in ((P.dequant_linear(A, l.q), mm(A, l.w.t()), A),
+                            (P.dequant_linear_backward(dY, l.q)[0], mm(dY, l.w), dY)):
+            bound = product_error([x], [l], x is dY, "f32") + 2.0 ** -24 * ref.abs() + 2.0 ** -149
+            check(got, ref, bound, f"{weight} {size}")
