@@ -333,13 +333,6 @@ struct SkinnyBackward {
     int wvec;               // four outputs' words, scales and zero points load together
 };
 
-// 2^t that brings v (> 0) to [2^14, 2^15), and 2^-t; 1 for 0
-__device__ __forceinline__ void f16_scale(float v, float &mul, float &inv) {
-    const int e = v == 0.f ? 14 : (int)((__builtin_bit_cast(unsigned, v) >> 23) & 255u) - 127;
-    const int t = max(-126, min(126, 14 - e));
-    mul = __builtin_bit_cast(float, (unsigned)(127 + t) << 23);
-    inv = __builtin_bit_cast(float, (unsigned)(127 - t) << 23);
-}
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
@@ -395,7 +388,8 @@ __global__ __launch_bounds__(256) void skinny_backward_kernel(SkinnyBackward p) 
     constexpr int AP = HI ? 2 : 1, LD = BK_RANGE + 8, PER = BK_RANGE / 64;
     __shared__ __attribute__((aligned(16))) _Float16 dz[AP][16][LD];
     __shared__ float red[4 * 16 * BK_COLS];
-    __shared__ float rowinv[16], gmax[8];
+    __shared__ float gmax[8];
+    __shared__ int rowexp[16];
     const FusedShape &s = p.f.s;
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -479,9 +473,10 @@ __global__ __launch_bounds__(256) void skinny_backward_kernel(SkinnyBackward p) 
         for (int b = 0; b < 4; ++b) {
             const int i = wave + 4 * b;
             if (i < s.m) {
-                float mul, inv;
-                f16_scale(mx[b], mul, inv);
-                if (lane == 0) rowinv[i] = inv;
+                float mul;
+                int undo;
+                fz_pow2_scale(mx[b], mul, undo);
+                if (lane == 0) rowexp[i] = undo;
 #pragma unroll
                 for (int c = 0; c < PER; ++c) {
                     float x = v[b][c] * mul;
@@ -504,8 +499,9 @@ __global__ __launch_bounds__(256) void skinny_backward_kernel(SkinnyBackward p) 
         }
     }
     __syncthreads();
-    float mul, inv;
-    f16_scale(gmax[gi - g0] * (float)((1 << BITS) - 1), mul, inv);
+    float mul;
+    int undo;
+    fz_pow2_scale(gmax[gi - g0] * (float)((1 << BITS) - 1), mul, undo);
 
     f32x4 acc[8];
 #pragma unroll
@@ -550,9 +546,9 @@ __global__ __launch_bounds__(256) void skinny_backward_kernel(SkinnyBackward p) 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int i = 4 * kg + e;
-        const float f = i < s.m ? rowinv[i] : 0.f;
+        const int both = (i < s.m ? rowexp[i] : 0) + undo;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) red[(wave * 16 + i) * BK_COLS + 8 * li + j] = acc[j][e] * f * inv;
+        for (int j = 0; j < 8; ++j) red[(wave * 16 + i) * BK_COLS + 8 * li + j] = fz_ldexp(acc[j][e], both);
     }
     __syncthreads();
     for (int x = tid; x < (int)s.m * BK_COLS; x += 256) {

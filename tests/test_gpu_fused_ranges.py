@@ -72,3 +72,27 @@ def test_factors_out_of_fp32_dense():
                             (P.dequant_linear_backward(dY, l.q)[0], mm(dY, l.w), dY)):
             bound = product_error([x], [l], x is dY, "f32") + 2.0 ** -24 * ref.abs() + 2.0 ** -149
             check(got, ref, bound, f"{weight} {size}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [1, 16])
+def test_large_rows_packed_backward(m, dt):
+    rng = np.random.default_rng(m)
+    d_out, d_in = 1400, 512
+    gate = Layer(rng, d_out, d_in, 4, 32, False, True)
+    up = Layer(rng, d_out, d_in, 4, 32, False, True, gate.perm)
+    dY, Z = large_rows(rng, m, d_out, dt, 29, 33), values(rng, (m, d_out), dt)
+    (da, ea), _ = ref_backward(dY, [gate], [None], "none", dt, dt)
+    check(P.dequant_linear_backward(dY, gate.q)[0], da, ea, "dA")
+    (da, ea), _ = ref_backward(dY, [gate, up], [Z, Z], "silu", dt, dt)
+    check(P.dequant_gated_backward(dY, gate.q, up.q, Z, Z)[0], da, ea, "dA gated")
+
+
+def test_factors_out_of_fp32_packed_backward():
+    rng = np.random.default_rng(2)
+    for weight, size in FACTORS:
+        l = scaled(Layer(rng, 300, 256, 4, 64, False, False), weight)
+        dY = values(rng, (9, 300), "f32") * size
+        ref = mm(dY, l.w)
+        bound = product_error([dY], [l], True, "f32") + 2.0 ** -24 * ref.abs() + 2.0 ** -149
+        check(P.dequant_linear_backward(dY, l.q)[0], ref, bound, f"{weight} {size}")
