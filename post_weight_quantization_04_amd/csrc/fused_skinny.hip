@@ -17,8 +17,12 @@ __device__ __forceinline__ int xcd_run(int b, int total) {
 
 // ---------------------------------------------------------------------------
 // Forward, few rows (up to 64 per work group): Z = A_p (q - z)^T per group on 16 x 16 x 32 bf16 MFMAs.
-// q - z is an integer in [-255, 255], exact in bf16, and a group's products
-// sum in fp32 before its scale: the same arithmetic for every output type.
+// q - z is an integer in [-255, 255], exact in bf16, and a chunk's products
+// sum in fp32 before the group's scale: the same arithmetic for every output
+// type.  The integers carry a factor 2^-(bits + 7), which the sums of a chunk
+// of 128 codes at most cannot grow out of again (without it, activations above
+// 1e35 overflowed there although the scaled sums did not); it leaves with the
+// waves' sums.
 // fp32 activations enter as three bf16 terms (24 bits), one MFMA each.
 //
 // A work group (8 waves) owns 16 V adjacent outputs of the layer (of both
@@ -31,8 +35,8 @@ __device__ __forceinline__ int xcd_run(int b, int total) {
 // has no branch around a load: rows past m and outputs past the end re-read
 // the last ones, units past a wave's run its last unit.  Measured: 1 row, 4096
 // x 4096, 4 bits 5.8 us (9.0 with a group's end looked for at every unit; the
-// loop has 51 instructions a unit and one MFMA); pair 11008 x 4096, 3 bits,
-// groups of 32, 1 row 33 us, 1.7 TB/s of words, scales and zero points (57
+// loop has 45 instructions a unit and one MFMA); pair 11008 x 4096, 3 bits,
+// groups of 32, 1 row 33 us, 1.7 TB/s of words, scales and zero points (50
 // instructions for eight codes of a lane).
 // ---------------------------------------------------------------------------
 constexpr int SK_NW = 8;
@@ -58,13 +62,19 @@ __device__ __forceinline__ void load_rows(const char *base, unsigned off, unsign
     }
 }
 
-// eight codes as bf16 integers q - z
+// eight codes as bf16 values (q - z) 2^-int_shift, zs: the zero point with that
+// factor (both products are exact: one rounding, of the difference, as without)
 template <int BITS>
-__device__ __forceinline__ bf16x8 int_weights(const Codes8<BITS> &c, float z) {
-    bf16x8 w;
+constexpr int int_shift() { return BITS + 7; }
+template <int BITS>
+constexpr float int_factor() { return 1.f / (float)(1 << int_shift<BITS>()); }
+template <int BITS>
+__device__ __forceinline__ bf16x8 int_weights(const Codes8<BITS> &c, float zs) {
+    u32x4 w;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = (__bf16)(c.at(e) - z);
-    return w;
+    for (int e = 0; e < 4; ++e)
+        w[e] = fz_pack_bf16(fmaf(c.at(2 * e), int_factor<BITS>(), -zs), fmaf(c.at(2 * e + 1), int_factor<BITS>(), -zs));
+    return __builtin_bit_cast(bf16x8, w);
 }
 
 // CH: units of a chunk (1 or 4) that lies in one group; 0: chunks of one unit
@@ -209,14 +219,14 @@ __global__ __launch_bounds__(64 * SK_NW) void skinny_forward_kernel(SkinnyForwar
         for (int l = 0; l < NL; ++l)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const unsigned zb = sl.z[l][j], s0 = sl.s0[l][j], s1 = sl.s1[l][HALF ? j : 0];
+                const float zs = __builtin_bit_cast(float, sl.z[l][j]) * int_factor<BITS>();
+                const unsigned s0 = sl.s0[l][j], s1 = sl.s1[l][HALF ? j : 0];
                 f32x4 dg[MT], dh[MT];
 #pragma unroll
                 for (int t = 0; t < MT; ++t) dg[t] = dh[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    const bf16x8 w = int_weights<BITS>(fz_codes8<BITS>(sl.w[c][l][0][j], sl.w[c][l][NWD - 1][j], sh),
-                                                       __builtin_bit_cast(float, zb));
+                    const bf16x8 w = int_weights<BITS>(fz_codes8<BITS>(sl.w[c][l][0][j], sl.w[c][l][NWD - 1][j], sh), zs);
                     const bf16x8 w0 = HALF && kg >= 2 ? bf16x8{} : w, w1 = kg < 2 ? bf16x8{} : w;
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
@@ -275,6 +285,7 @@ __global__ __launch_bounds__(64 * SK_NW) void skinny_forward_kernel(SkinnyForwar
                 z[l] = 0.f;
 #pragma unroll
                 for (int w = 0; w < SK_NW; ++w) z[l] += red[(w * NL + l) * 16 * ROWS + x];
+                z[l] = fz_ldexp(z[l], int_shift<BITS>());
             }
             const int64_t o = i * s.d_out + n;
             if (bias0) z[0] += fz_ld(bias0, n, p.f.bias_bf16);

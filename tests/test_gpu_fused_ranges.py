@@ -96,3 +96,25 @@ def test_factors_out_of_fp32_packed_backward():
         ref = mm(dY, l.w)
         bound = product_error([dY], [l], True, "f32") + 2.0 ** -24 * ref.abs() + 2.0 ** -149
         check(P.dequant_linear_backward(dY, l.q)[0], ref, bound, f"{weight} {size}")
+
+
+# chunks of four units, of one, of halves; one group over all columns
+@pytest.mark.parametrize("bits,g,d_in", [(4, 128, 1024), (3, 32, 992), (2, 48, 960), (8, -1, 1024), (8, 16, 512)])
+@pytest.mark.parametrize("m,dt", [(3, "bf16"), (3, "f32"), (100, "bf16")])
+def test_large_rows_packed_forward(m, dt, bits, g, d_in):
+    """A group's sum of a (q - z), before its scale, can pass fp32's largest
+    value where the scaled sum does not."""
+    rng = np.random.default_rng(m)
+    d_out = 8200 if bits == 4 else 300   # (two outputs per lane or one)
+    gate = Layer(rng, d_out, d_in, bits, g, False, True)
+    up = Layer(rng, d_out, d_in, bits, g, False, True, gate.perm)
+    A = large_rows(rng, m, d_in, dt, 33, 35.5)
+    (y, ey), _ = ref_linear(A, gate, None, "none", None, dt)
+    check(P.dequant_linear(A, gate.q), y, ey, "Y")
+    for layer in (gate, up):   # (so that H stays finite)
+        scaled(layer, 2.0 ** -60)
+    (h, eh), (gr, eg), (u, eu) = ref_gated(A, gate, up, None, None, "silu", dt)
+    H, G, U = P.dequant_gated(A, gate.q, up.q, save_preact=True)
+    check(G, gr, eg, "G")
+    check(U, u, eu, "U")
+    check(H, h, eh, "H")
