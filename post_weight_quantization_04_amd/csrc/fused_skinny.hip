@@ -23,7 +23,10 @@ __device__ __forceinline__ int xcd_run(int b, int total) {
 // of 128 codes at most cannot grow out of again (without it, activations above
 // 1e35 overflowed there although the scaled sums did not); it leaves with the
 // waves' sums.
-// fp32 activations enter as three bf16 terms (24 bits), one MFMA each.
+// fp32 activations enter as three bf16 terms of eight bits each, one MFMA per
+// term.  The terms are cut, not rounded: the largest finite values would round
+// to bf16's infinity, and a mask is cheaper than a conversion (11008 x 4096, 3
+// bits, one row: 25 us a call, 29 with conversions).
 //
 // A work group (8 waves) owns 16 V adjacent outputs of the layer (of both
 // layers of a gated pair, so that the product act(G) U is local) and the whole
@@ -199,18 +202,29 @@ __global__ __launch_bounds__(64 * SK_NW) void skinny_forward_kernel(SkinnyForwar
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 if constexpr (A32) {
+                    u32x4 term[3];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const unsigned bits = sl.a[c][t][e >> 2 & (AL - 1)][e & 3];
-                        const float x = __builtin_bit_cast(float, bits);
-                        const bool finite = fabsf(x) < __builtin_inff();   // (others only in the first term)
-                        const __bf16 b0 = (__bf16)x;
-                        const float x1 = finite ? x - (float)b0 : 0.f;
-                        const __bf16 b1 = (__bf16)x1;
-                        a[c][t][0][e] = b0;
-                        a[c][t][AP > 1 ? 1 : 0][e] = AP > 1 ? b1 : b0;
-                        a[c][t][AP - 1][e] = AP > 1 ? (__bf16)(x1 - (float)b1) : b0;
+                    for (int e = 0; e < 4; ++e) {
+                        float x[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const unsigned bits = sl.a[c][t][e >> 1 & (AL - 1)][2 * (e & 1) + h];
+                            x[h] = __builtin_bit_cast(float, bits);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 3; ++q) {
+                            const unsigned b0 = __builtin_bit_cast(unsigned, x[0]), b1 = __builtin_bit_cast(unsigned, x[1]);
+                            term[q][e] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);   // both upper halves
+                            // (an infinity only in the first term; NaN in all, also where its
+                            // payload was cut off)
+                            x[0] = q == 0 && fabsf(x[0]) == __builtin_inff()
+                                       ? 0.f : x[0] - __builtin_bit_cast(float, b0 & 0xffff0000u);
+                            x[1] = q == 0 && fabsf(x[1]) == __builtin_inff()
+                                       ? 0.f : x[1] - __builtin_bit_cast(float, b1 & 0xffff0000u);
+                        }
                     }
+#pragma unroll
+                    for (int q = 0; q < AP; ++q) a[c][t][q] = __builtin_bit_cast(bf16x8, term[q]);
                 } else {
                     a[c][t][0] = __builtin_bit_cast(bf16x8, sl.a[c][t][0]);
                 }

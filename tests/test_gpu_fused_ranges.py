@@ -118,3 +118,20 @@ def test_large_rows_packed_forward(m, dt, bits, g, d_in):
     check(G, gr, eg, "G")
     check(U, u, eu, "U")
     check(H, h, eh, "H")
+
+
+@pytest.mark.parametrize("g", [48, 32, 128])
+def test_fp32_values_above_bf16(g):
+    """Finite fp32 activations beyond the largest bf16 value, few rows."""
+    rng = np.random.default_rng(g)
+    l = scaled(Layer(rng, 200, 384, 4, g, False, False), 2.0 ** -40)
+    A = values(rng, (5, 384), "f32")
+    top = torch.finfo(torch.float32).max
+    A[0, 7], A[1, 11], A[1, 350], A[2, 0] = top, -top, top * (1 - 2.0 ** -10), 3.3961775e38
+    (y, ey), _ = ref_linear(A, l, None, "none", None, "f32")
+    check(P.dequant_linear(A, l.q), y, ey, "Y")
+    # NaN whose payload lies in the bits that bf16 does not hold
+    A.view(torch.int32)[3, 9] = 0x7f800001
+    got = P.dequant_linear(A, l.q)
+    assert torch.isnan(got[3]).all()
+    check(got[:3], y[:3], ey[:3], "the other rows")
