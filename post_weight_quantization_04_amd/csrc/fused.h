@@ -109,12 +109,13 @@ __device__ __forceinline__ float fz_act(float z) {
     return z;
 }
 
-// (beyond |z| = 64 every slope is 0 or 1 in fp32: clamped there, so that no
-// product of a vanishing and an overflowing factor arises; NaN stays NaN)
+// (beyond |z| = 128 every slope is 0 or 1 in fp32, silu's, the slowest to
+// vanish, from -108 on: clamped there, so that no product of a vanishing and an
+// overflowing factor arises; NaN stays NaN)
 template <int ACT>
 __device__ __forceinline__ float fz_slope(float z) {
     float p, q;
-    z = z > 64.f ? 64.f : (z < -64.f ? -64.f : z);
+    z = z > 128.f ? 128.f : (z < -128.f ? -128.f : z);
     if constexpr (ACT == 1) return z > 0.f ? 1.f : 0.f;
     if constexpr (ACT == 2)
         return 0.5f * erfcf(-z * FZ_SQRT_HALF) +

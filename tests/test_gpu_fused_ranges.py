@@ -135,3 +135,45 @@ def test_fp32_values_above_bf16(g):
     got = P.dequant_linear(A, l.q)
     assert torch.isnan(got[3]).all()
     check(got[:3], y[:3], ey[:3], "the other rows")
+
+
+# ---------------------------------------------------------------------------
+# slopes
+# ---------------------------------------------------------------------------
+def slope_bound(act, z):
+    """Error of a slope, sigmoid(x) + z x' sigmoid(x) sigmoid(-x) or Phi(z) +
+    z phi(z), in fp32: the argument of the exponential (of erfc) is off by a few
+    times 2^-24 of itself, functions and products by a few steps of the two
+    terms, and a factor below the smallest normal number may be taken for 0."""
+    if act in ("none", "relu"):
+        return torch.zeros_like(z)
+    if act == "gelu":
+        p, dp, grow = 0.5 * torch.erfc(-z / 2 ** 0.5), torch.exp(-z * z / 2) / (2 * np.pi) ** 0.5, 1.0
+        moved = 4 * z.abs() * dp * (1 + z * z)
+    else:
+        c = 2 * (2 / np.pi) ** 0.5
+        x, grow = (z, 1.0) if act == "silu" else (c * (z + 0.044715 * z ** 3), c * (1 + 3 * 0.044715 * z * z))
+        p = torch.sigmoid(x)
+        dp = p * torch.sigmoid(-x) * grow
+        moved = 4 * x.abs() * (p * torch.sigmoid(-x) + z.abs() * dp)
+    return 2.0 ** -23 * (moved + 16 * (p + z.abs() * dp)) + 2.0 ** -126 * (1 + z.abs() * grow)
+
+
+@pytest.mark.parametrize("m", [1, 20])
+@pytest.mark.parametrize("act", list(P.ACTIVATIONS))
+def test_slopes(act, m):
+    """The slope itself, as the bias gradient of one row of ones."""
+    z = torch.cat([torch.arange(-1120, 1121, device=DEV) / 8, torch.tensor([1e4, -1e4, 1e30, -1e30], device=DEV)])
+    rng = np.random.default_rng(3)
+    l = Layer(rng, len(z), 64, 4, 32, True, False)
+    dY, Z = torch.zeros(m, len(z), device=DEV), z.repeat(m, 1)
+    dY[m // 2] = 1
+    _, db = P.dequant_linear_backward(dY, l.q, act, Z, True)
+    near = z.to(F64).clamp(-200, 200)   # (beyond, every slope is 0 or 1 to the last bit)
+    err, bound = (db.to(F64) - slope64(act, near)).abs(), slope_bound(act, near)
+    worst = (err - bound).argmax()
+    say(f"  {act}: worst at z = {float(z[worst])}: {float(db[worst])}, bound {float(bound[worst]):.3g}")
+    assert (err <= bound).all()
+    ones = torch.ones_like(Z)
+    _, dbg, _ = P.dequant_gated_backward(dY, l.q, l.q, Z, ones, act, True)
+    assert ((dbg.to(F64) - slope64(act, near)).abs() <= bound).all()
