@@ -131,6 +131,13 @@ __device__ __forceinline__ float fz_slope(float z) {
     return 1.f;
 }
 
+// A gate's gradient d u act'(z): the slope first, which is below 1.13, as d u
+// can overflow where the slope brings it back (or is 0)
+template <int ACT>
+__device__ __forceinline__ float fz_gate_grad(float d, float u, float z) {
+    return d * fz_slope<ACT>(z) * u;
+}
+
 // f(std::integral_constant<int, act>) for a run-time activation
 template <class F>
 __host__ __device__ __forceinline__ void fz_with_act(int act, F f) {

@@ -357,7 +357,7 @@ __device__ __forceinline__ void put_dz8(const BackwardPrep &p, int64_t i, int64_
         if (p.layers == 2) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                d0[e] = d[e] * u[e] * fz_slope<ACT>(z[e]);
+                d0[e] = fz_gate_grad<ACT>(d[e], u[e], z[e]);
                 d1[e] = d[e] * fz_act<ACT>(z[e]);
             }
         } else {

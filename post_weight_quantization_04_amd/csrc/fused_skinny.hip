@@ -389,7 +389,7 @@ __global__ __launch_bounds__(256) void skinny_dz_kernel(SkinnyBackward p, int wr
             constexpr int ACT = decltype(act)::value;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                const float d0 = dy[b] * u[b] * fz_slope<ACT>(z[b]), d1 = dy[b] * fz_act<ACT>(z[b]);
+                const float d0 = fz_gate_grad<ACT>(dy[b], u[b], z[b]), d1 = dy[b] * fz_act<ACT>(z[b]);
                 const int64_t i = ib + 4 * b;
                 if (i >= s.m) break;
                 sum[0] += d0;

@@ -177,3 +177,23 @@ def test_slopes(act, m):
     ones = torch.ones_like(Z)
     _, dbg, _ = P.dequant_gated_backward(dY, l.q, l.q, Z, ones, act, True)
     assert ((dbg.to(F64) - slope64(act, near)).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("m", [2, 40])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gate_gradient_of_large_factors(m, dt):
+    """dG = dH U act'(G) where dH U passes fp32's largest value and act'(G)
+    brings it back, or is 0."""
+    rng = np.random.default_rng(m)
+    l = Layer(rng, 64, 64, 4, 32, True, False)
+    dH, U = torch.full((m, 64), 2.0 ** 70, device=DEV).to(DT[dt]), torch.full((m, 64), 2.0 ** 66, device=DEV).to(DT[dt])
+    G = torch.full((m, 64), -40.0, device=DEV).to(DT[dt])
+    dA, dbg, dbu = P.dequant_gated_backward(dH, l.q, l.q, G, U, "relu", True)
+    assert not dbg.any() and not dbu.any() and not dA.any()
+    dA, dbg, dbu = P.dequant_gated_backward(dH, l.q, l.q, G, U, "silu", True)
+    p = 1 / (1 + np.exp(40.0))
+    dg, du = 2.0 ** 136 * (p - 40 * p * (1 - p)) * m, 2.0 ** 70 * -40 * p * m
+    # (the sigmoid's exponent is off by 40 times a few 2^-24; m terms of a sum)
+    for got, want in ((dbg, dg), (dbu, du)):
+        assert ((got.to(F64) - want).abs() <= abs(want) * (100 + m) * 2.0 ** -23).all()
+    assert torch.isfinite(dA).all()
