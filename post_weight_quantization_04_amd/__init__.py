@@ -469,10 +469,21 @@ class _FusedCall:
     def pair(self, gate, up):
         if (up.d_in, up.bits, up.group_size, up.scales.shape[1]) != (self.d_in, self.bits, self.group, self.d_out):
             raise ValueError("the layers must have the same sizes, bits and group_size")
-        if up.act_order != gate.act_order or (up.act_order and up.perm.data_ptr() != self.perm):
+        if up.act_order != gate.act_order or (up.act_order and not self.same_order(gate.perm, up.perm)):
             raise ValueError("the layers must share one perm (quantize_layers gives them one)")
         if _torch().is_grad_enabled() and (up.scales.requires_grad or up.zeros.requires_grad):
             self.no_grad()
+
+    def same_order(self, a, b):
+        """One tensor, or two of equal values (compared on the call's stream, and waited for)."""
+        if _operand(b, "perm", a.dtype, a.shape, self.device) == self.perm:
+            return True
+        torch = _torch()
+        with self:
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("during a graph's capture the layers must share one perm tensor (two cannot be "
+                                 "compared)")
+            return torch.equal(a, b)
 
     def take(self, t, name, dtype, shape):
         """An optional operand's pointer."""
@@ -573,7 +584,9 @@ def dequant_gated(A, gate: "QuantizedLayer", up: "QuantizedLayer", activation="s
     the gated half of a feed-forward block in one call.
 
     gate, up: packed layers of the same sizes, bits and group_size sharing one
-    perm (quantize_layers).  Returns H [m, d_ff] in out_dtype (A's dtype by
+    perm (quantize_layers).  Equal perms in two tensors, as a reload gives, are
+    taken too, but comparing them waits for the device at every call and cannot
+    be captured: give both layers one tensor (up.perm = gate.perm).  Returns H [m, d_ff] in out_dtype (A's dtype by
     default), or (H, G, U) with both pre-activations when save_preact.  Other
     arguments as for dequant_linear."""
     f = _FusedCall(A, "A", gate, activation, out_dtype, workspace, stream)

@@ -197,3 +197,40 @@ def test_gate_gradient_of_large_factors(m, dt):
     for got, want in ((dbg, dg), (dbu, du)):
         assert ((got.to(F64) - want).abs() <= abs(want) * (100 + m) * 2.0 ** -23).all()
     assert torch.isfinite(dA).all()
+
+
+# ---------------------------------------------------------------------------
+# the binding
+# ---------------------------------------------------------------------------
+def test_pair_with_equal_orders_in_two_tensors():
+    """Layers read back from storage hold equal orders in tensors of their own."""
+    rng = np.random.default_rng(7)
+    gate = Layer(rng, 64, 128, 4, 32, True, True)
+    up = Layer(rng, 64, 128, 4, 32, True, True, gate.perm)
+    again = P.QuantizedLayer(up.q.qpacked, up.q.scales, up.q.zeros, up.q.perm.clone(), 4, 32, 128, True)
+    side = torch.cuda.Stream()
+    for m in (3, 150):
+        A, dH, G, U = (values(rng, (m, n), "bf16", True) for n in (128, 64, 64, 64))
+        side.wait_stream(torch.cuda.current_stream())
+        for stream in (None, side):
+            got = P.dequant_gated(A, gate.q, again, stream=stream)
+            grad = P.dequant_gated_backward(dH, gate.q, again, G, U, stream=stream)[0]
+            side.synchronize()
+            assert torch.equal(got, P.dequant_gated(A, gate.q, up.q))
+            assert torch.equal(grad, P.dequant_gated_backward(dH, gate.q, up.q, G, U)[0])
+    again.perm[:2] = again.perm[:2].flip(0)
+    with pytest.raises(ValueError, match="share one perm"):
+        P.dequant_gated(A, gate.q, again)
+    again.perm = gate.perm[:-1].contiguous()
+    with pytest.raises(ValueError, match="perm"):
+        P.dequant_gated(A, gate.q, again)
+    again.perm = gate.perm.clone()
+    P.dequant_gated(A, gate.q, up.q)   # (warm)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="share one perm"):   # (the values cannot be looked at here)
+            P.dequant_gated(A, gate.q, again)
+        held = P.dequant_gated(A, gate.q, up.q)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(held, P.dequant_gated(A, gate.q, up.q))
