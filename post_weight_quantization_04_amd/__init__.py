@@ -166,14 +166,14 @@ def _check(status: int) -> None:
         raise GptqError(status, _lib().gptq_last_error().decode(errors="replace"))
 
 
-_TORCH = None
+_TORCH = _FORWARD_AD = None
 
 
 def _torch():
-    global _TORCH
+    global _TORCH, _FORWARD_AD
     if _TORCH is None:
         import torch  # memory and streams only
-        _TORCH = torch
+        _TORCH, _FORWARD_AD = torch, torch.autograd.forward_ad
     return _TORCH
 
 
@@ -455,8 +455,7 @@ class _FusedCall:
         self.given_ws = workspace
         if workspace is not None:
             _operand(workspace, "workspace", workspace.dtype, workspace.shape, device)
-        if torch.is_grad_enabled() and (x.requires_grad or q.scales.requires_grad or q.zeros.requires_grad):
-            self.no_grad()
+        self.no_grad(x, q.scales, q.zeros)
 
     def layer(self, q):
         """A packed layer's pointers (codes, scales, zero points)."""
@@ -471,8 +470,7 @@ class _FusedCall:
             raise ValueError("the layers must have the same sizes, bits and group_size")
         if up.act_order != gate.act_order or (up.act_order and not self.same_order(gate.perm, up.perm)):
             raise ValueError("the layers must share one perm (quantize_layers gives them one)")
-        if _torch().is_grad_enabled() and (up.scales.requires_grad or up.zeros.requires_grad):
-            self.no_grad()
+        self.no_grad(up.scales, up.zeros)
 
     def same_order(self, a, b):
         """One tensor, or two of equal values (compared on the call's stream, and waited for)."""
@@ -489,14 +487,24 @@ class _FusedCall:
         """An optional operand's pointer."""
         if t is None:
             return None
-        if _torch().is_grad_enabled() and getattr(t, "requires_grad", False):
-            self.no_grad()
-        return _operand(t, name, dtype, shape, self.device)
+        p = _operand(t, name, dtype, shape, self.device)
+        self.no_grad(t)
+        return p
 
     @staticmethod
-    def no_grad():
-        raise ValueError("autograd does not see through the fused products: call them under torch.no_grad() (or "
-                         "inside a torch.autograd.Function) and their _backward calls for the gradients")
+    def no_grad(*tensors):
+        """Raises for operands whose gradients, or forward-mode tangents, would be dropped."""
+        if _TORCH.is_grad_enabled():
+            for t in tensors:
+                if t.requires_grad:
+                    raise ValueError("autograd does not see through the fused products: call them under "
+                                     "torch.no_grad() (or inside a torch.autograd.Function) and their _backward "
+                                     "calls for the gradients")
+        if _FORWARD_AD._current_level >= 0:
+            for t in tensors:
+                if _FORWARD_AD.unpack_dual(t).tangent is not None:
+                    raise ValueError("forward-mode tangents do not pass through the fused products: give them the "
+                                     "primals of dual tensors")
 
     def empty(self, shape, dtype=None):
         return _torch().empty(shape, dtype=dtype or self.out_dtype, device=self.device)

@@ -234,3 +234,32 @@ def test_pair_with_equal_orders_in_two_tensors():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(held, P.dequant_gated(A, gate.q, up.q))
+
+
+def test_forward_mode_tangents_are_refused():
+    import torch.autograd.forward_ad as fwAD
+
+    rng = np.random.default_rng(8)
+    gate = Layer(rng, 64, 128, 4, 32, True, True)
+    up = Layer(rng, 64, 128, 4, 32, True, True, gate.perm)
+    A, dY, Z = (values(rng, (4, n), "f32") for n in (128, 64, 64))
+    b = values(rng, (64,), "f32")
+    with fwAD.dual_level():
+        dual = lambda t: fwAD.make_dual(t, torch.ones_like(t))   # noqa: E731
+        calls = [lambda: P.dequant_linear(dual(A), gate.q), lambda: P.dequant_linear(A, gate.q, bias=dual(b)),
+                 lambda: P.dequant_linear(A, gate.q, residual=dual(Z)),
+                 lambda: P.dequant_linear_backward(dual(dY), gate.q),
+                 lambda: P.dequant_linear_backward(dY, gate.q, "silu", dual(Z)),
+                 lambda: P.dequant_gated(dual(A), gate.q, up.q),
+                 lambda: P.dequant_gated(A, gate.q, up.q, bias_up=dual(b)),
+                 lambda: P.dequant_gated(A, gate.q, P.QuantizedLayer(up.q.qpacked, dual(up.q.scales), up.q.zeros,
+                                                                     up.q.perm, 4, 32, 128, True)),
+                 lambda: P.dequant_gated_backward(dY, gate.q, up.q, Z, dual(Z))]
+        for i, call in enumerate(calls):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="tangent"):   # (which does not stop tangents)
+                call()
+        plain = P.dequant_linear(A, gate.q)   # operands without tangents pass
+        assert torch.equal(P.dequant_linear(fwAD.unpack_dual(dual(A)).primal, gate.q), plain)
+    assert torch.equal(P.dequant_linear(A, gate.q), plain)
