@@ -277,16 +277,24 @@ GPTQ_API gptq_status gptq_dequant_matmul(const void *A, gptq_dtype a_dtype, int6
  *              preact may be NULL when act is NONE.
  *   dbias*     fp32 outputs, overwritten (not accumulated); NULL: not formed.
  *   residual   NULL: none.
- * Numerics: fp32 sums, one rounding of each output to its dtype.  With an F32
- * output every product keeps fp32 accuracy (operands of 22 significand bits at
- * least); with a BF16 output the weights, and in the backward calls dZ, may be
- * rounded to 11 significand bits on the way (an eighth of the output's own
- * rounding each).  What is rounded so shares a power-of-two range of 2^29: a
- * row of activations or of dZ (in the gated pair's backward call measured from
- * max|dH| max(max|G|, max|U|) of the row), the weights of a layer's row in a
- * forward call, those of a group of columns in a backward one; values below
- * the range lose precision gradually.  Values of A, dY, dH, Z, G and U that
- * are not finite reach the results of their own row only.  All results are
+ * Numerics: fp32 sums, one rounding of each output to its dtype.  The operands
+ * of a product may be rounded on the way, all that share a largest value M
+ * alike:
+ *   F32 output   to 22 significand bits down to 2^-17 M, and to within 2^-39 M
+ *                below; of a product of two operands up to 2^-22 of it is
+ *                dropped.
+ *   BF16 output  weights, dZ and F32 activations to 11 bits (an eighth of the
+ *                output's own rounding each) down to 2^-28 M, and to within
+ *                2^-39 M below; BF16 activations enter exactly down to 2^-31 M.
+ * M is, for activations, the largest of their row; for dZ max|dY| of the row
+ * (in the gated pair's backward call max|dH| max(max|G|, max|U|)) times 1.13;
+ * for weights 2^bits - 1 times the largest scale, of the layer's row in a
+ * forward call, of a group over all outputs (of both layers) in a backward one.
+ * Calls of few rows round less.  A caller for whom 11 bits are too few asks for
+ * an F32 output.  Finite operands of any size give finite results where dZ, the
+ * terms of a sum and the sum itself are; activations below 2^-95 may lose
+ * precision.  Values of A, dY, dH, Z, G and U that are not finite reach the
+ * results of their own row only (and the bias gradients).  All results are
  * deterministic.
  * workspace  device scratch of the matching size query's bytes (may be NULL
  *            when that is 0), 256-byte aligned.  Its contents need not be

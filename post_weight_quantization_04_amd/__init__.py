@@ -538,6 +538,8 @@ def dequant_linear(A, q: "QuantizedLayer", bias=None, activation="none", residua
     ACTIVATIONS.  Returns Y, or (Y, Z) with the pre-activation Z = A W_hat^T +
     bias when save_preact.  workspace: any 256-byte aligned device tensor of at least
     dequant_linear_workspace_size bytes (allocated when absent or too small).
+    With a bfloat16 result the weights, and float32 activations, may be rounded
+    to 11 bits on the way; out_dtype=torch.float32 holds them to 22.
     Not differentiable by autograd: see dequant_linear_backward."""
     f = _FusedCall(A, "A", q, activation, out_dtype, workspace, stream)
     m, d_in = A.shape

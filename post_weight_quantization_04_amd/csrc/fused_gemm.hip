@@ -19,14 +19,16 @@
 // MB in 287 us).
 //
 // f16 operands.  Every row of A16 / D16 is scaled by a power of two that
-// brings its largest finite magnitude to [2^14, 2^15), every row n of W16 by
+// brings its largest finite magnitude M to [2^14, 2^15), every row n of W16 by
 // one that does the same for its weights; the epilogue undoes both exactly.
-// bf16 activations are then exact in f16 (down to 2^-29 of their row's
-// largest), weights and computed gradients are rounded once to 11 bits, an
-// eighth of a bf16 result's own rounding.  For an F32 result the operands are
-// split in two f16 planes, x = hi + lo (22 bits), and the product is three
-// passes over K, hi hi + hi lo + lo hi (two when the activations are exact),
-// which the matrix cores' fp32 accumulators add in one run.
+// bf16 activations are then exact in f16 (down to 2^-31 M), weights, computed
+// gradients and fp32 activations are rounded once to 11 bits, an eighth of a
+// bf16 result's own rounding (down to 2^-28 M; f16's smallest step leaves
+// 2^-39 M below).  For an F32 result the operands are split in two f16 planes,
+// x = hi + lo: 22 bits down to 2^-17 M, where lo meets f16's smallest step, and
+// 2^-39 M below.  The product is then three passes over K, hi hi + hi lo + lo
+// hi (two when the activations are exact), which the matrix cores' fp32
+// accumulators add in one run.
 #include "fused.h"
 
 #include <algorithm>

@@ -263,3 +263,46 @@ def test_forward_mode_tangents_are_refused():
         plain = P.dequant_linear(A, gate.q)   # operands without tangents pass
         assert torch.equal(P.dequant_linear(fwAD.unpack_dual(dual(A)).primal, gate.q), plain)
     assert torch.equal(P.dequant_linear(A, gate.q), plain)
+
+
+# ---------------------------------------------------------------------------
+# operands of very different sizes, to what the calls promise
+# ---------------------------------------------------------------------------
+def held(x, top, out):
+    """Largest error of operands x that share the largest value top."""
+    step, reach = (2.0 ** -22, 2.0 ** -17) if out == "f32" else (2.0 ** -11, 2.0 ** -28)
+    return torch.where(x >= reach * top, step * x, 2.0 ** -39 * top)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [3, 16, 200])
+def test_outliers_beside_small_values(m, out):
+    """One activation (one dZ) 2^8 to 2^26 times the others of its row meets a
+    column (row) of zero weights in most outputs: what is left has the
+    operands' errors relative to the outlier.  Weights differ by up to 2^16."""
+    rng = np.random.default_rng(m)
+    d_out, d_in, g = 256, 320, 64
+    l = Layer(rng, d_out, d_in, 4, g, False, False, spread=2.0 ** 8)
+    l.q.zeros.fill_(0)   # (w = s q)
+    codes = rng.integers(0, 16, size=(d_out, d_in))
+    codes[:200, 7] = 0
+    codes[9, :300] = 0
+    l.q.qpacked = torch.from_numpy(O.pack(codes, 4).view(np.int32)).to(DEV)
+    s = l.q.scales.to(F64).t()[:, torch.arange(d_in, device=DEV) // g]
+    l.w = s * torch.from_numpy(codes).to(DEV)
+    l.mag = l.w
+    for transposed in (False, True):
+        n, at = (d_out, 9) if transposed else (d_in, 7)
+        x = values(rng, (m, n), "f32")
+        x[:, at] = x.abs().amax(1) * torch.from_numpy(2.0 ** rng.integers(8, 27, size=m)).to(DEV).float()
+        x64, w = x.to(F64).abs(), l.w if transposed else l.w.t().contiguous()
+        # the weights' shared largest, scales times 15: of a layer's row forward, a group of columns backward
+        top = (15 * (s.amax(0) if transposed else s.amax(1)))[None].expand(w.shape)
+        ex, ew = held(x64, x64.amax(1, keepdim=True), out), held(w, top, out)
+        ref = mm(x, w)
+        bound = mm(ex, w) + mm(x64, ew) + mm(ex, ew) + 2.0 ** -22 * mm(x64, w)
+        bound = bound + 2.0 ** -24 * (max(g, 16) + x.shape[1] / 16 + 100) * mm(x64, w)
+        bound = bound + (2.0 ** -8 if out == "bf16" else 2.0 ** -24) * ref.abs() + 1e-37
+        call = P.dequant_linear_backward if transposed else P.dequant_linear
+        got = call(x, l.q, out_dtype=DT[out])
+        check(got[0] if transposed else got, ref, bound, f"{'dA' if transposed else 'Y'} {out}")
