@@ -306,3 +306,32 @@ def test_outliers_beside_small_values(m, out):
         call = P.dequant_linear_backward if transposed else P.dequant_linear
         got = call(x, l.q, out_dtype=DT[out])
         check(got[0] if transposed else got, ref, bound, f"{'dA' if transposed else 'Y'} {out}")
+
+
+# ---------------------------------------------------------------------------
+# activation order over wide layers
+# ---------------------------------------------------------------------------
+# two rows just above 64 KB of LDS, the 70B down projection, the most that is
+# staged, and the first width that is gathered one element at a time
+@pytest.mark.parametrize("d_in", [16392, 28672, 32768, 32776])
+@pytest.mark.parametrize("m", [129, 150])
+def test_wide_layers_in_activation_order(m, d_in):
+    """Bit for bit (a row's largest sum: 30 * 2^4 units of its finest scale per
+    column, below 2^24 over 32776 columns); captured and replayed as well."""
+    say(f"wide {m} x {d_in}")
+    rng = np.random.default_rng(d_in)
+    l = Layer(rng, 40, d_in, 4, 128, True, True)
+    A, dY = values(rng, (m, d_in), "bf16", True), values(rng, (m, 40), "bf16", True)
+    for out in ("bf16", "f32"):
+        assert torch.equal(P.dequant_linear(A, l.q, out_dtype=DT[out]), mm(A, l.w.t()).to(DT[out]))
+        assert torch.equal(P.dequant_linear_backward(dY, l.q, out_dtype=DT[out])[0], mm(dY, l.w).to(DT[out]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y = P.dequant_linear(A, l.q)
+    for _ in range(3):
+        A.copy_(values(rng, (m, d_in), "bf16", True))
+        eager = P.dequant_linear(A, l.q)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, eager) and torch.equal(Y, mm(A, l.w.t()).to(torch.bfloat16))
