@@ -39,7 +39,7 @@ __device__ __forceinline__ int xcd_run(int b, int total) {
 // the last ones, units past a wave's run its last unit.  Measured: 1 row, 4096
 // x 4096, 4 bits 5.8 us (9.0 with a group's end looked for at every unit; the
 // loop has 45 instructions a unit and one MFMA); pair 11008 x 4096, 3 bits,
-// groups of 32, 1 row 33 us, 1.7 TB/s of words, scales and zero points (50
+// groups of 32, 1 row 31 us, 1.8 TB/s of words, scales and zero points (50
 // instructions for eight codes of a lane).
 // ---------------------------------------------------------------------------
 constexpr int SK_NW = 8;
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(256) void gather_rows_kernel(const T *A, const int3
 // range enters LDS once per group (formed from dY and the saved
 // pre-activations by a kernel before, where there is an activation).  The groups' sums are added in range order by a second
 // kernel, which also moves the columns back to their original order.
-// Measured: 7 rows, 4096 x 4096, 4 bits 12.6 us + 2.8-3.8 us for the sums;
+// Measured: 7 rows, 4096 x 4096, 4 bits 13 us + 3-4 us for the sums;
 // 62% of the wave cycles wait (the loads before the first product, the
 // exchanges for the ranges, the barriers), the rest is the conversion.
 // ---------------------------------------------------------------------------
