@@ -291,11 +291,11 @@ GPTQ_API gptq_status gptq_dequant_matmul(const void *A, gptq_dtype a_dtype, int6
  * for weights 2^bits - 1 times the largest scale, of the layer's row in a
  * forward call, of a group over all outputs (of both layers) in a backward one.
  * Calls of few rows round less.  A caller for whom 11 bits are too few asks for
- * an F32 output.  Finite operands of any size give finite results where dZ, the
- * terms of a sum and the sum itself are; activations below 2^-95 may lose
- * precision.  Values of A, dY, dH, Z, G and U that are not finite reach the
- * results of their own row only (and the bias gradients).  All results are
- * deterministic.
+ * an F32 output.  Finite operands of any size give finite results where W_hat,
+ * dZ, the terms of a sum and the sum itself are; activations below 2^-95 and
+ * results below 2^-105 may lose precision.  Values of A, dY, dH, Z, G and U that
+ * are not finite reach the results of their own row only (and the bias
+ * gradients).  All results are deterministic.
  * workspace  device scratch of the matching size query's bytes (may be NULL
  *            when that is 0), 256-byte aligned.  Its contents need not be
  *            prepared and are not kept: calls of any sizes may share one as
