@@ -116,9 +116,10 @@ def _mx_values(x, fmt):
 
 
 def _pack(x, fmt):
-    """Codes and scale bytes: e4m3 one byte, e2m1 two to a byte, the even column in the low half."""
+    """Codes [rows][bytes] and scale bytes [steps of 128 columns][rows][4]: e4m3 one byte, e2m1 two to
+    a byte, the even column in the low half."""
     e, v = _mx(x, fmt)
-    scales = (e + 127).to(torch.uint8)
+    scales = (e + 127).to(torch.uint8).view(x.shape[0], -1, 4).transpose(0, 1)
     v = v.view(x.shape[0], -1)
     if fmt == "fp8":
         return v.to(torch.float8_e4m3fn).view(torch.uint8), scales
@@ -134,7 +135,7 @@ def _unpack(t):
     else:
         grid = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6], device=t["codes"].device)
         v = torch.stack([grid[(t["codes"] & 15).long()], grid[(t["codes"] >> 4).long()]], 2)
-    e = t["scales"].int() - 127
+    e = t["scales"].transpose(0, 1).flatten(1).int() - 127
     v = torch.ldexp(v.view(e.shape[0], -1, 32), e[:, :, None])
     return v.view(e.shape[0], -1)[:, :t["d"]]
 
@@ -336,7 +337,7 @@ def exact(case, seed):
         e, f = code % half // man, (code % man).double() / man
         v = torch.where(e > 0, (1 + f) * power(e - bias), f * 2.0 ** (1 - bias))
         v = torch.where(code >= half, -v, v)
-        unit = power(t["scales"].to(torch.int64) - 127).repeat_interleave(32, 1)
+        unit = torch.cat(list(power(t["scales"].to(torch.int64) - 127)), 1).repeat_interleave(32, 1)
         return (v * unit)[:, :t["d"]]
 
     def act(z):
