@@ -356,6 +356,128 @@ GPTQ_API gptq_status gptq_dequant_gated_backward(const void *dH, gptq_dtype dy_d
                                                  void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * Microscaled (MX) formats: a weight or activation matrix in blocks of 32
+ * columns that share a power of two, the low-bit format that the matrix cores
+ * multiply without conversion ("Optimization Gptq", "Configuracoes de
+ * quantizacao": low-bit weights in groups; the published OCP Microscaling
+ * Formats, version 1.0).
+ *
+ *   E = clamp(floor(log2 max|x|) - emax, -127, 127) over the block,
+ *   element = x 2^-E rounded to nearest even, saturated at the largest value;
+ *   GPTQ_MX_FP8: e4m3, emax 8, largest 448;  GPTQ_MX_FP4: e2m1, emax 2, largest 6.
+ * A block that holds a NaN or an infinity stands for NaN throughout.
+ *
+ * A matrix of `rows` rows and d columns is stored with its columns padded to
+ * whole 128 (s = ceil(d / 128) steps):
+ *   codes    uint8 [rows][gptq_mx_row_bytes(d, format)]: s * 128 bytes (FP8: one
+ *            per element) or s * 64 (FP4: two per byte, the even column in the
+ *            low half, the sign in a half's highest bit); 16-byte aligned
+ *   scales   uint8 [s][rows][4]: byte E + 127 of block b of row r at
+ *            [b / 4][r][b % 4], 255 for NaN; 4-byte aligned
+ * Padding columns have codes 0 and padding blocks scale bytes 0 (quantizing
+ * writes them; the products rely on it).  An all-zero block has scale byte 0.
+ *
+ *   gptq_mx_quantize     X [rows][d] -> codes, scales.
+ *   gptq_mx_dequantize   codes, scales -> Y [rows][d], rounded to y_dtype (exact
+ *                        in F32; in BF16 but for values below 2^-126).
+ * Limits: d in [1, 2^19], rows in [0, 2^31 - 1].  rows == 0 is a no-op.
+ * Everything is enqueued on `stream`, nothing synchronizes, no workspace.
+ * Errors: EINVAL (sizes, dtype, format, NULL or misaligned pointer), EHIP.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+    GPTQ_MX_FP8 = 0,   /* e4m3 elements */
+    GPTQ_MX_FP4 = 1    /* e2m1 elements */
+} gptq_mx_format;
+
+GPTQ_API int64_t gptq_mx_row_bytes(int64_t d, gptq_mx_format format);   /* host only; -1 if invalid */
+GPTQ_API int64_t gptq_mx_steps(int64_t d);                              /* ceil(d / 128), -1 if invalid */
+
+GPTQ_API gptq_status gptq_mx_quantize(const void *X, gptq_dtype x_dtype, int64_t rows, int64_t d,
+                                      gptq_mx_format format, uint8_t *codes, uint8_t *scales, void *stream);
+GPTQ_API gptq_status gptq_mx_dequantize(const uint8_t *codes, const uint8_t *scales, gptq_mx_format format,
+                                        int64_t rows, int64_t d, void *Y, gptq_dtype y_dtype, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Products with a layer in MXFP4, W [d_out][d_in] stored as above, with the
+ * epilogue of gptq_dequant_linear, and their gradients:
+ *   gptq_mx_linear           Z = A W^T + bias,  Y = act(Z) + residual
+ *   gptq_mx_linear_mx        the same for activations that are stored in an MX
+ *                            format themselves (codes, scales of [m][d_in])
+ *   gptq_mx_linear_backward  dZ = dY act'(Z),  dA = dZ W,  dbias[r] = sum_i dZ[i][r]
+ * Activations, epilogue operands, dtypes, aliasing, aligning, workspace, limits and
+ * errors are those of gptq_dequant_linear and gptq_dequant_linear_backward, with
+ * the code and scale alignments above.
+ * Numerics: fp32 sums, one rounding of each output to its dtype.  MX operands
+ * enter as they are stored; with MX activations every product is exact.  The
+ * other operands may be rounded on the way, relative to the largest value M of
+ * their row (activations; dZ as in gptq_dequant_linear_backward):
+ *   F32 output   to 22 significand bits down to 2^-17 M, and to within 2^-39 M
+ *                below;
+ *   BF16 output  dZ and F32 activations to 11 bits down to 2^-28 M, and to
+ *                within 2^-39 M below;
+ *   BF16 activations enter exactly down to 2^-31 M.
+ * Weights below 2^-37 of 6 times the largest scale of their row (in a backward
+ * call: of their 32 columns over all rows) may be rounded to within 2^-39 of
+ * it.  Calls of few rows round less.  All results are deterministic.
+ * ------------------------------------------------------------------------- */
+GPTQ_API size_t gptq_mx_linear_workspace_size(int64_t m, int64_t d_out, int64_t d_in, gptq_dtype a_dtype,
+                                              gptq_dtype y_dtype);
+GPTQ_API gptq_status gptq_mx_linear(const void *A, gptq_dtype a_dtype, int64_t m, int64_t d_in,
+                                    const uint8_t *codes, const uint8_t *scales, int64_t d_out, const void *bias,
+                                    gptq_dtype bias_dtype, gptq_activation act, const void *residual, void *Y,
+                                    gptq_dtype y_dtype, void *preact, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+GPTQ_API size_t gptq_mx_linear_mx_workspace_size(int64_t m, int64_t d_out, int64_t d_in, gptq_mx_format a_format,
+                                                 gptq_dtype y_dtype);
+GPTQ_API gptq_status gptq_mx_linear_mx(const uint8_t *a_codes, const uint8_t *a_scales, gptq_mx_format a_format,
+                                       int64_t m, int64_t d_in, const uint8_t *codes, const uint8_t *scales,
+                                       int64_t d_out, const void *bias, gptq_dtype bias_dtype, gptq_activation act,
+                                       const void *residual, void *Y, gptq_dtype y_dtype, void *preact,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
+GPTQ_API size_t gptq_mx_linear_backward_workspace_size(int64_t m, int64_t d_out, int64_t d_in, gptq_dtype dy_dtype,
+                                                       gptq_dtype da_dtype);
+GPTQ_API gptq_status gptq_mx_linear_backward(const void *dY, gptq_dtype dy_dtype, int64_t m, int64_t d_out,
+                                             const void *preact, gptq_activation act, const uint8_t *codes,
+                                             const uint8_t *scales, int64_t d_in, void *dA, gptq_dtype da_dtype,
+                                             float *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Root-mean-square norm in front of a projection, with the residual's addition
+ * and, for a projection that takes MX activations, their quantization:
+ *   S = X + residual, rounded to dtype (S = X without a residual)
+ *   Y = S r weight,  r = (mean_j S_j^2 + eps)^(-1/2) per row
+ *   backward: dX = r (weight dY - S r^2 mean_j(weight_j dY_j S_j)) + dS,
+ *             dweight = sum over rows of dY S r
+ * (dX is the residual's gradient too; dS, the gradient that reaches S by
+ * itself, may be NULL; through a quantized output the gradient passes as
+ * through an unquantized one).
+ *   X, residual, S, dY, dS, dX [m][d], weight [d]   of `dtype`; residual NULL: none
+ *   S        output, NULL: not written; may be X or the residual itself
+ *   Y        plain output of `dtype` (gptq_rms_norm); codes, scales (gptq_rms_norm_mx)
+ *            an MX output, rounded once from the 64-bit value of the norm
+ *   dX       may be dY or dS itself
+ *   dweight  fp32 [d], overwritten; NULL: not formed
+ * Row sums in 64 bits; a plain Y is rounded once from 64 bits, gradients are
+ * formed in fp32 and rounded once.  All results are deterministic.
+ * Limits: d in [1, 2^19], m in [0, 2^31 - 1], eps finite and >= 0.  m == 0 leaves
+ * dweight zero and is a no-op otherwise.  workspace (backward, with dweight):
+ * gptq_rms_norm_backward_workspace_size bytes, 256-byte aligned, in any state.
+ * Nothing synchronizes; every call can be captured into a graph.  Errors: EINVAL,
+ * ENOMEM, EHIP.
+ * ------------------------------------------------------------------------- */
+GPTQ_API gptq_status gptq_rms_norm(const void *X, const void *residual, const void *weight, gptq_dtype dtype,
+                                   int64_t m, int64_t d, double eps, void *S, void *Y, void *stream);
+GPTQ_API gptq_status gptq_rms_norm_mx(const void *X, const void *residual, const void *weight, gptq_dtype dtype,
+                                      int64_t m, int64_t d, double eps, void *S, gptq_mx_format format,
+                                      uint8_t *codes, uint8_t *scales, void *stream);
+GPTQ_API size_t gptq_rms_norm_backward_workspace_size(int64_t m, int64_t d);
+GPTQ_API gptq_status gptq_rms_norm_backward(const void *dY, const void *S, const void *weight, const void *dS,
+                                            gptq_dtype dtype, int64_t m, int64_t d, double eps, void *dX,
+                                            float *dweight, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Stage timing (tracing aid).  gptq_profile_enable(stage_mask): bit s set
  * makes every later call record a pair of hipEvents around stage s's launches
  * on the caller's stream (GPTQ_PROFILE_ALL: every stage; 0: none).  Reading

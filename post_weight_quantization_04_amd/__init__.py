@@ -14,6 +14,9 @@ is used for device memory and streams only.
     Y = dequant_linear(A, q, bias, "gelu", residual)   # the same with its epilogue fused
     h = dequant_gated(A, gate, up, "silu")         # act(A W_gate^T) * (A W_up^T)
     dA, _ = dequant_linear_backward(dY, q)         # gradients through packed layers
+    w = mx_quantize(W, "fp4")                      # microscaled 4-bit weights
+    x, S = rms_norm(X, weight, residual=R, format="fp8")   # the norm, its output in 8 bits
+    Y = mx_linear(x, w, bias, "silu")              # on the scaled matrix cores
 
 The library must have been built (python -m post_weight_quantization_04_amd.build);
 the first call into it raises ImportError if libgptq.so is missing (there is
@@ -33,10 +36,14 @@ __all__ = [
     "ACTIVATIONS", "dequant_linear", "dequant_linear_workspace_size", "dequant_linear_backward",
     "dequant_linear_backward_workspace_size", "dequant_gated", "dequant_gated_workspace_size",
     "dequant_gated_backward", "dequant_gated_backward_workspace_size",
+    "MX_FORMATS", "MxTensor", "mx_quantize", "mx_dequantize", "mx_linear", "mx_linear_workspace_size",
+    "mx_linear_backward", "mx_linear_backward_workspace_size", "rms_norm", "rms_norm_backward",
+    "rms_norm_backward_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq.so")
 F32, BF16 = 0, 1
+MX_FORMATS = {"fp8": 0, "fp4": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _STATUS = {0: "GPTQ_OK", 1: "GPTQ_EINVAL", 2: "GPTQ_ENOTSPD", 3: "GPTQ_EHIP", 4: "GPTQ_ENOMEM"}
 
@@ -99,6 +106,25 @@ def _load() -> ctypes.CDLL:
                                               i64, i32, i32, ptr, i32, ptr, ptr, ptr, size, ptr]
     for name in ("linear", "linear_backward", "gated", "gated_backward"):
         getattr(L, f"gptq_dequant_{name}").restype = i32
+    f64 = c.c_double
+    for name, args in {
+            "mx_quantize": [ptr, i32, i64, i64, i32, ptr, ptr, ptr],
+            "mx_dequantize": [ptr, ptr, i32, i64, i64, ptr, i32, ptr],
+            "mx_linear": [ptr, i32, i64, i64, ptr, ptr, i64, ptr, i32, i32, ptr, ptr, i32, ptr, ptr, size, ptr],
+            "mx_linear_mx": [ptr, ptr, i32, i64, i64, ptr, ptr, i64, ptr, i32, i32, ptr, ptr, i32, ptr, ptr, size, ptr],
+            "mx_linear_backward": [ptr, i32, i64, i64, ptr, i32, ptr, ptr, i64, ptr, i32, ptr, ptr, size, ptr],
+            "rms_norm": [ptr, ptr, ptr, i32, i64, i64, f64, ptr, ptr, ptr],
+            "rms_norm_mx": [ptr, ptr, ptr, i32, i64, i64, f64, ptr, i32, ptr, ptr, ptr],
+            "rms_norm_backward": [ptr, ptr, ptr, ptr, i32, i64, i64, f64, ptr, ptr, ptr, size, ptr]}.items():
+        f = getattr(L, f"gptq_{name}")
+        f.argtypes, f.restype = args, i32
+    for name in ("mx_linear", "mx_linear_mx", "mx_linear_backward"):
+        f = getattr(L, f"gptq_{name}_workspace_size")
+        f.argtypes, f.restype = [i64, i64, i64, i32, i32], size
+    L.gptq_rms_norm_backward_workspace_size.argtypes = [i64, i64]
+    L.gptq_rms_norm_backward_workspace_size.restype = size
+    L.gptq_mx_row_bytes.argtypes, L.gptq_mx_row_bytes.restype = [i64, i32], i64
+    L.gptq_mx_steps.argtypes, L.gptq_mx_steps.restype = [i64], i64
     L.gptq_inverse_factor.argtypes = [c.c_void_p, c.c_int64, c.c_float, c.c_int, c.c_void_p, c.c_void_p,
                                       c.c_void_p, c.c_size_t, c.c_void_p]
     L.gptq_inverse_factor.restype = c.c_int
@@ -418,29 +444,25 @@ def _operand(t, name, dtype, shape, device) -> int:
     raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
-class _FusedCall:
-    """Checks and buffers of one fused call: operands on one device, a
-    workspace and outputs that belong to the stream the work goes to."""
-    __slots__ = ("device", "in_code", "act", "out_dtype", "out_code", "d_in", "d_out", "words", "groups", "perm",
-                 "bits", "group", "stream", "given_ws", "guard")
+class _DeviceCall:
+    """Checks and buffers of one call: operands on one device, a workspace and
+    outputs that belong to the stream the work goes to."""
+    __slots__ = ("device", "act", "out_dtype", "out_code", "stream", "given_ws", "guard")
 
-    def __init__(self, x, name, q, activation, out_dtype, workspace, stream):
+    def epilogue(self, activation, out_dtype):
         torch = _torch()
-        _require(x, name, ndim=2)
-        self.in_code = _dtype_code(x)
-        device = self.device = x.device
         if activation not in ACTIVATIONS:
             raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}; got {activation!r}")
         self.act = ACTIVATIONS[activation]
-        self.out_dtype = out_dtype or x.dtype
+        self.out_dtype = out_dtype
         if self.out_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"unsupported out_dtype {self.out_dtype}; use float32 or bfloat16")
         self.out_code = F32 if self.out_dtype == torch.float32 else BF16
-        self.d_in, self.d_out, self.bits, self.group = q.d_in, q.scales.shape[1], q.bits, q.group_size
-        one = self.group == -1 or self.group >= self.d_in
-        self.words = -(-self.bits * self.d_in // 32)
-        self.groups = 1 if one or self.group < 1 else -(-self.d_in // self.group)
-        self.perm = _operand(q.perm, "perm", torch.int32, (self.d_in,), device) if q.act_order else None
+
+    def place(self, device, name, workspace, stream):
+        """The device and stream of the call (name: the operand whose device it is)."""
+        torch = _torch()
+        self.device = device
         self.guard = None
         if stream is not None:
             if stream.device != device:
@@ -455,33 +477,6 @@ class _FusedCall:
         self.given_ws = workspace
         if workspace is not None:
             _operand(workspace, "workspace", workspace.dtype, workspace.shape, device)
-        self.no_grad(x, q.scales, q.zeros)
-
-    def layer(self, q):
-        """A packed layer's pointers (codes, scales, zero points)."""
-        torch = _torch()
-        params = (self.groups, self.d_out)
-        return (_operand(q.qpacked, "qpacked", torch.int32, (self.words, self.d_out), self.device),
-                _operand(q.scales, "scales", torch.float32, params, self.device),
-                _operand(q.zeros, "zeros", torch.float32, params, self.device))
-
-    def pair(self, gate, up):
-        if (up.d_in, up.bits, up.group_size, up.scales.shape[1]) != (self.d_in, self.bits, self.group, self.d_out):
-            raise ValueError("the layers must have the same sizes, bits and group_size")
-        if up.act_order != gate.act_order or (up.act_order and not self.same_order(gate.perm, up.perm)):
-            raise ValueError("the layers must share one perm (quantize_layers gives them one)")
-        self.no_grad(up.scales, up.zeros)
-
-    def same_order(self, a, b):
-        """One tensor, or two of equal values (compared on the call's stream, and waited for)."""
-        if _operand(b, "perm", a.dtype, a.shape, self.device) == self.perm:
-            return True
-        torch = _torch()
-        with self:
-            if torch.cuda.is_current_stream_capturing():
-                raise ValueError("during a graph's capture the layers must share one perm tensor (two cannot be "
-                                 "compared)")
-            return torch.equal(a, b)
 
     def take(self, t, name, dtype, shape):
         """An optional operand's pointer."""
@@ -527,6 +522,50 @@ class _FusedCall:
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
+
+
+class _FusedCall(_DeviceCall):
+    """A call of the fused products on packed layers."""
+    __slots__ = ("in_code", "d_in", "d_out", "words", "groups", "perm", "bits", "group")
+
+    def __init__(self, x, name, q, activation, out_dtype, workspace, stream):
+        torch = _torch()
+        _require(x, name, ndim=2)
+        self.in_code = _dtype_code(x)
+        self.epilogue(activation, out_dtype or x.dtype)
+        self.d_in, self.d_out, self.bits, self.group = q.d_in, q.scales.shape[1], q.bits, q.group_size
+        one = self.group == -1 or self.group >= self.d_in
+        self.words = -(-self.bits * self.d_in // 32)
+        self.groups = 1 if one or self.group < 1 else -(-self.d_in // self.group)
+        self.perm = _operand(q.perm, "perm", torch.int32, (self.d_in,), x.device) if q.act_order else None
+        self.place(x.device, name, workspace, stream)
+        self.no_grad(x, q.scales, q.zeros)
+
+    def layer(self, q):
+        """A packed layer's pointers (codes, scales, zero points)."""
+        torch = _torch()
+        params = (self.groups, self.d_out)
+        return (_operand(q.qpacked, "qpacked", torch.int32, (self.words, self.d_out), self.device),
+                _operand(q.scales, "scales", torch.float32, params, self.device),
+                _operand(q.zeros, "zeros", torch.float32, params, self.device))
+
+    def pair(self, gate, up):
+        if (up.d_in, up.bits, up.group_size, up.scales.shape[1]) != (self.d_in, self.bits, self.group, self.d_out):
+            raise ValueError("the layers must have the same sizes, bits and group_size")
+        if up.act_order != gate.act_order or (up.act_order and not self.same_order(gate.perm, up.perm)):
+            raise ValueError("the layers must share one perm (quantize_layers gives them one)")
+        self.no_grad(up.scales, up.zeros)
+
+    def same_order(self, a, b):
+        """One tensor, or two of equal values (compared on the call's stream, and waited for)."""
+        if _operand(b, "perm", a.dtype, a.shape, self.device) == self.perm:
+            return True
+        torch = _torch()
+        with self:
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("during a graph's capture the layers must share one perm tensor (two cannot be "
+                                 "compared)")
+            return torch.equal(a, b)
 
 
 def dequant_linear(A, q: "QuantizedLayer", bias=None, activation="none", residual=None, out_dtype=None,
@@ -655,6 +694,242 @@ def dequant_gated_backward(dH, gate: "QuantizedLayer", up: "QuantizedLayer", gat
                                                   dbg.data_ptr() if bias_grad else None,
                                                   dbu.data_ptr() if bias_grad else None, ws, wsb, f.stream))
     return dA, dbg, dbu
+
+
+# ---------------------------------------------------------------------------
+# microscaled (MX) formats, products with MX weights, and the norm before them
+# ---------------------------------------------------------------------------
+@dataclass
+class MxTensor:
+    """A matrix [rows, d] in blocks of 32 columns that share a power of two
+    (gptq.h has the layout): codes uint8 [rows, row bytes], scales uint8
+    [ceil(d / 128), rows, 4], format "fp8" (e4m3) or "fp4" (e2m1)."""
+    codes: "object"
+    scales: "object"
+    format: str
+    d: int
+
+    @property
+    def shape(self):
+        return (self.codes.shape[0], self.d)
+
+
+def _mx_shapes(rows, d, format):
+    """The shapes of an MX matrix's codes and scales."""
+    steps = -(-d // 128)
+    return (rows, steps * (64 if format == "fp4" else 128)), (steps, rows, 4)
+
+
+def _mx_format(format) -> int:
+    if format not in MX_FORMATS:
+        raise ValueError(f"format must be one of {', '.join(MX_FORMATS)}; got {format!r}")
+    return MX_FORMATS[format]
+
+
+class _MxCall(_DeviceCall):
+    """A call of the MX operators and the norm."""
+    __slots__ = ()
+
+    def __init__(self, device, name, workspace=None, stream=None):
+        self.place(device, name, workspace, stream)
+
+    def matrix(self, t, name):
+        """An MX matrix's pointers."""
+        u8 = _torch().uint8
+        codes, scales = _mx_shapes(t.codes.shape[0], t.d, t.format)
+        return (_operand(t.codes, f"{name}.codes", u8, codes, self.device),
+                _operand(t.scales, f"{name}.scales", u8, scales, self.device))
+
+    def new_matrix(self, rows, d, format):
+        u8 = _torch().uint8
+        codes, scales = _mx_shapes(rows, d, format)
+        return MxTensor(self.empty(codes, u8), self.empty(scales, u8), format, d)
+
+
+def _mx_tensor(t, name, format=None):
+    if not isinstance(t, MxTensor):
+        raise TypeError(f"{name} must be an MxTensor")
+    _mx_format(t.format)
+    if format is not None and t.format != format:
+        raise ValueError(f"{name} must be in {format}, got {t.format}")
+    _require(t.codes, f"{name}.codes", ndim=2)
+
+
+def mx_quantize(X, format="fp4", stream=None) -> MxTensor:
+    """X [rows, d] bfloat16/float32 in an MX format (gptq_mx_quantize): "fp4"
+    for weights, "fp8" or "fp4" for activations."""
+    _require(X, "X", ndim=2)
+    code, fmt = _dtype_code(X), _mx_format(format)
+    f = _MxCall(X.device, "X", stream=stream)
+    f.no_grad(X)
+    rows, d = X.shape
+    with f:
+        t = f.new_matrix(rows, d, format)
+        _check(_lib().gptq_mx_quantize(X.data_ptr(), code, rows, d, fmt, t.codes.data_ptr(), t.scales.data_ptr(),
+                                       f.stream))
+    return t
+
+
+def mx_dequantize(t: MxTensor, dtype=None, stream=None):
+    """The values [rows, d] of t in float32 (exact; the default) or bfloat16 (gptq_mx_dequantize)."""
+    torch = _torch()
+    _mx_tensor(t, "t")
+    dtype = dtype or torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+    f = _MxCall(t.codes.device, "t", stream=stream)
+    codes, scales = f.matrix(t, "t")
+    rows = t.codes.shape[0]
+    with f:
+        Y = f.empty((rows, t.d), dtype)
+        _check(_lib().gptq_mx_dequantize(codes, scales, MX_FORMATS[t.format], rows, t.d, Y.data_ptr(),
+                                         F32 if dtype == torch.float32 else BF16, f.stream))
+    return Y
+
+
+def mx_linear_workspace_size(m, d_out, d_in, a_kind, y_dtype_code) -> int:
+    """a_kind: the activations' dtype code (F32, BF16) or MX format ("fp8", "fp4")."""
+    if isinstance(a_kind, str):
+        return int(_lib().gptq_mx_linear_mx_workspace_size(m, d_out, d_in, _mx_format(a_kind), y_dtype_code))
+    return int(_lib().gptq_mx_linear_workspace_size(m, d_out, d_in, a_kind, y_dtype_code))
+
+
+def mx_linear_backward_workspace_size(m, d_out, d_in, dy_dtype_code, da_dtype_code) -> int:
+    return int(_lib().gptq_mx_linear_backward_workspace_size(m, d_out, d_in, dy_dtype_code, da_dtype_code))
+
+
+def mx_linear(A, w: MxTensor, bias=None, activation="none", residual=None, out_dtype=None, save_preact=False,
+              workspace=None, stream=None):
+    """Y = act(A W^T + bias) + residual with MX weights w [d_out, d_in] in "fp4"
+    (gptq_mx_linear, gptq_mx_linear_mx).
+
+    A: [m, d_in], a bfloat16/float32 tensor (weights alone in 4 bits) or an
+    MxTensor in "fp8" or "fp4" (both operands enter the scaled matrix cores as
+    they are stored).  out_dtype: A's dtype by default, bfloat16 for an
+    MxTensor.  Other arguments and the result as for dequant_linear.
+    Not differentiable by autograd: see mx_linear_backward."""
+    torch = _torch()
+    _mx_tensor(w, "w", "fp4")
+    mx = isinstance(A, MxTensor)
+    if mx:
+        _mx_tensor(A, "A")
+    else:
+        _require(A, "A", ndim=2)
+    (m, d_in), d_out = A.shape, w.codes.shape[0]
+    f = _MxCall(A.codes.device if mx else A.device, "A", workspace, stream)
+    f.epilogue(activation, out_dtype or (torch.bfloat16 if mx else A.dtype))
+    if d_in != w.d:
+        raise ValueError(f"A has {d_in} columns, the layer {w.d}")
+    if mx:
+        a, kind = f.matrix(A, "A"), A.format
+    else:
+        kind = _dtype_code(A)
+        f.no_grad(A)
+    codes, scales = f.matrix(w, "w")
+    b = f.take(bias, "bias", bias.dtype, (d_out,)) if bias is not None else None
+    bcode = _dtype_code(bias) if bias is not None else 0
+    r = f.take(residual, "residual", f.out_dtype, (m, d_out))
+    with f:
+        Y = f.empty((m, d_out))
+        Z = f.empty((m, d_out)) if save_preact else None
+        _own, ws, wsb = f.workspace(mx_linear_workspace_size(m, d_out, d_in, kind, f.out_code))
+        rest = (m, d_in, codes, scales, d_out, b, bcode, f.act, r, Y.data_ptr(), f.out_code,
+                Z.data_ptr() if save_preact else None, ws, wsb, f.stream)
+        if mx:
+            _check(_lib().gptq_mx_linear_mx(a[0], a[1], MX_FORMATS[kind], *rest))
+        else:
+            _check(_lib().gptq_mx_linear(A.data_ptr(), kind, *rest))
+    return (Y, Z) if save_preact else Y
+
+
+def mx_linear_backward(dY, w: MxTensor, activation="none", preact=None, bias_grad=False, out_dtype=None,
+                       workspace=None, stream=None):
+    """(dA, dbias) of mx_linear (gptq_mx_linear_backward): dZ = dY act'(Z),
+    dA = dZ W, dbias the column sums of dZ.  Through quantized activations the
+    gradient passes as through unquantized ones.  Arguments and results as for
+    dequant_linear_backward."""
+    _mx_tensor(w, "w", "fp4")
+    _require(dY, "dY", ndim=2)
+    code = _dtype_code(dY)
+    f = _MxCall(dY.device, "dY", workspace, stream)
+    f.epilogue(activation, out_dtype or dY.dtype)
+    f.no_grad(dY)
+    m, d_out = dY.shape
+    if d_out != w.codes.shape[0]:
+        raise ValueError(f"dY has {d_out} columns, the layer {w.codes.shape[0]} rows")
+    if preact is None and f.act:
+        raise ValueError("preact is required unless activation is 'none'")
+    codes, scales = f.matrix(w, "w")
+    z = f.take(preact, "preact", dY.dtype, (m, d_out))
+    with f:
+        dA = f.empty((m, w.d))
+        db = f.empty((d_out,), _torch().float32) if bias_grad else None
+        _own, ws, wsb = f.workspace(mx_linear_backward_workspace_size(m, d_out, w.d, code, f.out_code))
+        _check(_lib().gptq_mx_linear_backward(dY.data_ptr(), code, m, d_out, z, f.act, codes, scales, w.d,
+                                              dA.data_ptr(), f.out_code, db.data_ptr() if bias_grad else None, ws,
+                                              wsb, f.stream))
+    return dA, db
+
+
+def rms_norm(X, weight, residual=None, eps=1e-6, format=None, stream=None):
+    """(Y, S): S = X + residual (rounded to X's dtype), Y = S / sqrt(mean(S^2) + eps) * weight
+    (gptq_rms_norm, gptq_rms_norm_mx).
+
+    X, residual: [m, d] bfloat16/float32; weight: [d] of X's dtype.  Y is a
+    tensor of X's dtype, or an MxTensor when format is "fp8" or "fp4" (what
+    mx_linear takes).  S is the residual stream behind the addition, X itself
+    without a residual; rms_norm_backward takes it."""
+    _require(X, "X", ndim=2)
+    code = _dtype_code(X)
+    fmt = None if format is None else _mx_format(format)
+    f = _MxCall(X.device, "X", stream=stream)
+    f.no_grad(X)
+    m, d = X.shape
+    if weight is None:
+        raise ValueError("weight is required")
+    w = f.take(weight, "weight", X.dtype, (d,))
+    r = f.take(residual, "residual", X.dtype, (m, d))
+    with f:
+        S = X if residual is None else f.empty((m, d), X.dtype)
+        s = None if residual is None else S.data_ptr()
+        if fmt is None:
+            Y = f.empty((m, d), X.dtype)
+            _check(_lib().gptq_rms_norm(X.data_ptr(), r, w, code, m, d, float(eps), s, Y.data_ptr(), f.stream))
+        else:
+            Y = f.new_matrix(m, d, format)
+            _check(_lib().gptq_rms_norm_mx(X.data_ptr(), r, w, code, m, d, float(eps), s, fmt, Y.codes.data_ptr(),
+                                           Y.scales.data_ptr(), f.stream))
+    return Y, S
+
+
+def rms_norm_backward_workspace_size(m, d) -> int:
+    return int(_lib().gptq_rms_norm_backward_workspace_size(m, d))
+
+
+def rms_norm_backward(dY, S, weight, eps=1e-6, dS=None, weight_grad=True, workspace=None, stream=None):
+    """(dX, dweight) of rms_norm (gptq_rms_norm_backward) from the S that it
+    returned; dX is the gradient of X and of the residual.
+
+    dY, S, dS: [m, d], one dtype; dS: the gradient that reaches S by itself (the
+    residual stream's), added to dX.  dX: of that dtype; dweight: [d] float32,
+    or None unless weight_grad."""
+    _require(dY, "dY", ndim=2)
+    code = _dtype_code(dY)
+    f = _MxCall(dY.device, "dY", workspace, stream)
+    f.no_grad(dY)
+    m, d = dY.shape
+    if S is None or weight is None:
+        raise ValueError("S and weight are required")
+    s = f.take(S, "S", dY.dtype, (m, d))
+    w = f.take(weight, "weight", dY.dtype, (d,))
+    t = f.take(dS, "dS", dY.dtype, (m, d))
+    with f:
+        dX = f.empty((m, d), dY.dtype)
+        dw = f.empty((d,), _torch().float32) if weight_grad else None
+        _own, ws, wsb = f.workspace(rms_norm_backward_workspace_size(m, d) if weight_grad else 0)
+        _check(_lib().gptq_rms_norm_backward(dY.data_ptr(), s, w, t, code, m, d, float(eps), dX.data_ptr(),
+                                             dw.data_ptr() if weight_grad else None, ws, wsb, f.stream))
+    return dX, dw
 
 
 def inverse_factor(H, damp: float = 0.01, act_order: bool = False, workspace=None, stream=None):

@@ -362,6 +362,70 @@ gptq_status run_backward(gptq::FusedBackward &a, const gptq_activation &act, voi
     return GPTQ_OK;
 }
 
+// ---------------------------------------------------------------------------
+// MX formats, their products, and the norm
+// ---------------------------------------------------------------------------
+bool valid_format(const gptq_mx_format &f) { return raw(f) == GPTQ_MX_FP8 || raw(f) == GPTQ_MX_FP4; }
+bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+gptq_status check_rows(int64_t rows, int64_t d) {
+    if (rows < 0 || rows > (int64_t)0x7fffffff) return fail(GPTQ_EINVAL, "rows must be in [0, 2^31 - 1]");
+    if (d < 1 || d > (int64_t)1 << 19) return fail(GPTQ_EINVAL, "d must be in [1, 2^19]");
+    return GPTQ_OK;
+}
+gptq_status check_mx(const void *codes, const void *scales) {
+    if (!codes || !scales) return fail(GPTQ_EINVAL, "a required pointer is NULL");
+    if (misaligned(codes, 16) || misaligned(scales, 4))
+        return fail(GPTQ_EINVAL, "codes must be 16-byte and scales 4-byte aligned");
+    return GPTQ_OK;
+}
+gptq_status check_mx_linear(int64_t m, int64_t d_out, int64_t d_in) {
+    gptq_status s = check_rows(m, d_in);
+    if (s != GPTQ_OK) return s;
+    if (d_out < 1 || d_out > (int64_t)1 << 19) return fail(GPTQ_EINVAL, "d_out must be in [1, 2^19]");
+    return GPTQ_OK;
+}
+int act_kind(const gptq_dtype &t) { return raw(t) == GPTQ_BF16 ? gptq::MX_ACT_BF16 : gptq::MX_ACT_F32; }
+
+// the checks and the launch that the two forward products share, a.A or a.a set
+gptq_status run_mx_linear(gptq::MxLinear &a, int a_kind, const gptq_dtype &bias_dtype, const gptq_activation &act,
+                          const gptq_dtype &y_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!valid_dtype(y_dtype)) return fail(GPTQ_EINVAL, "y_dtype must be GPTQ_F32 or GPTQ_BF16");
+    if (!valid_act(act)) return fail(GPTQ_EINVAL, "unknown activation (got %d)", raw(act));
+    if (a.bias && !valid_dtype(bias_dtype)) return fail(GPTQ_EINVAL, "bias_dtype must be GPTQ_F32 or GPTQ_BF16");
+    if (a.m == 0) return GPTQ_OK;
+    if (!a.Y) return fail(GPTQ_EINVAL, "a required pointer is NULL");
+    gptq_status s = check_mx(a.w.codes, a.w.scales);
+    if (s != GPTQ_OK) return s;
+    a.w.fmt = gptq::MX_FP4;
+    a.out_bf16 = raw(y_dtype) == GPTQ_BF16;
+    a.bias_bf16 = a.bias && raw(bias_dtype) == GPTQ_BF16;
+    a.act = raw(act);
+    s = check_ws(workspace, workspace_bytes, gptq::mx_linear_ws(a.m, a.d_out, a.d_in, a_kind, a.out_bf16));
+    if (s != GPTQ_OK) return s;
+    a.ws = (char *)workspace;
+    HIPCHECK(gptq::mx_linear_launch(a, (hipStream_t)stream));
+    return GPTQ_OK;
+}
+
+gptq::FusedShape mx_backward_shape(int64_t m, int64_t d_out, int64_t d_in, int dy_bf16, int da_bf16) {
+    gptq::FusedShape f{};
+    f.m = m;
+    f.d_out = d_out;
+    f.d_in = d_in;
+    f.ngroups = (int)cdiv(d_in, gptq::MX_BLOCK);
+    f.layers = 1;
+    f.in_bf16 = dy_bf16;
+    f.out_bf16 = da_bf16;
+    return f;
+}
+
+gptq_status check_norm(const gptq_dtype &dtype, int64_t m, int64_t d, double eps) {
+    if (!valid_dtype(dtype)) return fail(GPTQ_EINVAL, "dtype must be GPTQ_F32 or GPTQ_BF16");
+    if (!std::isfinite(eps) || eps < 0.0) return fail(GPTQ_EINVAL, "eps must be finite and >= 0");
+    return check_rows(m, d);
+}
+
 }  // namespace
 
 extern "C" {
@@ -734,6 +798,216 @@ gptq_status gptq_dequant_gated_backward(const void *dH, gptq_dtype dy_dtype, int
     a.dbias[0] = dbias_gate;
     a.dbias[1] = dbias_up;
     return run_backward(a, act, workspace, workspace_bytes, stream);
+}
+
+int64_t gptq_mx_row_bytes(int64_t d, gptq_mx_format format) {
+    return d < 1 || d > (int64_t)1 << 19 || !valid_format(format) ? -1 : gptq::mx_row_bytes(d, raw(format));
+}
+int64_t gptq_mx_steps(int64_t d) { return d < 1 || d > (int64_t)1 << 19 ? -1 : gptq::mx_steps(d); }
+
+gptq_status gptq_mx_quantize(const void *X, gptq_dtype x_dtype, int64_t rows, int64_t d, gptq_mx_format format,
+                             uint8_t *codes, uint8_t *scales, void *stream) {
+    g_err.clear();
+    gptq_status s = check_rows(rows, d);
+    if (s != GPTQ_OK) return s;
+    if (!valid_dtype(x_dtype)) return fail(GPTQ_EINVAL, "x_dtype must be GPTQ_F32 or GPTQ_BF16");
+    if (!valid_format(format)) return fail(GPTQ_EINVAL, "format must be GPTQ_MX_FP8 or GPTQ_MX_FP4");
+    if (rows == 0) return GPTQ_OK;
+    if (!X) return fail(GPTQ_EINVAL, "a required pointer is NULL");
+    s = check_mx(codes, scales);
+    if (s != GPTQ_OK) return s;
+    HIPCHECK(gptq::mx_quantize_launch(X, raw(x_dtype) == GPTQ_BF16, rows, d, raw(format), codes, scales,
+                                      (hipStream_t)stream));
+    return GPTQ_OK;
+}
+
+gptq_status gptq_mx_dequantize(const uint8_t *codes, const uint8_t *scales, gptq_mx_format format, int64_t rows,
+                               int64_t d, void *Y, gptq_dtype y_dtype, void *stream) {
+    g_err.clear();
+    gptq_status s = check_rows(rows, d);
+    if (s != GPTQ_OK) return s;
+    if (!valid_dtype(y_dtype)) return fail(GPTQ_EINVAL, "y_dtype must be GPTQ_F32 or GPTQ_BF16");
+    if (!valid_format(format)) return fail(GPTQ_EINVAL, "format must be GPTQ_MX_FP8 or GPTQ_MX_FP4");
+    if (rows == 0) return GPTQ_OK;
+    if (!Y) return fail(GPTQ_EINVAL, "a required pointer is NULL");
+    s = check_mx(codes, scales);
+    if (s != GPTQ_OK) return s;
+    HIPCHECK(gptq::mx_dequantize_launch({codes, scales, raw(format)}, rows, d, Y, raw(y_dtype) == GPTQ_BF16,
+                                        (hipStream_t)stream));
+    return GPTQ_OK;
+}
+
+size_t gptq_mx_linear_workspace_size(int64_t m, int64_t d_out, int64_t d_in, gptq_dtype a_dtype, gptq_dtype y_dtype) {
+    if (check_mx_linear(m, d_out, d_in) != GPTQ_OK || !valid_dtype(a_dtype) || !valid_dtype(y_dtype)) return 0;
+    return gptq::mx_linear_ws(m, d_out, d_in, act_kind(a_dtype), raw(y_dtype) == GPTQ_BF16);
+}
+
+gptq_status gptq_mx_linear(const void *A, gptq_dtype a_dtype, int64_t m, int64_t d_in, const uint8_t *codes,
+                           const uint8_t *scales, int64_t d_out, const void *bias, gptq_dtype bias_dtype,
+                           gptq_activation act, const void *residual, void *Y, gptq_dtype y_dtype, void *preact,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    g_err.clear();
+    gptq_status s = check_mx_linear(m, d_out, d_in);
+    if (s != GPTQ_OK) return s;
+    if (!valid_dtype(a_dtype)) return fail(GPTQ_EINVAL, "a_dtype must be GPTQ_F32 or GPTQ_BF16");
+    if (m > 0 && !A) return fail(GPTQ_EINVAL, "a required pointer is NULL");
+    gptq::MxLinear a{};
+    a.m = m;
+    a.d_out = d_out;
+    a.d_in = d_in;
+    a.A = A;
+    a.a_bf16 = raw(a_dtype) == GPTQ_BF16;
+    a.w.codes = codes;
+    a.w.scales = scales;
+    a.bias = bias;
+    a.residual = residual;
+    a.Y = Y;
+    a.pre = preact;
+    return run_mx_linear(a, act_kind(a_dtype), bias_dtype, act, y_dtype, workspace, workspace_bytes, stream);
+}
+
+size_t gptq_mx_linear_mx_workspace_size(int64_t m, int64_t d_out, int64_t d_in, gptq_mx_format a_format,
+                                        gptq_dtype y_dtype) {
+    if (check_mx_linear(m, d_out, d_in) != GPTQ_OK || !valid_format(a_format) || !valid_dtype(y_dtype)) return 0;
+    return gptq::mx_linear_ws(m, d_out, d_in, raw(a_format), raw(y_dtype) == GPTQ_BF16);
+}
+
+gptq_status gptq_mx_linear_mx(const uint8_t *a_codes, const uint8_t *a_scales, gptq_mx_format a_format, int64_t m,
+                              int64_t d_in, const uint8_t *codes, const uint8_t *scales, int64_t d_out,
+                              const void *bias, gptq_dtype bias_dtype, gptq_activation act, const void *residual,
+                              void *Y, gptq_dtype y_dtype, void *preact, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+    g_err.clear();
+    gptq_status s = check_mx_linear(m, d_out, d_in);
+    if (s != GPTQ_OK) return s;
+    if (!valid_format(a_format)) return fail(GPTQ_EINVAL, "a_format must be GPTQ_MX_FP8 or GPTQ_MX_FP4");
+    if (m > 0 && (s = check_mx(a_codes, a_scales)) != GPTQ_OK) return s;
+    gptq::MxLinear a{};
+    a.m = m;
+    a.d_out = d_out;
+    a.d_in = d_in;
+    a.a = {a_codes, a_scales, raw(a_format)};
+    a.w.codes = codes;
+    a.w.scales = scales;
+    a.bias = bias;
+    a.residual = residual;
+    a.Y = Y;
+    a.pre = preact;
+    return run_mx_linear(a, raw(a_format), bias_dtype, act, y_dtype, workspace, workspace_bytes, stream);
+}
+
+size_t gptq_mx_linear_backward_workspace_size(int64_t m, int64_t d_out, int64_t d_in, gptq_dtype dy_dtype,
+                                              gptq_dtype da_dtype) {
+    if (check_mx_linear(m, d_out, d_in) != GPTQ_OK || !valid_dtype(dy_dtype) || !valid_dtype(da_dtype) || m == 0)
+        return 0;
+    return gptq::mx_linear_backward_ws(
+        mx_backward_shape(m, d_out, d_in, raw(dy_dtype) == GPTQ_BF16, raw(da_dtype) == GPTQ_BF16));
+}
+
+gptq_status gptq_mx_linear_backward(const void *dY, gptq_dtype dy_dtype, int64_t m, int64_t d_out, const void *preact,
+                                    gptq_activation act, const uint8_t *codes, const uint8_t *scales, int64_t d_in,
+                                    void *dA, gptq_dtype da_dtype, float *dbias, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
+    g_err.clear();
+    gptq_status s = check_mx_linear(m, d_out, d_in);
+    if (s != GPTQ_OK) return s;
+    if (!valid_dtype(dy_dtype) || !valid_dtype(da_dtype))
+        return fail(GPTQ_EINVAL, "every dtype must be GPTQ_F32 or GPTQ_BF16");
+    if (!valid_act(act)) return fail(GPTQ_EINVAL, "unknown activation (got %d)", raw(act));
+    gptq::FusedBackward a{};
+    a.s = mx_backward_shape(m, d_out, d_in, raw(dy_dtype) == GPTQ_BF16, raw(da_dtype) == GPTQ_BF16);
+    if (m > 0) {
+        if (!dY || !dA) return fail(GPTQ_EINVAL, "a required pointer is NULL");
+        if (raw(act) != GPTQ_ACT_NONE && !preact)
+            return fail(GPTQ_EINVAL, "preact is required unless the activation is GPTQ_ACT_NONE");
+        if ((s = check_mx(codes, scales)) != GPTQ_OK) return s;
+        s = check_ws(workspace, workspace_bytes, gptq::mx_linear_backward_ws(a.s));
+        if (s != GPTQ_OK) return s;
+    }
+    a.dY = dY;
+    a.pre[0] = preact;
+    a.act = raw(act);
+    a.mx = {codes, scales, gptq::MX_FP4};
+    a.dA = dA;
+    a.dbias[0] = dbias;
+    a.ws = (char *)workspace;
+    HIPCHECK(gptq::mx_linear_backward_launch(a, (hipStream_t)stream));
+    return GPTQ_OK;
+}
+
+gptq_status gptq_rms_norm(const void *X, const void *residual, const void *weight, gptq_dtype dtype, int64_t m,
+                          int64_t d, double eps, void *S, void *Y, void *stream) {
+    g_err.clear();
+    gptq_status s = check_norm(dtype, m, d, eps);
+    if (s != GPTQ_OK || m == 0) return s;
+    if (!X || !weight || !Y) return fail(GPTQ_EINVAL, "a required pointer is NULL");
+    gptq::RmsNorm a{};
+    a.m = m;
+    a.d = d;
+    a.bf16 = raw(dtype) == GPTQ_BF16;
+    a.X = X;
+    a.residual = residual;
+    a.weight = weight;
+    a.eps = eps;
+    a.S = S;
+    a.Y = Y;
+    HIPCHECK(gptq::rms_norm_launch(a, (hipStream_t)stream));
+    return GPTQ_OK;
+}
+
+gptq_status gptq_rms_norm_mx(const void *X, const void *residual, const void *weight, gptq_dtype dtype, int64_t m,
+                             int64_t d, double eps, void *S, gptq_mx_format format, uint8_t *codes, uint8_t *scales,
+                             void *stream) {
+    g_err.clear();
+    gptq_status s = check_norm(dtype, m, d, eps);
+    if (s != GPTQ_OK) return s;
+    if (!valid_format(format)) return fail(GPTQ_EINVAL, "format must be GPTQ_MX_FP8 or GPTQ_MX_FP4");
+    if (m == 0) return GPTQ_OK;
+    if (!X || !weight) return fail(GPTQ_EINVAL, "a required pointer is NULL");
+    if ((s = check_mx(codes, scales)) != GPTQ_OK) return s;
+    gptq::RmsNorm a{};
+    a.m = m;
+    a.d = d;
+    a.bf16 = raw(dtype) == GPTQ_BF16;
+    a.X = X;
+    a.residual = residual;
+    a.weight = weight;
+    a.eps = eps;
+    a.S = S;
+    a.codes = codes;
+    a.scales = scales;
+    a.fmt = raw(format);
+    HIPCHECK(gptq::rms_norm_launch(a, (hipStream_t)stream));
+    return GPTQ_OK;
+}
+
+size_t gptq_rms_norm_backward_workspace_size(int64_t m, int64_t d) {
+    return check_rows(m, d) != GPTQ_OK ? 0 : gptq::rms_norm_backward_ws(m, d);
+}
+
+gptq_status gptq_rms_norm_backward(const void *dY, const void *S, const void *weight, const void *dS,
+                                   gptq_dtype dtype, int64_t m, int64_t d, double eps, void *dX, float *dweight,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+    g_err.clear();
+    gptq_status s = check_norm(dtype, m, d, eps);
+    if (s != GPTQ_OK) return s;
+    if (m > 0 && (!dY || !S || !weight || !dX)) return fail(GPTQ_EINVAL, "a required pointer is NULL");
+    s = check_ws(workspace, workspace_bytes, dweight ? gptq::rms_norm_backward_ws(m, d) : 0);
+    if (s != GPTQ_OK) return s;
+    gptq::RmsNormBackward a{};
+    a.m = m;
+    a.d = d;
+    a.bf16 = raw(dtype) == GPTQ_BF16;
+    a.dY = dY;
+    a.S = S;
+    a.weight = weight;
+    a.dS = dS;
+    a.eps = eps;
+    a.dX = dX;
+    a.dweight = dweight;
+    a.ws = (char *)workspace;
+    HIPCHECK(gptq::rms_norm_backward_launch(a, (hipStream_t)stream));
+    return GPTQ_OK;
 }
 
 gptq_status gptq_inverse_factor(const float *H, int64_t d_in, float damp, int act_order, int32_t *perm, float *U,

@@ -163,9 +163,25 @@ struct PackedLayer {
     const float *scales;    // [G][d_out]
     const float *zeros;     // [G][d_out]
 };
+// Microscaled (MX) matrices: blocks of 32 columns share a power of two, rows
+// padded to whole MX_PAD columns (codes 0, scale bytes 0).
+//   codes   [rows][mx_row_bytes]  e4m3 a byte each, or e2m1 two to a byte, the
+//           even column in the low half
+//   scales  [mx_steps][rows][4]   byte e stands for 2^(e - 127), 255 for NaN;
+//           block b of row r at [b / 4][r][b % 4]
+constexpr int MX_BLOCK = 32, MX_PAD = 128;
+constexpr int MX_FP8 = 0, MX_FP4 = 1;
+static constexpr inline int64_t mx_steps(int64_t d) { return cdiv(d, MX_PAD); }
+static constexpr inline int64_t mx_row_bytes(int64_t d, int fmt) {
+    return mx_steps(d) * (fmt == MX_FP4 ? MX_PAD / 2 : MX_PAD);
+}
+struct MxMatrix {
+    const uint8_t *codes, *scales;
+    int fmt;
+};
 struct FusedShape {
     int64_t m, d_out, d_in;
-    int bits, group;        // group: effective group size
+    int bits, group;        // group: effective group size (bits 0: an MX layer in 4 bits)
     int ngroups;
     int layers;             // 1, or 2: the gated pair (gate, up)
     int in_bf16, out_bf16;  // dtype of A / dY and its kin, and of Y / dA
@@ -174,6 +190,7 @@ struct FusedForward {
     FusedShape s;
     const void *A;          // [m][d_in]
     PackedLayer w[2];
+    MxMatrix mx;            // the layer where bits is 0
     const int32_t *perm;    // NULL: identity
     const void *bias[2];    // NULL: none
     int bias_bf16, act;
@@ -188,6 +205,7 @@ struct FusedBackward {
     const void *pre[2];     // saved pre-activations (Z, or G and U)
     int act;
     PackedLayer w[2];
+    MxMatrix mx;
     const int32_t *perm;
     void *dA;               // [m][d_in]
     float *dbias[2];        // NULL: not formed
@@ -197,5 +215,59 @@ size_t fused_forward_ws(const FusedShape &s);
 size_t fused_backward_ws(const FusedShape &s);
 hipError_t fused_forward_launch(const FusedForward &a, hipStream_t st);
 hipError_t fused_backward_launch(const FusedBackward &a, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// MX formats (mx_quant.hip) and products with MX weights (mx_gemm.hip,
+// mx_skinny.hip; the dense form above where activations are bf16 or fp32)
+// ---------------------------------------------------------------------------
+hipError_t mx_quantize_launch(const void *X, int x_bf16, int64_t rows, int64_t d, int fmt, uint8_t *codes,
+                              uint8_t *scales, hipStream_t st);
+hipError_t mx_dequantize_launch(const MxMatrix &x, int64_t rows, int64_t d, void *Y, int y_bf16, hipStream_t st);
+
+struct MxLinear {
+    int64_t m, d_out, d_in;
+    const void *A;          // [m][d_in] bf16 or fp32, or NULL: the activations are `a`
+    int a_bf16;
+    MxMatrix a, w;
+    const void *bias;       // NULL: none
+    int bias_bf16, act;
+    const void *residual;   // NULL: none
+    void *Y, *pre;          // pre: NULL: not kept
+    int out_bf16;
+    char *ws;
+};
+// a_kind: MX_FP8, MX_FP4, or MX_ACT_F32, MX_ACT_BF16
+constexpr int MX_ACT_F32 = 2, MX_ACT_BF16 = 3;
+size_t mx_linear_ws(int64_t m, int64_t d_out, int64_t d_in, int a_kind, int out_bf16);
+hipError_t mx_linear_launch(const MxLinear &a, hipStream_t st);
+// shapes with bits 0, ngroups = blocks of a row
+size_t mx_linear_backward_ws(const FusedShape &s);
+hipError_t mx_linear_backward_launch(const FusedBackward &a, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// Root-mean-square norm (norm.hip)
+// ---------------------------------------------------------------------------
+struct RmsNorm {
+    int64_t m, d;
+    int bf16;               // dtype of X, residual, weight, S and of a plain Y
+    const void *X, *residual, *weight;   // residual: NULL: none
+    double eps;
+    void *S;                // NULL: not written
+    void *Y;                // plain output, or NULL: MX output in `codes` and `scales`
+    uint8_t *codes, *scales;
+    int fmt;
+};
+hipError_t rms_norm_launch(const RmsNorm &a, hipStream_t st);
+struct RmsNormBackward {
+    int64_t m, d;
+    int bf16;
+    const void *dY, *S, *weight, *dS;    // dS: NULL: none
+    double eps;
+    void *dX;
+    float *dweight;         // NULL: not formed
+    char *ws;
+};
+size_t rms_norm_backward_ws(int64_t m, int64_t d);
+hipError_t rms_norm_backward_launch(const RmsNormBackward &a, hipStream_t st);
 
 }  // namespace gptq

@@ -184,6 +184,29 @@ __device__ __forceinline__ Codes8<BITS> fz_codes8(unsigned lo, unsigned hi, int 
 }
 
 // ---------------------------------------------------------------------------
+// LDS stages filled by buffer loads
+// ---------------------------------------------------------------------------
+typedef __attribute__((address_space(3))) void gm_lds_void;
+
+template <int N>
+__device__ __forceinline__ void gm_wait() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+// barrier without the fence of __syncthreads(), which would wait for every
+// stage in flight; this wave's LDS reads are drained first
+__device__ __forceinline__ void gm_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+// buffer resource over [p, p + bytes), base and size in scalar registers
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t gm_rsrc(const void *p, int64_t bytes) {
+    const uint64_t b = reinterpret_cast<uint64_t>(p);
+    const uint64_t bu = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((unsigned)(b >> 32)) << 32) |
+                        (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((unsigned)b);
+    const int n = __builtin_amdgcn_readfirstlane((int)std::min<int64_t>(std::max<int64_t>(bytes, 0), (int64_t)0x7fffffff));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)bu, (short)0, n, 0x00020000);
+}
+
+// ---------------------------------------------------------------------------
 // dense form (fused_gemm.hip)
 // ---------------------------------------------------------------------------
 size_t dense_forward_ws(const FusedShape &s);

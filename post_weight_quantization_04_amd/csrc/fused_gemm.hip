@@ -108,6 +108,7 @@ struct ForwardPrep {
     int *ea;                    // [m] exponents that undo the rows' factors
     int pairs;                  // gather from two bf16 rows staged in the launch's LDS
     PackedLayer w[2];
+    MxMatrix mx;
     int64_t d_out, nwords;
     int g, ngroups, layers;
     uint16_t *W16;              // per layer: rows [d_out], contraction [planes_w][kp]
@@ -251,11 +252,65 @@ __device__ void prep_weights(const ForwardPrep &p, unsigned b, float *lds) {
     }
 }
 
+// MX weights as f16: a row's factor brings 6 times its largest scale to [2^14,
+// 2^15); two significant bits leave them exact in f16 down to 2^-37 of that,
+// one plane therefore serves F32 results too.
+typedef __attribute__((ext_vector_type(2))) _Float16 mx_f16x2;
+// the factor of a block of scale byte `byte` in a row (or a column) whose
+// largest is `top`, as the fp32 scale that the conversion takes (it reads the
+// exponent bits; NaN for 255, 0 far below)
+__device__ __forceinline__ float mx_f16_scale(int byte, int top) {
+    return __builtin_bit_cast(float, (unsigned)(byte == 255 ? 255 : max(0, byte - top + 12 + 127)) << 23);
+}
+__device__ __forceinline__ int mx_undo(int top) { return top - 127 - 12; }   // the exponent that undoes it
+__device__ __forceinline__ int mx_top(unsigned scales) {   // largest of four scale bytes, NaN aside
+    int t = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const int s = (int)((scales >> (8 * b)) & 255u);
+        t = max(t, s == 255 ? 0 : s);
+    }
+    return t;
+}
+// rows and columns as in prep_weights: a lane takes eight codes of a row
+__device__ void prep_mx_weights(const ForwardPrep &p, unsigned b, int *lds) {
+    const int tid = threadIdx.x, d_out = (int)p.d_out;
+    const int tile = (int)(b / (unsigned)p.kchunks), kc = (int)b - tile * p.kchunks, r0 = tile * FW_ROWS;
+    const int steps = (int)mx_steps(p.d_in);
+    const unsigned *sc = (const unsigned *)p.mx.scales;
+    int top = 0;
+    for (int s = tid >> 5; s < steps; s += 8)
+        top = max(top, mx_top(sc[(int64_t)s * d_out + std::min(r0 + (tid & 31), d_out - 1)]));
+    lds[tid] = top;
+    __syncthreads();
+    const int wave = tid >> 6, lane = tid & 63, rl = 8 * wave + (lane & 7), r = r0 + rl;
+    top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, lds[32 * e + rl]);
+    if (r >= d_out) return;
+    if (kc == 0 && lane < 8) p.ew[r] = mx_undo(top);
+    const unsigned *codes = (const unsigned *)(p.mx.codes + r * mx_row_bytes(p.d_in, MX_FP4));
+    const int kend = std::min((int)p.kp, (kc + 1) * FW_K);
+#pragma unroll 4
+    for (int k0 = kc * FW_K + 8 * (lane >> 3); k0 < kend; k0 += 64) {
+        const unsigned w = codes[k0 >> 3];
+        const float s = mx_f16_scale((int)((sc[(int64_t)(k0 >> 7) * d_out + r] >> (8 * ((k0 >> 5) & 3))) & 255u), top);
+        const mx_f16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0);
+        const mx_f16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1);
+        const mx_f16x2 x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2);
+        const mx_f16x2 x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3);
+        *(f16x8 *)(p.W16 + operand_at(r, k0, p.kp)) = f16x8{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
+    }
+}
+
+// (BITS 0: an MX layer)
 template <int BITS>
 __global__ __launch_bounds__(256) void forward_prep_kernel(ForwardPrep p) {
     extern __shared__ __attribute__((aligned(16))) char dyn[];
     if ((int64_t)blockIdx.x < p.row_blocks)
         prep_rows(p, 2 * (int64_t)blockIdx.x, dyn);
+    else if constexpr (BITS == 0)
+        prep_mx_weights(p, (unsigned)((int64_t)blockIdx.x - p.row_blocks), (int *)dyn);
     else
         prep_weights<BITS>(p, (unsigned)((int64_t)blockIdx.x - p.row_blocks), (float *)dyn);
 }
@@ -276,6 +331,7 @@ struct BackwardPrep {
     int *ea;                    // [m] exponents that undo them
     float *bias_part;           // [row blocks][layers][d_out], or NULL: no bias gradients
     PackedLayer w[2];
+    MxMatrix mx;
     const int32_t *perm;
     int64_t d_in, nwords;
     int g, ngroups, wvec;       // wvec: four rows' words load together
@@ -383,6 +439,15 @@ __device__ __forceinline__ void form_dz8(const BackwardPrep &p, int64_t i, int64
 template <int NW>
 __device__ __forceinline__ void group_range(const BackwardPrep &p, int gi) {
     float mx = 0.f;
+    if (p.mx.codes) {   // an MX layer: the largest scale bytes of block gi's columns
+        for (int64_t r = threadIdx.x; r < p.d_out; r += 64 * NW) {
+            const uint8_t s = p.mx.scales[((int64_t)(gi >> 2) * p.d_out + r) * 4 + (gi & 3)];
+            mx = fmaxf(mx, s == 255 ? 0.f : (float)s);
+        }
+        mx = block_max<NW>(mx);
+        if (threadIdx.x == 0) p.fg[gi] = mx;
+        return;
+    }
     for (int l = 0; l < p.layers; ++l)
         for (int64_t r = threadIdx.x; r < p.d_out; r += 64 * NW)
             mx = fmaxf(mx, finite_abs(p.w[l].scales[(int64_t)gi * p.d_out + r]));
@@ -570,11 +635,52 @@ __device__ void prep_weights_t(const BackwardPrep &p, unsigned b) {
     }
 }
 
+// the same for an MX layer: the eight rows' scales, of one block, relative to
+// the largest of the block's columns
+__device__ void prep_mx_weights_t(const BackwardPrep &p, unsigned b) {
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const unsigned rtiles = (unsigned)((p.kp + BW_ROWS - 1) / BW_ROWS), tc = b / rtiles;
+    const int64_t r0 = (int64_t)(b - tc * rtiles) * BW_ROWS + 32 * wave + 8 * (lane & 3);
+    const int64_t k0 = (int64_t)tc * BW_COLS + 8 * (lane >> 2);
+    if (r0 >= p.kp || k0 >= p.d_in) return;
+    const int top = (int)p.fg[k0 >> 5];
+    const int64_t row_bytes = mx_row_bytes(p.d_in, MX_FP4);
+    unsigned code[8], sc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {   // (rows past the end: the last one again, as zeros)
+        const int64_t r = std::min(r0 + e, p.d_out - 1);
+        code[e] = *(const unsigned *)(p.mx.codes + r * row_bytes + (k0 >> 1));
+        sc[e] = ((const unsigned *)p.mx.scales)[(k0 >> 7) * p.d_out + r];
+    }
+    mx_f16x2 h[8][4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const bool in = r0 + e < p.d_out;
+        const unsigned w = in ? code[e] : 0u;
+        const float s = mx_f16_scale(in ? (int)((sc[e] >> (8 * ((k0 >> 5) & 3))) & 255u) : 0, top);
+        h[e][0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0);
+        h[e][1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1);
+        h[e][2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2);
+        h[e][3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (k0 + k >= p.d_in) break;
+        f16x8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = h[e][k >> 1][k & 1];
+        *(f16x8 *)(p.W16 + operand_at(k0 + k, r0, p.kp)) = v;
+        if (r0 == 0) p.ew[k0 + k] = mx_undo(top);
+    }
+}
+
 template <int BITS>
 __global__ __launch_bounds__(256) void backward_prep_kernel(BackwardPrep p) {
     __shared__ float lds[2048];
     if ((int64_t)blockIdx.x < p.dz_blocks)
         prep_dz(p, blockIdx.x, lds);
+    else if constexpr (BITS == 0)
+        prep_mx_weights_t(p, (unsigned)((int64_t)blockIdx.x - p.dz_blocks));
     else
         prep_weights_t<BITS>(p, (unsigned)((int64_t)blockIdx.x - p.dz_blocks));
 }
@@ -599,8 +705,8 @@ struct Gemm {
     const uint16_t *A, *B;      // f16 operands of m rows, and of n rows for each layer
     int64_t lda, ldb;           // contraction elements of a row, all planes
     int64_t kp;                 // elements of one pass over the contraction (whole stages)
-    int passes;                 // pass 1 reads B's second plane, pass 2 (with exact: pass 0) A's
-    int exact;
+    int passes;                 // pass 1 reads B's second plane (b_plane further on; 0: B has one)
+    int a_pass;                 // the pass that reads A's second plane
     int64_t a_plane, b_plane;   // elements between the planes of a row
     int64_t m, n;
     int layers;                 // 2: the gated pair's forward product
@@ -667,26 +773,6 @@ __device__ __forceinline__ void epilogue(const Gemm &p, const Columns<GATED, W> 
     store(p.Y, y);
 }
 
-typedef __attribute__((address_space(3))) void gm_lds_void;
-
-template <int N>
-__device__ __forceinline__ void gm_wait() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
-// barrier without the fence of __syncthreads(), which would wait for every
-// stage in flight; this wave's LDS reads are drained first
-__device__ __forceinline__ void gm_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-// buffer resource over [p, p + bytes), base and size in scalar registers
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t gm_rsrc(const void *p, int64_t bytes) {
-    const uint64_t b = reinterpret_cast<uint64_t>(p);
-    const uint64_t bu = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((unsigned)(b >> 32)) << 32) |
-                        (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((unsigned)b);
-    const int n = __builtin_amdgcn_readfirstlane((int)std::min<int64_t>(std::max<int64_t>(bytes, 0), (int64_t)0x7fffffff));
-    return __builtin_amdgcn_make_buffer_rsrc((void *)bu, (short)0, n, 0x00020000);
-}
-
 // C tile of 64 NJ columns n by 64 MI rows, four waves of 32 NJ by 32 MI as
 // 32 x 32 MFMA tiles.  The weights are the MFMA's first operand, so that a lane holds
 // four consecutive columns of one activation row.  Both operands move by
@@ -751,7 +837,7 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
     int left = __builtin_amdgcn_readfirstlane(spp - (st0 - pass0 * spp));
     constexpr int BYTES = (int)TILE_STAGE * 2;
     const int bsecond = (int)(p.b_plane / GK) * BYTES, asecond = (int)(p.a_plane / GK) * BYTES;
-    const int apass = p.exact ? 0 : 2;                // the pass that reads A's second plane
+    const int apass = p.a_pass;
     int bk = (st0 - pass0 * spp) * BYTES + (pass0 == 1 ? bsecond : 0);
     int ak = (st0 - pass0 * spp) * BYTES + (pass0 == apass ? asecond : 0);
     auto issue = [&](int part) {
@@ -978,6 +1064,10 @@ ForwardWs forward_layout(const FusedShape &s, char *base) {
     ForwardWs w{};
     w.planes_a = w.planes_w = s.out_bf16 ? 1 : 2;
     w.passes = s.out_bf16 ? 1 : (s.in_bf16 ? 2 : 3);
+    if (s.bits == 0) {   // MX weights are exact in one plane; bf16 activations too
+        w.planes_a = w.passes = s.out_bf16 || s.in_bf16 ? 1 : 2;
+        w.planes_w = 1;
+    }
     w.kp = pad_stage(s.d_in);
     w.rows = std::min(s.m, DENSE_ROWS);
     w.plan = plan_gemm(w.rows, s.d_out, s.layers, (int)(w.kp / GK) * w.passes);
@@ -1007,6 +1097,10 @@ BackwardWs backward_layout(const FusedShape &s, char *base) {
     BackwardWs w{};
     w.planes_a = w.planes_w = s.out_bf16 ? 1 : 2;
     w.passes = s.out_bf16 ? 1 : 3;
+    if (s.bits == 0) {
+        w.passes = w.planes_a;
+        w.planes_w = 1;
+    }
     w.kp = pad_stage(s.d_out);
     w.rows = std::min(s.m, DENSE_ROWS);
     w.plan = plan_gemm(w.rows, s.d_in, 1, (int)(w.kp / GK) * s.layers * w.passes);
@@ -1105,6 +1199,7 @@ hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st) {
         p.ea = w.ea;
         p.pairs = p.perm && p.vec && s.in_bf16 && (size_t)s.d_in * 4 <= PREP_LDS_MAX;
         for (int l = 0; l < s.layers; ++l) p.w[l] = a.w[l];
+        p.mx = a.mx;
         p.d_out = s.d_out;
         p.nwords = cdiv(s.bits * s.d_in, 32);
         p.g = s.group;
@@ -1119,6 +1214,7 @@ hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st) {
         const int64_t blocks = p.row_blocks + (i0 == 0 ? s.layers * cdiv(s.d_out, FW_ROWS) * p.kchunks : 0);
         hipError_t e = hipErrorInvalidValue;
         switch (s.bits) {
+            case 0: e = launch_forward_prep<0>(p, blocks, st); break;
             case 2: e = launch_forward_prep<2>(p, blocks, st); break;
             case 3: e = launch_forward_prep<3>(p, blocks, st); break;
             case 4: e = launch_forward_prep<4>(p, blocks, st); break;
@@ -1130,9 +1226,11 @@ hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st) {
         g.B = w.W16;
         g.lda = w.planes_a * w.kp;
         g.ldb = w.planes_w * w.kp;
-        g.kp = g.a_plane = g.b_plane = w.kp;
+        g.kp = g.a_plane = w.kp;
+        g.b_plane = w.planes_w > 1 ? w.kp : 0;
         g.passes = w.passes;
-        g.exact = w.passes == 2;
+        // (activations that are exact meet the weights' high plane as their second, in pass 0)
+        g.a_pass = s.bits == 0 ? 1 : (w.passes == 2 ? 0 : 2);
         g.m = m;
         g.n = s.d_out;
         g.layers = s.layers;
@@ -1186,6 +1284,7 @@ hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st) {
         p.fa = w.fa;
         p.ea = w.ea;
         p.bias_part = bias ? w.bias : nullptr;
+        p.mx = a.mx;
         p.perm = a.perm;
         p.d_in = s.d_in;
         p.nwords = cdiv(s.bits * s.d_in, 32);
@@ -1217,6 +1316,7 @@ hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st) {
             p.dz_blocks + (i0 == 0 ? s.layers * cdiv(w.kp, BW_ROWS) * cdiv(s.d_in, BW_COLS) : 0);
         if (blocks > 0) {
             switch (s.bits) {
+                case 0: backward_prep_kernel<0><<<(unsigned)blocks, 256, 0, st>>>(p); break;
                 case 2: backward_prep_kernel<2><<<(unsigned)blocks, 256, 0, st>>>(p); break;
                 case 3: backward_prep_kernel<3><<<(unsigned)blocks, 256, 0, st>>>(p); break;
                 case 4: backward_prep_kernel<4><<<(unsigned)blocks, 256, 0, st>>>(p); break;
@@ -1237,8 +1337,10 @@ hipError_t dense_backward_launch(const FusedBackward &a, hipStream_t st) {
         g.kp = s.layers * w.kp;
         g.lda = w.planes_a * g.kp;
         g.ldb = w.planes_w * g.kp;
-        g.a_plane = g.b_plane = g.kp;
+        g.a_plane = g.kp;
+        g.b_plane = w.planes_w > 1 ? g.kp : 0;
         g.passes = w.passes;
+        g.a_pass = s.bits == 0 ? 1 : 2;
         g.m = m;
         g.n = s.d_in;
         g.layers = 1;
