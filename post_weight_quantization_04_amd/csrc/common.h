@@ -188,7 +188,8 @@ struct FusedShape {
 };
 struct FusedForward {
     FusedShape s;
-    const void *A;          // [m][d_in]
+    const void *A;          // [m][d_in], or NULL: fp8 activations in `amx`
+    MxMatrix amx;
     PackedLayer w[2];
     MxMatrix mx;            // the layer where bits is 0
     const int32_t *perm;    // NULL: identity

@@ -99,7 +99,9 @@ __device__ __forceinline__ void put_planes(uint16_t *out, int64_t plane, int pla
 // forward operands: rows of A (gathered into processing order), weights [n][k]
 // ---------------------------------------------------------------------------
 struct ForwardPrep {
-    const void *A;
+    const void *A;              // NULL: fp8 activations in amx, all_rows of them, from row0 on
+    MxMatrix amx;
+    int64_t all_rows, row0;
     int a_bf16, vec;            // vec: whole aligned 16-byte pieces
     const int32_t *perm;
     int64_t m, d_in, kp;        // kp: d_in padded to whole stages
@@ -303,13 +305,47 @@ __device__ void prep_mx_weights(const ForwardPrep &p, unsigned b, int *lds) {
     }
 }
 
+// Two rows of fp8 activations as f16: a row's factor brings 448 times its
+// largest scale to [2^14, 2^15), four significant bits leave the values exact
+// down to 2^-35 of that
+__device__ void prep_mx_rows(const ForwardPrep &p, int64_t i0) {
+    const int64_t row_bytes = mx_row_bytes(p.d_in, MX_FP8);
+    for (int64_t i = i0; i < std::min(i0 + 2, p.m); ++i) {
+        const unsigned *sc = (const unsigned *)p.amx.scales + p.row0 + i;
+        int top = 0;
+        for (int64_t s = threadIdx.x; s < mx_steps(p.d_in); s += 256) top = max(top, mx_top(sc[s * p.all_rows]));
+        top = (int)block_max((float)top);
+        if (threadIdx.x == 0) p.ea[i] = top - 127 - 6;
+        const uint8_t *codes = p.amx.codes + (p.row0 + i) * row_bytes;
+        for (int64_t k = 8 * threadIdx.x; k < p.kp; k += 8 * 256) {
+            const u32x2 w = *(const u32x2 *)(codes + k);
+            const int byte = (int)((sc[(k >> 7) * p.all_rows] >> (8 * ((k >> 5) & 3))) & 255u);
+            const float s = __builtin_bit_cast(float, (unsigned)(byte == 255 ? 255 : max(0, byte - top + 6 + 127)) << 23);
+            f16x8 v;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const mx_f16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[h], s, false);
+                const mx_f16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[h], s, true);
+                v[4 * h] = x0[0];
+                v[4 * h + 1] = x0[1];
+                v[4 * h + 2] = x1[0];
+                v[4 * h + 3] = x1[1];
+            }
+            *(f16x8 *)(p.A16 + operand_at(i, k, p.kp)) = v;
+        }
+    }
+}
+
 // (BITS 0: an MX layer)
 template <int BITS>
 __global__ __launch_bounds__(256) void forward_prep_kernel(ForwardPrep p) {
     extern __shared__ __attribute__((aligned(16))) char dyn[];
-    if ((int64_t)blockIdx.x < p.row_blocks)
-        prep_rows(p, 2 * (int64_t)blockIdx.x, dyn);
-    else if constexpr (BITS == 0)
+    if ((int64_t)blockIdx.x < p.row_blocks) {
+        if (BITS == 0 && !p.A)
+            prep_mx_rows(p, 2 * (int64_t)blockIdx.x);
+        else
+            prep_rows(p, 2 * (int64_t)blockIdx.x, dyn);
+    } else if constexpr (BITS == 0)
         prep_mx_weights(p, (unsigned)((int64_t)blockIdx.x - p.row_blocks), (int *)dyn);
     else
         prep_weights<BITS>(p, (unsigned)((int64_t)blockIdx.x - p.row_blocks), (float *)dyn);
@@ -1187,7 +1223,10 @@ hipError_t dense_forward_launch(const FusedForward &a, hipStream_t st) {
     for (int64_t i0 = 0; i0 < s.m; i0 += DENSE_ROWS) {
         const int64_t m = std::min(DENSE_ROWS, s.m - i0);
         ForwardPrep p{};
-        p.A = at(a.A, i0 * s.d_in, s.in_bf16);
+        p.A = a.A ? at(a.A, i0 * s.d_in, s.in_bf16) : nullptr;
+        p.amx = a.amx;
+        p.all_rows = s.m;
+        p.row0 = i0;
         p.a_bf16 = s.in_bf16;
         p.vec = s.d_in % 8 == 0 && aligned(a.A, 16);
         p.perm = a.perm;

@@ -8,6 +8,13 @@
 // from the lanes of half b.  A stage of 128 columns holds four blocks; the
 // s-th of its two MFMAs takes blocks s and 2 + s, so that a lane's two scale
 // bytes lie side by side and the MFMA selects one by its immediate.
+//
+// Precision.  Products of two e2m1 operands add exactly into fp32.  With an e4m3
+// operand the MFMA aligns a group's products to the largest and keeps about 14
+// bits below it (measured: 2^-15 to 2^-14 of the sum of magnitudes, for any
+// length).  A BF16 result rounds at 2^-9; an F32 result of fp8 activations is
+// formed on the 16-bit matrix cores instead (the dense form of the fused
+// products, mx_skinny.hip), where both operands are exact.
 #include "mx.h"
 
 #include <algorithm>
@@ -354,13 +361,13 @@ hipError_t mx_gemm_launch(const MxLinear &a, hipStream_t st) {
 
 size_t mx_linear_ws(int64_t m, int64_t d_out, int64_t d_in, int a_kind, int out_bf16) {
     if (m == 0 || mx_skinny_takes(m, d_out, d_in, a_kind)) return 0;
-    if (a_kind == MX_FP8 || a_kind == MX_FP4) return mx_gemm_ws(m, d_out, d_in, a_kind);
+    if (a_kind == MX_FP4 || (a_kind == MX_FP8 && out_bf16)) return mx_gemm_ws(m, d_out, d_in, a_kind);
     FusedShape s{};
     s.m = m;
     s.d_out = d_out;
     s.d_in = d_in;
     s.layers = 1;
-    s.in_bf16 = a_kind == MX_ACT_BF16;
+    s.in_bf16 = a_kind != MX_ACT_F32;   // (fp8 activations are exact in f16 too)
     s.out_bf16 = out_bf16;
     return dense_forward_ws(s);
 }
@@ -368,15 +375,16 @@ size_t mx_linear_ws(int64_t m, int64_t d_out, int64_t d_in, int a_kind, int out_
 hipError_t mx_linear_launch(const MxLinear &a, hipStream_t st) {
     const int kind = a.A ? (a.a_bf16 ? MX_ACT_BF16 : MX_ACT_F32) : a.a.fmt;
     if (mx_skinny_takes(a.m, a.d_out, a.d_in, kind)) return mx_skinny_launch(a, st);
-    if (!a.A) return mx_gemm_launch(a, st);
+    if (kind == MX_FP4 || (kind == MX_FP8 && a.out_bf16)) return mx_gemm_launch(a, st);
     FusedForward f{};
     f.s.m = a.m;
     f.s.d_out = a.d_out;
     f.s.d_in = a.d_in;
     f.s.layers = 1;
-    f.s.in_bf16 = a.a_bf16;
+    f.s.in_bf16 = kind != MX_ACT_F32;
     f.s.out_bf16 = a.out_bf16;
     f.A = a.A;
+    f.amx = a.a;
     f.mx = a.w;
     f.bias[0] = a.bias;
     f.bias_bf16 = a.bias_bf16;

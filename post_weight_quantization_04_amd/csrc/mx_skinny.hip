@@ -12,6 +12,9 @@
 //                           operands take the contraction in that order).  fp32
 //                           activations are cut into three bf16 terms (8 bits
 //                           each, together all 24): three times the MFMAs.
+//   fp8, F32 results        activations and weights both as bf16, exactly: the
+//                           scaled MFMA adds the products of e4m3 operands with
+//                           about 14 bits below the largest (see mx_gemm.hip)
 // The waves' sums meet in LDS and are added in their order.
 #include "mx.h"
 
@@ -78,7 +81,18 @@ __device__ __forceinline__ bf16x8 codes_bf16(unsigned w, float scale) {
     return __builtin_bit_cast(bf16x8, u32x4{u[0], u[1], u[2], u[3]});
 }
 
-// KIND: MX_FP8, MX_FP4, MX_ACT_F32 or MX_ACT_BF16; MT: 16-row tiles of activations
+// eight e4m3 codes of a block times its scale
+__device__ __forceinline__ bf16x8 codes8_bf16(u32x2 w, float scale) {
+    const unsigned u[4] = {__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], scale, false)),
+                           __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], scale, true)),
+                           __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], scale, false)),
+                           __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], scale, true))};
+    return __builtin_bit_cast(bf16x8, u32x4{u[0], u[1], u[2], u[3]});
+}
+
+// KIND: MX_FP8, MX_FP4, MX_ACT_F32, MX_ACT_BF16, or WIDE_FP8 (fp8 as bf16);
+// MT: 16-row tiles of activations
+constexpr int WIDE_FP8 = 4;
 template <int KIND, int MT>
 __global__ __launch_bounds__(64 * SK_WAVES) void mx_skinny_kernel(SkinnyArgs p) {
     __shared__ f32x4 lds[SK_WAVES][MT][64];
@@ -136,7 +150,13 @@ __global__ __launch_bounds__(64 * SK_WAVES) void mx_skinny_kernel(SkinnyArgs p) 
                     const bf16x8 wb = codes_bf16(w[u][j], scale);
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
-                        if constexpr (KIND == MX_ACT_BF16) {
+                        if constexpr (KIND == WIDE_FP8) {
+                            const unsigned as = ((const unsigned *)p.a.scales)[s * p.m + arow[t]];
+                            const u32x2 ac = *(const u32x2 *)(p.a.codes + arow[t] * p.a_bytes + k + 8 * j);
+                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                wb, codes8_bf16(ac, __builtin_bit_cast(float, ((as >> (8 * g)) & 255u) << 23)), acc[t],
+                                0, 0, 0);
+                        } else if constexpr (KIND == MX_ACT_BF16) {
                             acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, act_bf16(p, arow[t], k + 8 * j),
                                                                             acc[t], 0, 0, 0);
                         } else {
@@ -203,7 +223,8 @@ hipError_t mx_skinny_launch(const MxLinear &a, hipStream_t st) {
     p.a_bytes = a.A ? 0 : mx_row_bytes(a.d_in, a.a.fmt);
     p.vec = a.d_in % 8 == 0 && reinterpret_cast<uintptr_t>(a.A) % 16 == 0;
     p.out = mx_epilogue_of(a);
-    if (!a.A) return a.a.fmt == MX_FP8 ? launch<MX_FP8>(p, st) : launch<MX_FP4>(p, st);
+    if (!a.A && a.a.fmt == MX_FP8) return a.out_bf16 ? launch<MX_FP8>(p, st) : launch<WIDE_FP8>(p, st);
+    if (!a.A) return launch<MX_FP4>(p, st);
     return a.a_bf16 ? launch<MX_ACT_BF16>(p, st) : launch<MX_ACT_F32>(p, st);
 }
 

@@ -13,6 +13,8 @@ Tolerances, from the arithmetic (a rounding is off by at most half a step:
     11 bits, 2^-11 T, and half a bf16 step of the result; an F32 result of it:
     operands held to 22 bits, 2^-22 T, one term of products dropped, 2^-22 T;
     at the bottom of a row's shared range K 2^-38 max|a| max|w|;
+  * FP8 activations with a BF16 result: the matrix cores keep 14 bits below the
+    largest product of a group, 2^-13 T;
   * an activation passes errors on with its largest slope (below 1.13) and adds
     a few fp32 steps of its argument, 2^-20 (|z| + 1);
   * a norm's plain output: half a step (all else in 64 bits); its gradients:
@@ -252,6 +254,8 @@ def bounds(kind, out, m, a64, w64, dense):
     T = a64.abs() @ w64.abs().t()
     K = a64.shape[1]
     e = 2.0 ** -24 * (K + 100) * T
+    if kind == "fp8" and out == "bf16":
+        e = e + 2.0 ** -13 * T
     if dense:
         if kind == "f32" or kind == "dz":
             e = e + (2.0 ** -11 if out == "bf16" else 2.0 ** -21) * T
@@ -280,12 +284,27 @@ def test_linear(m, n, k, act, bias, res, save, kind, out):
     y, z = got if save else (got, None)
     assert y.dtype == DT[out]
     z64 = a64 @ w64.t() + (b.double() if bias else 0)
-    e = bounds(kind, out, m, a64, w64, m > 64 and kind in DT) + 2.0 ** -24 * z64.abs()
+    e = bounds(kind, out, m, a64, w64, m > 64 and (kind in DT or (kind, out) == ("fp8", "f32"))) + 2.0 ** -24 * z64.abs()
     if save:
         assert ((z.double() - z64).abs() <= e + HALF_STEP[out] * (z64.abs() + e)).all()
     y64 = act64(z64, act) + (r.double() if res else 0)
     e = SLOPE * e + (2.0 ** -20 * (z64.abs() + 1) if act != "none" else 0) + 2.0 ** -24 * y64.abs()
     assert ((y.double() - y64).abs() <= e + HALF_STEP[out] * (y64.abs() + e)).all()
+
+
+@pytest.mark.parametrize("m", [20, 150])
+def test_fp8_activations_of_wide_range_in_fp32(m):
+    """Elements and blocks that span the format's range: an F32 result adds their products in fp32, not in the
+    scaled matrix cores' 14 bits."""
+    n, k = 60, 640
+    x = gauss(1, m, k) * torch.exp2(torch.randint(-17, 1, (m, k), device=DEV).float()) * 448
+    t, a64 = make_acts("fp8", x)
+    wq = P.mx_quantize(gauss(2, n, k), "fp4")
+    w64 = values_of(wq)
+    got = P.mx_linear(t, wq, out_dtype=torch.float32)
+    want = a64 @ w64.t()
+    assert ((got.double() - want).abs() <= bounds("fp8", "f32", m, a64, w64, m > 64)).all()
+    assert float((got.double() - want).norm() / want.norm()) < 1e-6
 
 
 BACK = [(1, 48, 256, "none", False), (7, 333, 1000, "silu", True), (65, 100, 31, "gelu", True),
