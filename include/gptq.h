@@ -466,7 +466,7 @@ GPTQ_API gptq_status gptq_mx_linear_backward(const void *dY, gptq_dtype dy_dtype
  * Row sums in 64 bits; a plain Y is rounded once from 64 bits, gradients are
  * formed in fp32 and rounded once.  All results are deterministic.
  * Limits: d in [1, 2^19], m in [0, 2^31 - 1], eps finite and >= 0.  m == 0 leaves
- * dweight zero and is a no-op otherwise.  workspace (backward, with dweight):
+ * dweight zero and is a no-op otherwise.  workspace (backward):
  * gptq_rms_norm_backward_workspace_size bytes, 256-byte aligned, in any state.
  * Nothing synchronizes; every call can be captured into a graph.  Errors: EINVAL,
  * ENOMEM, EHIP.

@@ -502,7 +502,10 @@ class _DeviceCall:
                                      "primals of dual tensors")
 
     def empty(self, shape, dtype=None):
-        return _torch().empty(shape, dtype=dtype or self.out_dtype, device=self.device)
+        # (the strides given: a third less time than torch.empty takes)
+        n = len(shape)
+        strides = (shape[1], 1) if n == 2 else (1,) if n == 1 else (shape[1] * shape[2], shape[2], 1)
+        return _TORCH.empty_strided(shape, strides, dtype=dtype or self.out_dtype, device=self.device)
 
     def workspace(self, need):
         """(owner, pointer, bytes): the caller's when it suffices, otherwise allocated."""
@@ -735,10 +738,12 @@ class _MxCall(_DeviceCall):
 
     def matrix(self, t, name):
         """An MX matrix's pointers."""
-        u8 = _torch().uint8
-        codes, scales = _mx_shapes(t.codes.shape[0], t.d, t.format)
-        return (_operand(t.codes, f"{name}.codes", u8, codes, self.device),
-                _operand(t.scales, f"{name}.scales", u8, scales, self.device))
+        c, s, device, u8 = t.codes, t.scales, self.device, _TORCH.uint8
+        codes, scales = _mx_shapes(c.shape[0], t.d, t.format)
+        if (c.dtype is u8 and s.dtype is u8 and c.shape == codes and s.shape == scales and c.device == device
+                and s.device == device and c.is_contiguous() and s.is_contiguous()):
+            return c.data_ptr(), s.data_ptr()
+        return (_operand(c, f"{name}.codes", u8, codes, device), _operand(s, f"{name}.scales", u8, scales, device))
 
     def new_matrix(self, rows, d, format):
         u8 = _torch().uint8
@@ -749,7 +754,8 @@ class _MxCall(_DeviceCall):
 def _mx_tensor(t, name, format=None):
     if not isinstance(t, MxTensor):
         raise TypeError(f"{name} must be an MxTensor")
-    _mx_format(t.format)
+    if t.format not in MX_FORMATS:
+        _mx_format(t.format)
     if format is not None and t.format != format:
         raise ValueError(f"{name} must be in {format}, got {t.format}")
     _require(t.codes, f"{name}.codes", ndim=2)
@@ -926,7 +932,7 @@ def rms_norm_backward(dY, S, weight, eps=1e-6, dS=None, weight_grad=True, worksp
     with f:
         dX = f.empty((m, d), dY.dtype)
         dw = f.empty((d,), _torch().float32) if weight_grad else None
-        _own, ws, wsb = f.workspace(rms_norm_backward_workspace_size(m, d) if weight_grad else 0)
+        _own, ws, wsb = f.workspace(rms_norm_backward_workspace_size(m, d))
         _check(_lib().gptq_rms_norm_backward(dY.data_ptr(), s, w, t, code, m, d, float(eps), dX.data_ptr(),
                                              dw.data_ptr() if weight_grad else None, ws, wsb, f.stream))
     return dX, dw

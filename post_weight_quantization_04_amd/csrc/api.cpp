@@ -992,7 +992,7 @@ gptq_status gptq_rms_norm_backward(const void *dY, const void *S, const void *we
     gptq_status s = check_norm(dtype, m, d, eps);
     if (s != GPTQ_OK) return s;
     if (m > 0 && (!dY || !S || !weight || !dX)) return fail(GPTQ_EINVAL, "a required pointer is NULL");
-    s = check_ws(workspace, workspace_bytes, dweight ? gptq::rms_norm_backward_ws(m, d) : 0);
+    s = check_ws(workspace, workspace_bytes, gptq::rms_norm_backward_ws(m, d));
     if (s != GPTQ_OK) return s;
     gptq::RmsNormBackward a{};
     a.m = m;

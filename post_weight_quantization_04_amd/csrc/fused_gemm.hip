@@ -730,6 +730,7 @@ __global__ __launch_bounds__(256) void bias_reduce_kernel(const float *part, int
     float *db = l ? db1 : db0;
     if (r >= d_out || !db) return;
     float v = more ? db[r] : 0.f;
+#pragma unroll 8
     for (int64_t b = 0; b < blocks; ++b) v += part[(b * layers + l) * d_out + r];
     db[r] = v;
 }

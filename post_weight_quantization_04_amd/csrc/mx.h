@@ -82,7 +82,8 @@ __device__ __forceinline__ void mx_ld8(const void *x, int64_t row, int64_t d, in
     }
 }
 
-// Outputs n .. n + W - 1 of activation row i from their sums
+// The epilogue of the products: bias, the pre-activation kept, activation,
+// residual.
 struct MxEpilogue {
     int64_t n;                  // outputs per row
     const void *bias;
@@ -90,30 +91,86 @@ struct MxEpilogue {
     const void *residual;
     void *Y, *pre;
     int out_bf16;
-    int vec;                    // four consecutive outputs load and store together
+    int width;                  // consecutive outputs that load and store together: 8, 4 or 1
 };
-template <int W>
-__device__ __forceinline__ void mx_epilogue(const MxEpilogue &p, int64_t i, int64_t n, f32x4 z) {
-    const int64_t o = i * p.n + n;
-    auto load = [&](const void *x, int64_t at, int bf16) {
-        if constexpr (W == 4) return fz_ld4(x, at, bf16);
-        return f32x4{fz_ld(x, at, bf16), 0.f, 0.f, 0.f};
-    };
-    auto store = [&](void *x, f32x4 v) {
-        if constexpr (W == 4)
-            fz_st4(x, o, v, p.out_bf16);
-        else
-            fz_st(x, o, v[0], p.out_bf16);
-    };
-    if (p.bias) z += load(p.bias, n, p.bias_bf16);
-    if (p.pre) store(p.pre, z);
-    f32x4 y = z;
+// eight values from column n of a row (offset o) on, `width` at a time, those
+// inside n_all (as n itself is)
+__device__ __forceinline__ void mx_ld_row8(const void *x, int64_t o, int64_t n, int64_t n_all, int bf16, int width,
+                                           float (&v)[8]) {
+    if (width == 8) {
+        fz_ld8(x, o, bf16, v);
+    } else if (width == 4) {
+        const bool more = n + 4 < n_all;
+        const f32x4 a = fz_ld4(x, o, bf16), b = fz_ld4(x, more ? o + 4 : o, bf16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = a[e];
+            v[4 + e] = b[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fz_ld(x, n + e < n_all ? o + e : o, bf16);
+    }
+}
+__device__ __forceinline__ void mx_st_row8(void *x, int64_t o, int64_t n, int64_t n_all, int bf16, int width,
+                                           const float (&v)[8]) {
+    if (width == 8) {
+        if (bf16) {
+            *(u32x4 *)((uint16_t *)x + o) = u32x4{fz_pack_bf16(v[0], v[1]), fz_pack_bf16(v[2], v[3]),
+                                                  fz_pack_bf16(v[4], v[5]), fz_pack_bf16(v[6], v[7])};
+        } else {
+            fz_st4(x, o, f32x4{v[0], v[1], v[2], v[3]}, 0);
+            fz_st4(x, o + 4, f32x4{v[4], v[5], v[6], v[7]}, 0);
+        }
+    } else if (width == 4) {
+        fz_st4(x, o, f32x4{v[0], v[1], v[2], v[3]}, bf16);
+        if (n + 4 < n_all) fz_st4(x, o + 4, f32x4{v[4], v[5], v[6], v[7]}, bf16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (n + e < n_all) fz_st(x, o + e, v[e], bf16);
+    }
+}
+// R rows (those below m) of eight outputs from column n, inside the row, on:
+// their sums z become the outputs.  Loads first, so that they overlap.
+template <int R>
+__device__ __forceinline__ void mx_epilogue(const MxEpilogue &p, int64_t m, const int64_t (&row)[R], int64_t n,
+                                            const float (&bias)[8], float (&z)[R][8]) {
+    float res[R][8];
+    if (p.residual) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            mx_ld_row8(p.residual, std::min(row[r], m - 1) * p.n + n, n, p.n, p.out_bf16, p.width, res[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[r][e] += bias[e];
+    if (p.pre) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (row[r] < m) mx_st_row8(p.pre, row[r] * p.n + n, n, p.n, p.out_bf16, p.width, z[r]);
+    }
     fz_with_act(p.act, [&](auto act) {
 #pragma unroll
-        for (int e = 0; e < W; ++e) y[e] = fz_act<decltype(act)::value>(z[e]);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[r][e] = fz_act<decltype(act)::value>(z[r][e]);
     });
-    if (p.residual) y += load(p.residual, o, p.out_bf16);
-    store(p.Y, y);
+    if (p.residual) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[r][e] += res[r][e];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (row[r] < m) mx_st_row8(p.Y, row[r] * p.n + n, n, p.n, p.out_bf16, p.width, z[r]);
+}
+__device__ __forceinline__ void mx_bias8(const MxEpilogue &p, int64_t n, float (&b)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = 0.f;
+    if (p.bias) mx_ld_row8(p.bias, n, n, p.n, p.bias_bf16, p.width, b);
 }
 
 // the products' forms

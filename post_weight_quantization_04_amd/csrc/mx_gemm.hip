@@ -32,7 +32,7 @@ struct MxGemm {
     int steps;                  // stages of the contraction
     MxEpilogue out;
     float *part;                // [nsplit][m][np] when nsplit > 1
-    int64_t np;                 // n padded to whole quads
+    int64_t np;                 // n padded to whole eights
     int nsplit;
     int mt, nt;                 // tiles
 };
@@ -47,15 +47,15 @@ __device__ __forceinline__ int swz8(int row) { return row & 7; }
 // stay in flight across the one barrier per stage.  Each MFMA group runs beside
 // the operand reads of the next and half of a refill.
 template <int FA, int MI, int NJ, int NBUF>
-__global__ __launch_bounds__(256) void mx_gemm_kernel(MxGemm p) {
+__global__ __launch_bounds__(256, MI * NJ == 16 ? 1 : 2) void mx_gemm_kernel(MxGemm p) {
     constexpr int BM = 64 * MI, BN = 64 * NJ;
     constexpr int AROW = FA == MX_FP4 ? 64 : 128, AQ = AROW / 64;     // bytes of a row's stage, reads of a fragment
     constexpr int WSIDE = BN * 64, ASIDE = BM * AROW, SSIDE = (BM + BN) * 4;
     constexpr int STAGE = WSIDE + ASIDE + SSIDE;
     constexpr int WDMA = NJ, ADMA = AQ * MI, SDMA = (MI + NJ) / 4;    // loads per wave and stage
     constexpr int PER_STAGE = WDMA + ADMA + SDMA;
-    constexpr int EROW = BN + 4;
-    __shared__ __attribute__((aligned(16))) char lds[std::max(NBUF * STAGE, 2 * 64 * EROW * 4)];
+    constexpr int EROW = 32 * NJ + 4;                                 // floats of an epilogue row (padded)
+    __shared__ __attribute__((aligned(16))) char lds[std::max(NBUF * STAGE, 4 * 64 * EROW * 4)];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave >> 1, wm = wave & 1;
@@ -226,74 +226,99 @@ __global__ __launch_bounds__(256) void mx_gemm_kernel(MxGemm p) {
     gm_wait<0>();   // the loads past the end must land before the ring is reused
     gm_barrier();
 
-    // lane (h, li), register 4 q + e of tile (j, i) <-> output 8 q + 4 h + e, row li;
-    // the sums leave through LDS, 64 rows at a time in two buffers
-    const int tid = threadIdx.x;
-    auto leave = [&](auto width, const float *out, int i) {
-        constexpr int W = decltype(width)::value, TPR = BN / W;   // threads per row of outputs
-        const int c = W * (tid % TPR);
-        const int64_t n = n0 + c;
-        if (n >= p.n) return;
-        for (int rr = tid / TPR; rr < 64; rr += 256 / TPR) {
-            const int64_t row = m0 + 32 * i + (rr >> 5) * 32 * MI + (rr & 31);
-            if (row >= p.m) continue;
-            f32x4 z = {0.f, 0.f, 0.f, 0.f};
+    // lane (h, li), register 4 q + e of tile (j, i) <-> output 8 q + 4 h + e, row li.
+    // Each wave turns 64 rows at a time around through its own part of LDS, so
+    // that it reads and writes whole row segments, 16 bytes a lane, several rows
+    // in flight together.  (Four outputs a lane and one row at a time took 23 us
+    // per tile of 256 x 256, as long as the products of K = 4096.)
+    constexpr int COLS = 32 * NJ, LPR = COLS / 8, RPP = 64 / LPR, R = 4;   // lanes per row, rows per pass
+    const int lc = 8 * (lane % LPR), lr = lane / LPR;
+    const int64_t n = n0 + wn * COLS + lc;
+    float *out = (float *)lds + wave * 64 * EROW;
+    float bias[8] = {};
+    if (p.nsplit == 1 && n < p.n) mx_bias8(p.out, n, bias);
 #pragma unroll
-            for (int e = 0; e < W; ++e) z[e] = out[rr * EROW + c + e];
-            if (W == 4 && p.nsplit > 1)
-                *(f32x4 *)(p.part + ((int64_t)split * p.m + row) * p.np + n) = z;
-            else
-                mx_epilogue<W>(p.out, row, n, z);
-        }
-    };
+    for (int i0 = 0; i0 < MI; i0 += 2) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        float *out = (float *)lds + (i & 1) * 64 * EROW;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *(f32x4 *)(out + (wm * 32 + li) * EROW + wn * 32 * NJ + 32 * j + 8 * q + 4 * h) =
-                    f32x4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
-        gm_barrier();   // (the buffer two passes back was read before the previous barrier)
-        if (p.out.vec || p.nsplit > 1)
-            leave(std::integral_constant<int, 4>{}, out, i);
-        else
-            leave(std::integral_constant<int, 1>{}, out, i);
+                for (int q = 0; q < 4; ++q)
+                    *(f32x4 *)(out + (32 * i + li) * EROW + 32 * j + 8 * q + 4 * h) =
+                        f32x4{acc[j][i0 + i][4 * q], acc[j][i0 + i][4 * q + 1], acc[j][i0 + i][4 * q + 2],
+                              acc[j][i0 + i][4 * q + 3]};
+        // (other lanes of the wave read what this one wrote)
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (n < p.n)
+#pragma unroll 1
+            for (int c0 = 0; c0 < 64 / RPP; c0 += R) {
+                int64_t row[R];
+                float z[R][8];
+#pragma unroll
+                for (int c = 0; c < R; ++c) {
+                    const int at = (c0 + c) * RPP + lr;
+                    const f32x4 z0 = *(const f32x4 *)(out + at * EROW + lc), z1 = *(const f32x4 *)(out + at * EROW + lc + 4);
+                    row[c] = m0 + wm * 32 * MI + 32 * i0 + at;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        z[c][e] = z0[e];
+                        z[c][4 + e] = z1[e];
+                    }
+                }
+                if (p.nsplit > 1) {
+#pragma unroll
+                    for (int c = 0; c < R; ++c) {
+                        if (row[c] >= p.m) continue;
+                        float *part = p.part + ((int64_t)split * p.m + row[c]) * p.np + n;
+                        *(f32x4 *)part = f32x4{z[c][0], z[c][1], z[c][2], z[c][3]};
+                        *(f32x4 *)(part + 4) = f32x4{z[c][4], z[c][5], z[c][6], z[c][7]};
+                    }
+                } else {
+                    mx_epilogue(p.out, p.m, row, n, bias, z);
+                }
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (read before the next rows overwrite them)
     }
 }
 
-// the splits' sums in split order, and the epilogue: W outputs per thread
-template <int W>
+// the splits' sums in split order, and the epilogue: eight outputs per thread
 __global__ __launch_bounds__(256) void mx_split_reduce_kernel(MxGemm p) {
-    const int64_t per = (p.n + W - 1) / W;
+    const int64_t per = p.np / 8;
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (t >= p.m * per) return;
-    const int64_t i = t / per, n = W * (t - i * per);
-    f32x4 z = {0.f, 0.f, 0.f, 0.f};
+    const int64_t row[1] = {t / per}, n = 8 * (t - row[0] * per);
+    float z[1][8] = {};
     for (int s = 0; s < p.nsplit; ++s) {
-        const float *z0 = p.part + ((int64_t)s * p.m + i) * p.np + n;
-        if constexpr (W == 4)
-            z += *(const f32x4 *)z0;
-        else
-            z[0] += z0[0];
+        const float *z0 = p.part + ((int64_t)s * p.m + row[0]) * p.np + n;
+        const f32x4 a = *(const f32x4 *)z0, b = *(const f32x4 *)(z0 + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            z[0][e] += a[e];
+            z[0][4 + e] += b[e];
+        }
     }
-    mx_epilogue<W>(p.out, i, n, z);
+    float bias[8];
+    mx_bias8(p.out, n, bias);
+    mx_epilogue(p.out, p.m, row, n, bias, z);
 }
 
+// Tiles of 256 x 256 where they fill half the CUs at once and K is long; otherwise
+// of 128 x 128, two groups to a CU, so that one's epilogue runs beside the
+// other's products.  Large / small, us a call: fp4 4096 x 11008 outputs K = 1024
+// 62 / 52, K = 4096 124 / 147; fp8 2048 x 28672 outputs K = 1024 93 / 70, 4096 209
+// / 202, 8192 369 / 386; fp4 1000 x 4096 outputs K = 11008 (four splits) 51 / 33.
+// k splits for grids that leave CUs idle, each of at least four stages.
 struct Plan {
     int size, mt, nt, nsplit;   // tile of 64 size rows and outputs
 };
 Plan plan_mx(int64_t m, int64_t n, int steps) {
     Plan p;
-    for (int size = 4; size >= 2; size -= 2) {
-        p.size = size;
-        p.mt = (int)cdiv(m, 64 * size);
-        p.nt = (int)cdiv(n, 64 * size);
-        const int64_t tiles = (int64_t)p.mt * p.nt;
-        p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, (int64_t)steps / 4, (int64_t)16}));
-        if (tiles >= 32 && tiles * p.nsplit >= 128) break;
-    }
+    p.size = cdiv(m, 256) * cdiv(n, 256) >= 128 && steps >= 32 ? 4 : 2;
+    p.mt = (int)cdiv(m, 64 * p.size);
+    p.nt = (int)cdiv(n, 64 * p.size);
+    const int64_t tiles = (int64_t)p.mt * p.nt;
+    p.nsplit = p.size == 4 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, (int64_t)steps / 4, 16}));
     return p;
 }
 
@@ -320,14 +345,15 @@ MxEpilogue mx_epilogue_of(const MxLinear &a) {
     e.Y = a.Y;
     e.pre = a.pre;
     e.out_bf16 = a.out_bf16;
-    e.vec = a.d_out % 4 == 0 && aligned(a.Y, 16) && (!a.residual || aligned(a.residual, 16)) &&
-            (!a.bias || aligned(a.bias, 16)) && (!a.pre || aligned(a.pre, 16));
+    const bool whole = aligned(a.Y, 16) && (!a.residual || aligned(a.residual, 16)) && (!a.bias || aligned(a.bias, 16)) &&
+                       (!a.pre || aligned(a.pre, 16));
+    e.width = !whole || a.d_out % 4 ? 1 : (a.d_out % 8 ? 4 : 8);
     return e;
 }
 
 size_t mx_gemm_ws(int64_t m, int64_t d_out, int64_t d_in, int) {
     const Plan p = plan_mx(m, d_out, (int)mx_steps(d_in));
-    return p.nsplit > 1 ? align256((size_t)p.nsplit * m * (cdiv(d_out, 4) * 4) * sizeof(float)) : 0;
+    return p.nsplit > 1 ? align256((size_t)p.nsplit * m * (cdiv(d_out, 8) * 8) * sizeof(float)) : 0;
 }
 
 hipError_t mx_gemm_launch(const MxLinear &a, hipStream_t st) {
@@ -341,7 +367,7 @@ hipError_t mx_gemm_launch(const MxLinear &a, hipStream_t st) {
     g.steps = (int)mx_steps(a.d_in);
     g.out = mx_epilogue_of(a);
     g.part = (float *)a.ws;
-    g.np = cdiv(g.n, 4) * 4;
+    g.np = cdiv(g.n, 8) * 8;
     const Plan p = plan_mx(g.m, g.n, g.steps);
     g.mt = p.mt;
     g.nt = p.nt;
@@ -352,10 +378,7 @@ hipError_t mx_gemm_launch(const MxLinear &a, hipStream_t st) {
         launch_tiles<MX_FP8>(g, p.size, st);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || g.nsplit == 1) return e;
-    if (g.out.vec)
-        mx_split_reduce_kernel<4><<<(unsigned)cdiv(g.m * cdiv(g.n, 4), 256), 256, 0, st>>>(g);
-    else
-        mx_split_reduce_kernel<1><<<(unsigned)cdiv(g.m * g.n, 256), 256, 0, st>>>(g);
+    mx_split_reduce_kernel<<<(unsigned)cdiv(g.m * (g.np / 8), 256), 256, 0, st>>>(g);
     return hipGetLastError();
 }
 

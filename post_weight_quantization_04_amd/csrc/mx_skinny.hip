@@ -179,20 +179,20 @@ __global__ __launch_bounds__(64 * SK_WAVES) void mx_skinny_kernel(SkinnyArgs p) 
 #pragma unroll
     for (int t = 0; t < MT; ++t) lds[wave][t][lane] = acc[t];
     __syncthreads();
-    // lane, element e of tile t <-> activation row 16 t + lane % 16, output n0 + 4 (lane / 16) + e
-    if (wave >= MT) return;
-    f32x4 z = lds[0][wave][lane];
+    // lane, element e of tile t <-> activation row 16 t + lane % 16, output n0 + 4 (lane / 16) + e;
+    // half a wave forms the outputs of a tile, eight per lane
+    if (wave >= MT || g >= 2) return;
+    f32x4 z0 = lds[0][wave][32 * g + r], z1 = lds[0][wave][32 * g + 16 + r];
 #pragma unroll
-    for (int w = 1; w < SK_WAVES; ++w) z += lds[w][wave][lane];
-    const int64_t i = 16 * wave + r, n = n0 + 4 * g;
-    if (i >= p.m) return;
-    if (p.out.vec) {
-        if (n < p.d_out) mx_epilogue<4>(p.out, i, n, z);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n + e < p.d_out) mx_epilogue<1>(p.out, i, n + e, f32x4{z[e], 0.f, 0.f, 0.f});
+    for (int w = 1; w < SK_WAVES; ++w) {
+        z0 += lds[w][wave][32 * g + r];
+        z1 += lds[w][wave][32 * g + 16 + r];
     }
+    const int64_t row[1] = {16 * wave + r}, n = n0 + 8 * g;
+    if (row[0] >= p.m || n >= p.d_out) return;
+    float bias[8], z[1][8] = {{z0[0], z0[1], z0[2], z0[3], z1[0], z1[1], z1[2], z1[3]}};
+    mx_bias8(p.out, n, bias);
+    mx_epilogue(p.out, p.m, row, n, bias, z);
 }
 
 template <int KIND>

@@ -139,94 +139,186 @@ struct NormBackArgs {
     int vec;
     double inv_d;
     float *part;                // [groups][d] the groups' sums of dw, or NULL
+    float *stats;               // [m][2] r and r^2 c of wide rows
     int64_t groups;
 };
 
-// A group (WPR waves) takes every groups-th row.  The weights and the group's
-// sums of dw stay in registers, NC pieces of eight columns a thread; columns
-// beyond them go through memory (their sums in the group's own row of `part`).
-template <int WPR, int NC>
-__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rms_norm_backward_kernel(NormBackArgs p) {
-    constexpr int STEP = 512 * WPR;
-    __shared__ double lds[2 * WPR];
-    const int64_t group = WPR == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-    if (group >= p.groups) return;
-    const int64_t k0 = 8 * (WPR == 1 ? threadIdx.x & 63 : threadIdx.x), d = p.a.d;
-    const int bf16 = p.a.bf16;
-    float w[NC][8], dw[NC][8] = {};
+// eight values as they lie in memory, zeros past the row's end
+template <bool BF16>
+struct Raw8 {
+    u32x4 q[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void *x, int64_t row, int64_t d, int64_t k, int vec) {
+        const int64_t o = row * d + k;
+        if (vec) {
+            const bool in = k < d;
+            const u32x4 *src = (const u32x4 *)((const char *)x + (in ? o : 0) * (BF16 ? 2 : 4));
 #pragma unroll
-    for (int c = 0; c < NC; ++c) mx_ld8(p.a.weight, 0, d, k0 + c * STEP, bf16, p.vec, w[c]);
-    for (int64_t row = group; row < p.a.m; row += p.groups) {
-        float s[NC][8], g[NC][8];
-        double dot = 0.0, sq = 0.0;   // (64 bits: squares of large values stay finite)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            mx_ld8(p.a.S, row, d, k0 + c * STEP, bf16, p.vec, s[c]);
-            mx_ld8(p.a.dY, row, d, k0 + c * STEP, bf16, p.vec, g[c]);
-        }
-        auto take = [&](const float (&s)[8], const float (&g)[8], const float (&w)[8]) {
+            for (int i = 0; i < (BF16 ? 1 : 2); ++i) q[i] = in ? src[i] : u32x4{0u, 0u, 0u, 0u};
+        } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                sq += (double)s[e] * (double)s[e];
-                dot += (double)s[e] * (double)g[e] * (double)w[e];
+                if constexpr (BF16) {
+                    const unsigned v = k + e < d ? ((const uint16_t *)x)[o + e] : 0u;
+                    q[0][e >> 1] = (e & 1) ? q[0][e >> 1] | v << 16 : v;
+                } else {
+                    q[e >> 2][e & 3] = k + e < d ? ((const unsigned *)x)[o + e] : 0u;
+                }
             }
-        };
-#pragma unroll
-        for (int c = 0; c < NC; ++c) take(s[c], g[c], w[c]);
-        for (int64_t k = k0 + NC * STEP; k < d; k += STEP) {
-            float s1[8], g1[8], w1[8];
-            mx_ld8(p.a.S, row, d, k, bf16, p.vec, s1);
-            mx_ld8(p.a.dY, row, d, k, bf16, p.vec, g1);
-            mx_ld8(p.a.weight, 0, d, k, bf16, p.vec, w1);
-            take(s1, g1, w1);
-        }
-        sq = row_sum<WPR>(sq, lds);
-        dot = row_sum<WPR>(dot, lds + (WPR > 1 ? WPR : 0));
-        const double rd = 1.0 / sqrt(sq * p.inv_d + p.a.eps);
-        const float r = (float)rd, f = (float)(rd * rd * (dot * p.inv_d));
-        auto leave = [&](int64_t k, const float (&s)[8], const float (&g)[8], const float (&w)[8], float (&dw)[8]) {
-            float x[8], t[8] = {};
-            if (p.a.dS) mx_ld8(p.a.dS, row, d, k, bf16, p.vec, t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] = r * (g[e] * w[e] - s[e] * f) + t[e];
-                dw[e] += g[e] * (s[e] * r);
-            }
-            put8(p.a.dX, row, d, k, bf16, p.vec, x);
-        };
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (k0 + c * STEP < d) leave(k0 + c * STEP, s[c], g[c], w[c], dw[c]);
-        for (int64_t k = k0 + NC * STEP; k < d; k += STEP) {
-            float s1[8], g1[8], w1[8], dw1[8] = {};
-            mx_ld8(p.a.S, row, d, k, bf16, p.vec, s1);
-            mx_ld8(p.a.dY, row, d, k, bf16, p.vec, g1);
-            mx_ld8(p.a.weight, 0, d, k, bf16, p.vec, w1);
-            if (p.part && row != group) mx_ld8(p.part, group, d, k, 0, 0, dw1);
-            leave(k, s1, g1, w1, dw1);
-            if (p.part) put8(p.part, group, d, k, 0, 0, dw1);
         }
     }
-    if (p.part)
+    __device__ __forceinline__ float at(int e) const {
+        if constexpr (BF16)
+            return __builtin_bit_cast(float, (e & 1) ? q[0][e >> 1] & 0xffff0000u : q[0][e >> 1] << 16);
+        return __builtin_bit_cast(float, +q[BF16 ? 0 : e >> 2][e & 3]);   // (of a value: of an element in place it takes the first)
+    }
+};
+
+// a row's contribution to sum S^2 and sum dY w S, in 64 bits: squares of large
+// values stay finite, and c keeps its digits where its terms cancel
+template <bool BF16>
+__device__ __forceinline__ void norm_sums(const Raw8<BF16> &s, const Raw8<BF16> &g, const Raw8<BF16> &w, double &sq,
+                                          double &dot) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (k0 + c * STEP < d) put8(p.part, group, d, k0 + c * STEP, 0, d % 4 == 0 && k0 + c * STEP + 8 <= d, dw[c]);
+    for (int e = 0; e < 8; ++e) {
+        const double v = (double)s.at(e);
+        sq += v * v;
+        if constexpr (BF16)   // (dY w of bf16 values is exact in fp32)
+            dot += v * (double)(g.at(e) * w.at(e));
+        else
+            dot += v * ((double)g.at(e) * (double)w.at(e));
+    }
+}
+// eight columns of a row: dX, and dw's terms
+template <bool BF16>
+__device__ __forceinline__ void norm_leave(const NormBackArgs &p, int64_t row, int64_t k, float r, float f,
+                                           const Raw8<BF16> &s, const Raw8<BF16> &g, const Raw8<BF16> &w,
+                                           const Raw8<BF16> &t, float (&dw)[8]) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        x[e] = r * (g.at(e) * w.at(e) - s.at(e) * f) + t.at(e);
+        dw[e] += g.at(e) * (s.at(e) * r);
+    }
+    put8(p.a.dX, row, p.a.d, k, BF16, p.vec, x);
+}
+__device__ __forceinline__ void norm_factors(const NormBackArgs &p, double sq, double dot, float &r, float &f) {
+    const double rd = 1.0 / sqrt(sq * p.inv_d + p.a.eps);
+    r = (float)rd;
+    f = (float)(rd * rd * (dot * p.inv_d));
+}
+__device__ __forceinline__ void norm_put_sums(const NormBackArgs &p, int64_t group, int64_t k, const float (&dw)[8]) {
+    if (p.part && k < p.a.d) put8(p.part, group, p.a.d, k, 0, p.a.d % 4 == 0 && k + 8 <= p.a.d, dw);
 }
 
-// dw from the groups' sums: 32 columns of a block, eight threads a column, each
-// every eighth group in turn, added in their order in 64 bits
-__global__ __launch_bounds__(256) void norm_weight_reduce_kernel(const float *part, int64_t groups, int64_t d,
-                                                                 float *dw) {
-    __shared__ double lds[256];
+// Rows that fit a group of WPR waves, eight columns a thread: read once.  A
+// group takes every groups-th row, the next one's loads in flight behind the
+// present one's sums; the weights and its sums of dw stay in registers.
+template <int WPR, bool BF16>
+__global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_backward_kernel(NormBackArgs p) {
+    constexpr int PER = WPR < 4 ? 4 / WPR : 1;   // groups of a block
+    __shared__ double lds[2][PER][2][WPR];
+    const int sub = threadIdx.x / (64 * WPR), tid = threadIdx.x % (64 * WPR);
+    const int64_t group = (int64_t)blockIdx.x * PER + sub, d = p.a.d, k = 8 * tid;
+    Raw8<BF16> w, s, g, t, s1, g1, t1;
+    w.load(p.a.weight, 0, d, k, p.vec);
+    auto load = [&](int64_t row) {
+        row = std::min(row, p.a.m - 1);
+        s1.load(p.a.S, row, d, k, p.vec);
+        g1.load(p.a.dY, row, d, k, p.vec);
+        if (p.a.dS) t1.load(p.a.dS, row, d, k, p.vec);
+    };
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) t1.q[i] = u32x4{0u, 0u, 0u, 0u};
+    float dw[8] = {};
+    load(group);
+    int turn = 0;
+    // (every group of a block makes the same number of turns: they meet at the barriers)
+    for (int64_t first = (int64_t)blockIdx.x * PER; first < p.a.m; first += p.groups, turn ^= 1) {
+        const int64_t row = first + sub;
+        s = s1;
+        g = g1;
+        t = t1;
+        load(row + p.groups);
+        double sq = 0.0, dot = 0.0;
+        norm_sums(s, g, w, sq, dot);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            sq += __shfl_xor(sq, o);
+            dot += __shfl_xor(dot, o);
+        }
+        if constexpr (WPR > 1) {   // (two buffers in turn: one barrier a row)
+            if ((tid & 63) == 0) {
+                lds[turn][sub][0][tid >> 6] = sq;
+                lds[turn][sub][1][tid >> 6] = dot;
+            }
+            __syncthreads();
+            sq = lds[turn][sub][0][0];
+            dot = lds[turn][sub][1][0];
+#pragma unroll
+            for (int i = 1; i < WPR; ++i) {
+                sq += lds[turn][sub][0][i];
+                dot += lds[turn][sub][1][i];
+            }
+        }
+        float r, f;
+        norm_factors(p, sq, dot, r, f);
+        if (row < p.a.m && k < d) norm_leave(p, row, k, r, f, s, g, w, t, dw);
+    }
+    if (group < p.groups) norm_put_sums(p, group, k, dw);
+}
+
+// Wider rows: their factors first ...
+template <bool BF16>
+__global__ __launch_bounds__(1024) void norm_factors_kernel(NormBackArgs p) {
+    __shared__ double lds[2][16];
+    const int64_t row = blockIdx.x, d = p.a.d;
+    double sq = 0.0, dot = 0.0;
+    for (int64_t k = 8 * threadIdx.x; k < d; k += 8 * 1024) {
+        Raw8<BF16> s, g, w;
+        s.load(p.a.S, row, d, k, p.vec);
+        g.load(p.a.dY, row, d, k, p.vec);
+        w.load(p.a.weight, 0, d, k, p.vec);
+        norm_sums(s, g, w, sq, dot);
+    }
+    sq = row_sum<16>(sq, lds[0]);
+    dot = row_sum<16>(dot, lds[1]);
+    if (threadIdx.x == 0) norm_factors(p, sq, dot, p.stats[2 * row], p.stats[2 * row + 1]);
+}
+// ... then 2048 columns of every groups-th row to a block
+template <bool BF16>
+__global__ __launch_bounds__(256) void norm_columns_kernel(NormBackArgs p) {
+    const int64_t k = (int64_t)blockIdx.x * 2048 + 8 * threadIdx.x, group = blockIdx.y, d = p.a.d;
+    if (k >= d) return;
+    Raw8<BF16> w;
+    w.load(p.a.weight, 0, d, k, p.vec);
+    float dw[8] = {};
+#pragma unroll 2
+    for (int64_t row = group; row < p.a.m; row += p.groups) {
+        Raw8<BF16> s, g, t;
+        s.load(p.a.S, row, d, k, p.vec);
+        g.load(p.a.dY, row, d, k, p.vec);
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) t.q[i] = u32x4{0u, 0u, 0u, 0u};
+        if (p.a.dS) t.load(p.a.dS, row, d, k, p.vec);
+        norm_leave(p, row, k, p.stats[2 * row], p.stats[2 * row + 1], s, g, w, t, dw);
+    }
+    norm_put_sums(p, group, k, dw);
+}
+
+// dw from the groups' sums: 32 columns of a block, 32 threads a column, each
+// every 32nd group in turn, added in their order in 64 bits
+__global__ __launch_bounds__(1024) void norm_weight_reduce_kernel(const float *part, int64_t groups, int64_t d,
+                                                                  float *dw) {
+    __shared__ double lds[1024];
     const int64_t k = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     double sum = 0.0;
     if (k < d)
 #pragma unroll 8
-        for (int64_t g = threadIdx.x >> 5; g < groups; g += 8) sum += (double)part[g * d + k];
+        for (int64_t g = threadIdx.x >> 5; g < groups; g += 32) sum += (double)part[g * d + k];
     lds[threadIdx.x] = sum;
     __syncthreads();
     if (threadIdx.x >= 32 || k >= d) return;
-    for (int i = 1; i < 8; ++i) sum += lds[32 * i + threadIdx.x];
+    for (int i = 1; i < 32; ++i) sum += lds[32 * i + threadIdx.x];
     dw[k] = (float)sum;
 }
 
@@ -260,9 +352,42 @@ hipError_t with_plan(const RowPlan &p, F f) {
     return hipGetLastError();
 }
 
-constexpr int64_t NORM_GROUPS = 512;   // groups of rows that sum dw at once
-int64_t norm_groups(int64_t m, const RowPlan &p) {
-    return std::min<int64_t>(m, p.wpr == 1 ? 4 * NORM_GROUPS : NORM_GROUPS);
+// The backward pass: waves of a group (0: rows wider than one group reads), and
+// the groups of rows that sum dw at once, multiples of a block's.
+struct BackPlan {
+    int wpr;
+    int64_t groups;
+};
+constexpr int64_t NORM_WAVES = 4096;
+BackPlan back_plan(int64_t m, int64_t d) {
+    BackPlan p{1, 0};
+    if (d > 8192) {
+        p.wpr = 0;
+        p.groups = std::min(m, std::max<int64_t>(1, 1024 / cdiv(d, 2048)));
+        return p;
+    }
+    while (512 * p.wpr < d) p.wpr *= 2;
+    const int64_t per = p.wpr < 4 ? 4 / p.wpr : 1;
+    p.groups = std::min(cdiv(m, per) * per, NORM_WAVES / p.wpr);
+    return p;
+}
+template <bool BF16>
+hipError_t launch_backward(const NormBackArgs &p, int wpr, hipStream_t st) {
+    const unsigned blocks = (unsigned)p.groups;
+    switch (wpr) {
+        case 1: rms_norm_backward_kernel<1, BF16><<<blocks / 4, 256, 0, st>>>(p); break;
+        case 2: rms_norm_backward_kernel<2, BF16><<<blocks / 2, 256, 0, st>>>(p); break;
+        case 4: rms_norm_backward_kernel<4, BF16><<<blocks, 256, 0, st>>>(p); break;
+        case 8: rms_norm_backward_kernel<8, BF16><<<blocks, 512, 0, st>>>(p); break;
+        case 16: rms_norm_backward_kernel<16, BF16><<<blocks, 1024, 0, st>>>(p); break;
+        default: {
+            norm_factors_kernel<BF16><<<(unsigned)p.a.m, 1024, 0, st>>>(p);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            norm_columns_kernel<BF16><<<dim3((unsigned)cdiv(p.a.d, 2048), blocks), 256, 0, st>>>(p);
+        }
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -284,7 +409,9 @@ hipError_t rms_norm_launch(const RmsNorm &a, hipStream_t st) {
 }
 
 size_t rms_norm_backward_ws(int64_t m, int64_t d) {
-    return m == 0 ? 0 : align256((size_t)norm_groups(m, row_plan(m, d)) * d * sizeof(float));
+    if (m == 0) return 0;
+    const BackPlan p = back_plan(m, d);
+    return align256((size_t)p.groups * d * sizeof(float)) + (p.wpr ? 0 : align256((size_t)m * 2 * sizeof(float)));
 }
 
 hipError_t rms_norm_backward_launch(const RmsNormBackward &a, hipStream_t st) {
@@ -293,19 +420,16 @@ hipError_t rms_norm_backward_launch(const RmsNormBackward &a, hipStream_t st) {
     p.vec = a.d % 8 == 0 && aligned16(a.dY) && aligned16(a.S) && aligned16(a.weight) && (!a.dS || aligned16(a.dS)) &&
             aligned16(a.dX);
     p.inv_d = 1.0 / (double)a.d;
-    p.part = a.dweight ? (float *)a.ws : nullptr;
-    const RowPlan plan = row_plan(a.m, a.d);
-    p.groups = norm_groups(a.m, plan);
     if (a.m > 0) {
-        const hipError_t e = with_plan(plan, [&](auto w, auto n) {
-            constexpr int W = decltype(w)::value, N = decltype(n)::value;
-            const unsigned blocks = (unsigned)(W == 1 ? cdiv(p.groups, 4) : p.groups);
-            rms_norm_backward_kernel<W, N><<<blocks, W == 1 ? 256 : 64 * W, 0, st>>>(p);
-        });
-        if (e != hipSuccess || !a.dweight) return e;
+        const BackPlan plan = back_plan(a.m, a.d);
+        p.groups = plan.groups;
+        p.part = a.dweight ? (float *)a.ws : nullptr;
+        p.stats = (float *)(a.ws + align256((size_t)p.groups * a.d * sizeof(float)));
+        const hipError_t e = a.bf16 ? launch_backward<true>(p, plan.wpr, st) : launch_backward<false>(p, plan.wpr, st);
+        if (e != hipSuccess) return e;
     }
     if (!a.dweight) return hipSuccess;
-    norm_weight_reduce_kernel<<<(unsigned)cdiv(a.d, 32), 256, 0, st>>>(p.part, a.m > 0 ? p.groups : 0, a.d, a.dweight);
+    norm_weight_reduce_kernel<<<(unsigned)cdiv(a.d, 32), 1024, 0, st>>>(p.part, p.groups, a.d, a.dweight);
     return hipGetLastError();
 }
 
