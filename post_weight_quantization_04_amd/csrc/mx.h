@@ -70,6 +70,16 @@ __device__ __forceinline__ void mx_put8(const float (&v)[8], int64_t rows, int64
     if ((piece & 3) == 0) scales[((piece >> 4) * rows + row) * 4 + ((piece >> 2) & 3)] = (uint8_t)byte;
 }
 
+// eight values to an aligned place
+__device__ __forceinline__ void mx_st8(void *x, int64_t o, int bf16, const float (&v)[8]) {
+    if (bf16) {
+        *(u32x4 *)((uint16_t *)x + o) = u32x4{fz_pack_bf16(v[0], v[1]), fz_pack_bf16(v[2], v[3]),
+                                              fz_pack_bf16(v[4], v[5]), fz_pack_bf16(v[6], v[7])};
+    } else {
+        fz_st4(x, o, f32x4{v[0], v[1], v[2], v[3]}, 0);
+        fz_st4(x, o + 4, f32x4{v[4], v[5], v[6], v[7]}, 0);
+    }
+}
 // eight values of a row from column k on, zeros past its end
 __device__ __forceinline__ void mx_ld8(const void *x, int64_t row, int64_t d, int64_t k, int bf16, int vec,
                                        float (&v)[8]) {
@@ -115,13 +125,7 @@ __device__ __forceinline__ void mx_ld_row8(const void *x, int64_t o, int64_t n, 
 __device__ __forceinline__ void mx_st_row8(void *x, int64_t o, int64_t n, int64_t n_all, int bf16, int width,
                                            const float (&v)[8]) {
     if (width == 8) {
-        if (bf16) {
-            *(u32x4 *)((uint16_t *)x + o) = u32x4{fz_pack_bf16(v[0], v[1]), fz_pack_bf16(v[2], v[3]),
-                                                  fz_pack_bf16(v[4], v[5]), fz_pack_bf16(v[6], v[7])};
-        } else {
-            fz_st4(x, o, f32x4{v[0], v[1], v[2], v[3]}, 0);
-            fz_st4(x, o + 4, f32x4{v[4], v[5], v[6], v[7]}, 0);
-        }
+        mx_st8(x, o, bf16, v);
     } else if (width == 4) {
         fz_st4(x, o, f32x4{v[0], v[1], v[2], v[3]}, bf16);
         if (n + 4 < n_all) fz_st4(x, o + 4, f32x4{v[4], v[5], v[6], v[7]}, bf16);

@@ -102,8 +102,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantMx p) {
             }
             const int64_t o = row * p.d + k;
             if (p.vec) {
-                fz_st4(p.Y, o, f32x4{v[0], v[1], v[2], v[3]}, p.bf16);
-                fz_st4(p.Y, o + 4, f32x4{v[4], v[5], v[6], v[7]}, p.bf16);
+                mx_st8(p.Y, o, p.bf16, v);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
