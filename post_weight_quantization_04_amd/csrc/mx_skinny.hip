@@ -50,27 +50,30 @@ __device__ __forceinline__ bf16x8 act_bf16(const SkinnyArgs &p, int64_t row, int
         if (k + e < p.d_in) u[e >> 1] |= (unsigned)a[k + e] << (16 * (e & 1));
     return __builtin_bit_cast(bf16x8, u);
 }
-// fp32 activations as three bf16 terms, each the leading bits of what is left
-// (truncated, so that no term overflows); infinities and NaN in the first alone
-__device__ __forceinline__ void act_terms(const SkinnyArgs &p, int64_t row, int64_t k, bf16x8 (&t)[3]) {
-    float v[8];
-    mx_ld8(p.A, row, p.d_in, k, 0, p.vec, v);
-    u32x4 u[3] = {};
+// fp32 values as N bf16 terms, each the leading bits of what is left (truncated,
+// so that no term overflows; the last of two rounded to nearest); infinities
+// and NaN in the first alone
+template <int N>
+__device__ __forceinline__ void bf16_terms(const float (&v)[8], bf16x8 (&t)[N]) {
+    u32x4 u[N] = {};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const unsigned b = __builtin_bit_cast(unsigned, v[e]), mag = b & 0x7fffffffu;
         const bool finite = mag < 0x7f800000u;
         const unsigned hi = (b & 0xffff0000u) | (mag > 0x7f800000u ? 0x400000u : 0u);
         const float r1 = finite ? v[e] - __builtin_bit_cast(float, hi) : 0.f;
-        const unsigned mid = __builtin_bit_cast(unsigned, r1) & 0xffff0000u;
-        const float r2 = r1 - __builtin_bit_cast(float, mid);
-        const unsigned lo = __builtin_bit_cast(unsigned, r2);
         u[0][e >> 1] |= (e & 1) ? hi : hi >> 16;
-        u[1][e >> 1] |= (e & 1) ? mid : mid >> 16;
-        u[2][e >> 1] |= (e & 1) ? lo & 0xffff0000u : lo >> 16;
+        if constexpr (N == 2) u[1][e >> 1] |= (unsigned)fz_to_bf16(r1) << (16 * (e & 1));
+        if constexpr (N == 3) {
+            const unsigned mid = __builtin_bit_cast(unsigned, r1) & 0xffff0000u;
+            const float r2 = r1 - __builtin_bit_cast(float, mid);
+            const unsigned lo = __builtin_bit_cast(unsigned, r2);
+            u[1][e >> 1] |= (e & 1) ? mid : mid >> 16;
+            u[N - 1][e >> 1] |= (e & 1) ? lo & 0xffff0000u : lo >> 16;
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 3; ++i) t[i] = __builtin_bit_cast(bf16x8, u[i]);
+    for (int i = 0; i < N; ++i) t[i] = __builtin_bit_cast(bf16x8, u[i]);
 }
 // a word's eight codes times 2^(scale byte - 127)
 __device__ __forceinline__ bf16x8 codes_bf16(unsigned w, float scale) {
@@ -160,8 +163,10 @@ __global__ __launch_bounds__(64 * SK_WAVES) void mx_skinny_kernel(SkinnyArgs p) 
                             acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, act_bf16(p, arow[t], k + 8 * j),
                                                                             acc[t], 0, 0, 0);
                         } else {
+                            float v[8];
                             bf16x8 a[3];
-                            act_terms(p, arow[t], k + 8 * j, a);
+                            mx_ld8(p.A, arow[t], p.d_in, k + 8 * j, 0, p.vec, v);
+                            bf16_terms<3>(v, a);
 #pragma unroll
                             for (int i = 2; i >= 0; --i)
                                 acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, a[i], acc[t], 0, 0, 0);
@@ -206,6 +211,191 @@ hipError_t launch(const SkinnyArgs &p, hipStream_t st) {
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// backward: dA = dZ W, few rows
+// ---------------------------------------------------------------------------
+// A work group takes 128 columns (a step of the weights' rows) and a range of
+// outputs r; a wave 32 outputs at a time: lane (g, l) loads 8 codes (columns 8 l ..)
+// of the 8 rows 8 g .., which it turns around in registers into the operands of
+// eight bf16 MFMAs (16 x 16 x 32), the c-th for columns 8 l + c.  The weights are
+// exact in bf16; dZ, formed from dY and the saved Z on the way, enters in two
+// bf16 terms (16 bits) for a BF16 result, three (24) for an F32 one, one where it
+// is bf16 itself.  The waves' sums meet in LDS, the ranges' in memory, both added
+// in their order.  Bias gradients: the groups of the first 128 columns add
+// their dZ over the rows.
+struct SkinnyBack {
+    const void *dY, *pre;
+    int in_bf16, act, vec;      // vec: whole aligned pieces of eight
+    int64_t m, d_out, d_in;
+    MxMatrix w;
+    int64_t w_bytes;
+    float *dbias;               // NULL: not formed
+    void *dA;
+    int out_bf16;
+    float *part;                // [nsplit][m][np]
+    int64_t np;                 // d_in padded to whole steps
+    int nsplit;
+};
+
+// dZ of activation row `row`, outputs r .. r + 7; zeros past the ends
+__device__ __forceinline__ void back_dz(const SkinnyBack &p, int64_t row, int64_t r, float (&v)[8]) {
+    const bool in = row < p.m;
+    mx_ld8(p.dY, in ? row : 0, p.d_out, in ? r : p.d_out, p.in_bf16, p.vec, v);
+    if (p.act) {
+        float z[8];
+        mx_ld8(p.pre, in ? row : 0, p.d_out, in ? r : p.d_out, p.in_bf16, p.vec, z);
+        fz_with_act(p.act, [&](auto act) {
+            constexpr int ACT = decltype(act)::value;
+            if constexpr (ACT) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = v[e] * fz_slope<ACT>(z[e]);
+            }
+        });
+    }
+}
+
+// TERMS bf16 terms of dZ; MT: 16-row tiles
+template <int TERMS, int MT>
+__global__ __launch_bounds__(64 * SK_WAVES) void mx_skinny_backward_kernel(SkinnyBack p) {
+    __shared__ float lds[SK_WAVES / 2][16][MX_PAD + 4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l = lane & 15, g = lane >> 4;
+    const int64_t tile = blockIdx.x;
+    const int split = blockIdx.y;
+    const int64_t pieces = (p.d_out + 31) / 32;           // of 32 outputs
+    const int64_t q0 = pieces * split / p.nsplit, q1 = pieces * (split + 1) / p.nsplit;
+    const unsigned *sc = (const unsigned *)p.w.scales + tile * p.d_out;
+    const uint8_t *wc = p.w.codes + tile * (MX_PAD / 2) + 4 * l;
+    f32x4 acc[8][MT];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[c][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int64_t q = q0 + wave; q < q1; q += SK_WAVES) {
+        const int64_t r0 = 32 * q + 8 * g;
+        unsigned code[8], scale[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {                     // (rows past the end: the last one, against dZ = 0 ...)
+            const int64_t r = std::min(r0 + e, p.d_out - 1);
+            code[e] = *(const unsigned *)(wc + r * p.w_bytes);
+            scale[e] = sc[r];
+        }
+        bf16x8 dz[MT][TERMS];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            float v[8];
+            back_dz(p, 16 * t + l, r0, v);
+            if (p.dbias && tile == 0) {
+                // the tile's 16 rows are the lanes of a group
+                float sum[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sum[e] = v[e];
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) sum[e] += __shfl_xor(sum[e], o);
+                }
+                if (l == 0)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (r0 + e < p.d_out) p.dbias[r0 + e] = t ? p.dbias[r0 + e] + sum[e] : sum[e];
+            }
+            bf16_terms<TERMS>(v, dz[t]);
+        }
+        u32x4 wt[8];                                      // operand c: eight rows of column 8 l + c
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            unsigned lo[2], hi[2];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                unsigned x[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // (... and weights 0, also where they stand for NaN)
+                    const bool in = r0 + e + i < p.d_out;
+                    const float s = __builtin_bit_cast(
+                        float, in ? ((scale[e + i] >> (8 * (l >> 2))) & 255u) << 23 : 0u);
+                    const unsigned w = in ? code[e + i] : 0u;
+                    switch (h) {
+                        case 0: x[i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)); break;
+                        case 1: x[i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)); break;
+                        case 2: x[i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)); break;
+                        default: x[i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3)); break;
+                    }
+                }
+                wt[2 * h][e >> 1] = (x[0] & 0xffffu) | (x[1] << 16);
+                wt[2 * h + 1][e >> 1] = (x[0] >> 16) | (x[1] & 0xffff0000u);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const bf16x8 w = __builtin_bit_cast(bf16x8, wt[c]);
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int i = TERMS - 1; i >= 0; --i)
+                    acc[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, dz[t][i], acc[c][t], 0, 0, 0);
+        }
+    }
+    // register e of lane (g, l), operand c <-> column 8 (4 g + e) + c, row l of the tile;
+    // the waves' sums, the later four first to LDS, then added to the earlier four's
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        for (int half = 1; half >= 0; --half) {
+            __syncthreads();
+            if (wave / (SK_WAVES / 2) == half) {
+                float (*out)[MX_PAD + 4] = lds[wave % (SK_WAVES / 2)];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float &x = out[l][8 * (4 * g + e) + c];
+                        x = half ? acc[c][t][e] : x + acc[c][t][e];
+                    }
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 16 * MX_PAD / 4; i += 64 * SK_WAVES) {
+            const int row = i / (MX_PAD / 4), col = 4 * (i % (MX_PAD / 4));
+            if (16 * t + row >= p.m) continue;
+            f32x4 z = *(const f32x4 *)&lds[0][row][col];
+#pragma unroll
+            for (int w = 1; w < SK_WAVES / 2; ++w) z += *(const f32x4 *)&lds[w][row][col];
+            *(f32x4 *)(p.part + ((int64_t)split * p.m + 16 * t + row) * p.np + tile * MX_PAD + col) = z;
+        }
+    }
+}
+
+// the ranges' sums, four columns per thread
+__global__ __launch_bounds__(256) void mx_skinny_join_kernel(SkinnyBack p) {
+    const int64_t per = p.np / 4, t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= p.m * per) return;
+    const int64_t i = t / per, k = 4 * (t - i * per);
+    f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int s = 0; s < p.nsplit; ++s) z += *(const f32x4 *)(p.part + ((int64_t)s * p.m + i) * p.np + k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (k + e < p.d_in) fz_st(p.dA, i * p.d_in + k + e, z[e], p.out_bf16);
+}
+
+// ranges of outputs: two work groups a CU, at least 32 outputs to a wave
+int back_splits(int64_t d_out, int64_t d_in) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>({512 / mx_steps(d_in), cdiv(d_out, 32 * SK_WAVES), 64}));
+}
+
+template <int TERMS>
+hipError_t launch_backward(const SkinnyBack &p, hipStream_t st) {
+    const dim3 grid((unsigned)mx_steps(p.d_in), (unsigned)p.nsplit);
+    switch (cdiv(p.m, 16)) {
+        case 1: mx_skinny_backward_kernel<TERMS, 1><<<grid, 64 * SK_WAVES, 0, st>>>(p); break;
+        default: mx_skinny_backward_kernel<TERMS, 2><<<grid, 64 * SK_WAVES, 0, st>>>(p); break;
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    mx_skinny_join_kernel<<<(unsigned)cdiv(p.m * (p.np / 4), 256), 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 bool mx_skinny_takes(int64_t m, int64_t, int64_t, int) { return m <= 64; }
@@ -226,6 +416,33 @@ hipError_t mx_skinny_launch(const MxLinear &a, hipStream_t st) {
     if (!a.A && a.a.fmt == MX_FP8) return a.out_bf16 ? launch<MX_FP8>(p, st) : launch<WIDE_FP8>(p, st);
     if (!a.A) return launch<MX_FP4>(p, st);
     return a.a_bf16 ? launch<MX_ACT_BF16>(p, st) : launch<MX_ACT_F32>(p, st);
+}
+
+bool mx_skinny_backward_takes(const FusedShape &s) { return s.m <= 32; }
+size_t mx_skinny_backward_ws(const FusedShape &s) {
+    return align256((size_t)back_splits(s.d_out, s.d_in) * s.m * mx_steps(s.d_in) * MX_PAD * sizeof(float));
+}
+hipError_t mx_skinny_backward_launch(const FusedBackward &a, hipStream_t st) {
+    SkinnyBack p{};
+    p.dY = a.dY;
+    p.pre = a.pre[0];
+    p.in_bf16 = a.s.in_bf16;
+    p.act = a.act;
+    p.vec = a.s.d_out % 8 == 0 && reinterpret_cast<uintptr_t>(a.dY) % 16 == 0 &&
+            (!a.act || reinterpret_cast<uintptr_t>(a.pre[0]) % 16 == 0);
+    p.m = a.s.m;
+    p.d_out = a.s.d_out;
+    p.d_in = a.s.d_in;
+    p.w = a.mx;
+    p.w_bytes = mx_row_bytes(a.s.d_in, MX_FP4);
+    p.dbias = a.dbias[0];
+    p.dA = a.dA;
+    p.out_bf16 = a.s.out_bf16;
+    p.part = (float *)a.ws;
+    p.np = mx_steps(a.s.d_in) * MX_PAD;
+    p.nsplit = back_splits(a.s.d_out, a.s.d_in);
+    if (a.s.in_bf16 && !a.act) return launch_backward<1>(p, st);
+    return a.s.out_bf16 ? launch_backward<2>(p, st) : launch_backward<3>(p, st);
 }
 
 }  // namespace gptq
