@@ -385,10 +385,9 @@ gptq_status check_mx_linear(int64_t m, int64_t d_out, int64_t d_in) {
     if (d_out < 1 || d_out > (int64_t)1 << 19) return fail(GPTQ_EINVAL, "d_out must be in [1, 2^19]");
     return GPTQ_OK;
 }
-int act_kind(const gptq_dtype &t) { return raw(t) == GPTQ_BF16 ? gptq::MX_ACT_BF16 : gptq::MX_ACT_F32; }
 
 // the checks and the launch that the two forward products share, a.A or a.a set
-gptq_status run_mx_linear(gptq::MxLinear &a, int a_kind, const gptq_dtype &bias_dtype, const gptq_activation &act,
+gptq_status run_mx_linear(gptq::MxLinear &a, const gptq_dtype &bias_dtype, const gptq_activation &act,
                           const gptq_dtype &y_dtype, void *workspace, size_t workspace_bytes, void *stream) {
     if (!valid_dtype(y_dtype)) return fail(GPTQ_EINVAL, "y_dtype must be GPTQ_F32 or GPTQ_BF16");
     if (!valid_act(act)) return fail(GPTQ_EINVAL, "unknown activation (got %d)", raw(act));
@@ -401,7 +400,7 @@ gptq_status run_mx_linear(gptq::MxLinear &a, int a_kind, const gptq_dtype &bias_
     a.out_bf16 = raw(y_dtype) == GPTQ_BF16;
     a.bias_bf16 = a.bias && raw(bias_dtype) == GPTQ_BF16;
     a.act = raw(act);
-    s = check_ws(workspace, workspace_bytes, gptq::mx_linear_ws(a.m, a.d_out, a.d_in, a_kind, a.out_bf16));
+    s = check_ws(workspace, workspace_bytes, gptq::mx_linear_ws(a.m, a.d_out, a.d_in, gptq::mx_kind(a), a.out_bf16));
     if (s != GPTQ_OK) return s;
     a.ws = (char *)workspace;
     HIPCHECK(gptq::mx_linear_launch(a, (hipStream_t)stream));
@@ -839,7 +838,8 @@ gptq_status gptq_mx_dequantize(const uint8_t *codes, const uint8_t *scales, gptq
 
 size_t gptq_mx_linear_workspace_size(int64_t m, int64_t d_out, int64_t d_in, gptq_dtype a_dtype, gptq_dtype y_dtype) {
     if (check_mx_linear(m, d_out, d_in) != GPTQ_OK || !valid_dtype(a_dtype) || !valid_dtype(y_dtype)) return 0;
-    return gptq::mx_linear_ws(m, d_out, d_in, act_kind(a_dtype), raw(y_dtype) == GPTQ_BF16);
+    return gptq::mx_linear_ws(m, d_out, d_in, raw(a_dtype) == GPTQ_BF16 ? gptq::MX_ACT_BF16 : gptq::MX_ACT_F32,
+                              raw(y_dtype) == GPTQ_BF16);
 }
 
 gptq_status gptq_mx_linear(const void *A, gptq_dtype a_dtype, int64_t m, int64_t d_in, const uint8_t *codes,
@@ -863,13 +863,15 @@ gptq_status gptq_mx_linear(const void *A, gptq_dtype a_dtype, int64_t m, int64_t
     a.residual = residual;
     a.Y = Y;
     a.pre = preact;
-    return run_mx_linear(a, act_kind(a_dtype), bias_dtype, act, y_dtype, workspace, workspace_bytes, stream);
+    return run_mx_linear(a, bias_dtype, act, y_dtype, workspace, workspace_bytes, stream);
 }
 
 size_t gptq_mx_linear_mx_workspace_size(int64_t m, int64_t d_out, int64_t d_in, gptq_mx_format a_format,
                                         gptq_dtype y_dtype) {
     if (check_mx_linear(m, d_out, d_in) != GPTQ_OK || !valid_format(a_format) || !valid_dtype(y_dtype)) return 0;
-    return gptq::mx_linear_ws(m, d_out, d_in, raw(a_format), raw(y_dtype) == GPTQ_BF16);
+    const int bf16 = raw(y_dtype) == GPTQ_BF16;
+    return gptq::mx_linear_ws(m, d_out, d_in, raw(a_format) == GPTQ_MX_FP8 && !bf16 ? gptq::MX_WIDE_FP8 : raw(a_format),
+                              bf16);
 }
 
 gptq_status gptq_mx_linear_mx(const uint8_t *a_codes, const uint8_t *a_scales, gptq_mx_format a_format, int64_t m,
@@ -893,7 +895,7 @@ gptq_status gptq_mx_linear_mx(const uint8_t *a_codes, const uint8_t *a_scales, g
     a.residual = residual;
     a.Y = Y;
     a.pre = preact;
-    return run_mx_linear(a, raw(a_format), bias_dtype, act, y_dtype, workspace, workspace_bytes, stream);
+    return run_mx_linear(a, bias_dtype, act, y_dtype, workspace, workspace_bytes, stream);
 }
 
 size_t gptq_mx_linear_backward_workspace_size(int64_t m, int64_t d_out, int64_t d_in, gptq_dtype dy_dtype,

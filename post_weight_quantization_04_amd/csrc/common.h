@@ -237,9 +237,14 @@ struct MxLinear {
     int out_bf16;
     char *ws;
 };
-// a_kind: MX_FP8, MX_FP4, or MX_ACT_F32, MX_ACT_BF16
-constexpr int MX_ACT_F32 = 2, MX_ACT_BF16 = 3;
-size_t mx_linear_ws(int64_t m, int64_t d_out, int64_t d_in, int a_kind, int out_bf16);
+// The kinds of activations: MX_FP8, MX_FP4 and these; fp8 ones with an F32 result
+// go to the 16-bit matrix cores (MX_WIDE_FP8)
+constexpr int MX_ACT_F32 = 2, MX_ACT_BF16 = 3, MX_WIDE_FP8 = 4;
+static inline int mx_kind(const MxLinear &a) {
+    if (a.A) return a.a_bf16 ? MX_ACT_BF16 : MX_ACT_F32;
+    return a.a.fmt == MX_FP8 && !a.out_bf16 ? MX_WIDE_FP8 : a.a.fmt;
+}
+size_t mx_linear_ws(int64_t m, int64_t d_out, int64_t d_in, int kind, int out_bf16);
 hipError_t mx_linear_launch(const MxLinear &a, hipStream_t st);
 // shapes with bits 0, ngroups = blocks of a row
 size_t mx_linear_backward_ws(const FusedShape &s);

@@ -179,12 +179,12 @@ __device__ __forceinline__ void mx_bias8(const MxEpilogue &p, int64_t n, float (
 
 // the products' forms
 MxEpilogue mx_epilogue_of(const MxLinear &a);
-bool mx_skinny_takes(int64_t m, int64_t d_out, int64_t d_in, int a_kind);
+bool mx_skinny_takes(int64_t m, int64_t d_out, int64_t d_in, int kind);
 hipError_t mx_skinny_launch(const MxLinear &a, hipStream_t st);
 bool mx_skinny_backward_takes(const FusedShape &s);
 size_t mx_skinny_backward_ws(const FusedShape &s);
 hipError_t mx_skinny_backward_launch(const FusedBackward &a, hipStream_t st);
-size_t mx_gemm_ws(int64_t m, int64_t d_out, int64_t d_in, int a_fmt);
+size_t mx_gemm_ws(int64_t m, int64_t d_out, int64_t d_in);
 hipError_t mx_gemm_launch(const MxLinear &a, hipStream_t st);
 
 }  // namespace gptq

@@ -351,7 +351,7 @@ MxEpilogue mx_epilogue_of(const MxLinear &a) {
     return e;
 }
 
-size_t mx_gemm_ws(int64_t m, int64_t d_out, int64_t d_in, int) {
+size_t mx_gemm_ws(int64_t m, int64_t d_out, int64_t d_in) {
     const Plan p = plan_mx(m, d_out, (int)mx_steps(d_in));
     return p.nsplit > 1 ? align256((size_t)p.nsplit * m * (cdiv(d_out, 8) * 8) * sizeof(float)) : 0;
 }
@@ -382,23 +382,23 @@ hipError_t mx_gemm_launch(const MxLinear &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-size_t mx_linear_ws(int64_t m, int64_t d_out, int64_t d_in, int a_kind, int out_bf16) {
-    if (m == 0 || mx_skinny_takes(m, d_out, d_in, a_kind)) return 0;
-    if (a_kind == MX_FP4 || (a_kind == MX_FP8 && out_bf16)) return mx_gemm_ws(m, d_out, d_in, a_kind);
+size_t mx_linear_ws(int64_t m, int64_t d_out, int64_t d_in, int kind, int out_bf16) {
+    if (m == 0 || mx_skinny_takes(m, d_out, d_in, kind)) return 0;
+    if (kind == MX_FP4 || kind == MX_FP8) return mx_gemm_ws(m, d_out, d_in);
     FusedShape s{};
     s.m = m;
     s.d_out = d_out;
     s.d_in = d_in;
     s.layers = 1;
-    s.in_bf16 = a_kind != MX_ACT_F32;   // (fp8 activations are exact in f16 too)
+    s.in_bf16 = kind != MX_ACT_F32;   // (fp8 activations are exact in f16 too)
     s.out_bf16 = out_bf16;
     return dense_forward_ws(s);
 }
 
 hipError_t mx_linear_launch(const MxLinear &a, hipStream_t st) {
-    const int kind = a.A ? (a.a_bf16 ? MX_ACT_BF16 : MX_ACT_F32) : a.a.fmt;
+    const int kind = mx_kind(a);
     if (mx_skinny_takes(a.m, a.d_out, a.d_in, kind)) return mx_skinny_launch(a, st);
-    if (kind == MX_FP4 || (kind == MX_FP8 && a.out_bf16)) return mx_gemm_launch(a, st);
+    if (kind == MX_FP4 || kind == MX_FP8) return mx_gemm_launch(a, st);
     FusedForward f{};
     f.s.m = a.m;
     f.s.d_out = a.d_out;

@@ -36,19 +36,30 @@ struct SkinnyArgs {
 
 typedef __attribute__((ext_vector_type(8))) int i32x8;
 
-// eight bf16 of activation row `row`, columns k ..; zeros past the end
-__device__ __forceinline__ bf16x8 act_bf16(const SkinnyArgs &p, int64_t row, int64_t k) {
-    const uint16_t *a = (const uint16_t *)p.A + row * p.d_in;
+// eight values of activation row `row`, columns k .., as they lie in memory
+// (BYTES 2 or 4 each); zeros past the end
+template <int BYTES>
+__device__ __forceinline__ void act_raw(const SkinnyArgs &p, int64_t row, int64_t k, u32x4 *out) {
+    const char *a = (const char *)p.A + row * p.d_in * BYTES;
     if (p.vec) {
         const bool in = k < p.d_in;
-        const u32x4 u = *(const u32x4 *)(a + (in ? k : 0));
-        return __builtin_bit_cast(bf16x8, in ? u : u32x4{0u, 0u, 0u, 0u});
-    }
-    u32x4 u = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (k + e < p.d_in) u[e >> 1] |= (unsigned)a[k + e] << (16 * (e & 1));
-    return __builtin_bit_cast(bf16x8, u);
+        for (int i = 0; i < BYTES / 2; ++i) {
+            const u32x4 u = *(const u32x4 *)(a + (in ? k : 0) * BYTES + 16 * i);
+            out[i] = in ? u : u32x4{0u, 0u, 0u, 0u};
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < BYTES / 2; ++i) out[i] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (k + e >= p.d_in) continue;
+            if constexpr (BYTES == 2)
+                out[0][e >> 1] |= (unsigned)((const uint16_t *)a)[k + e] << (16 * (e & 1));
+            else
+                out[e >> 2][e & 3] = ((const unsigned *)a)[k + e];
+        }
+    }
 }
 // fp32 values as N bf16 terms, each the leading bits of what is left (truncated,
 // so that no term overflows; the last of two rounded to nearest); infinities
@@ -93,9 +104,7 @@ __device__ __forceinline__ bf16x8 codes8_bf16(u32x2 w, float scale) {
     return __builtin_bit_cast(bf16x8, u32x4{u[0], u[1], u[2], u[3]});
 }
 
-// KIND: MX_FP8, MX_FP4, MX_ACT_F32, MX_ACT_BF16, or WIDE_FP8 (fp8 as bf16);
-// MT: 16-row tiles of activations
-constexpr int WIDE_FP8 = 4;
+// KIND: of the activations (MX_WIDE_FP8: fp8 as bf16); MT: their 16-row tiles
 template <int KIND, int MT>
 __global__ __launch_bounds__(64 * SK_WAVES) void mx_skinny_kernel(SkinnyArgs p) {
     __shared__ f32x4 lds[SK_WAVES][MT][64];
@@ -113,6 +122,82 @@ __global__ __launch_bounds__(64 * SK_WAVES) void mx_skinny_kernel(SkinnyArgs p) 
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+    // A step's work in units of whole operands: the activations of one are loaded
+    // beside the products of the one before it.
+    constexpr bool MX = KIND == MX_FP8 || KIND == MX_FP4, SCALED = MX || KIND == MX_WIDE_FP8;
+    constexpr int UNITS = MX ? 1 : 2;
+    constexpr int RAW = KIND == MX_ACT_F32 ? 4 : (KIND == MX_ACT_BF16 || KIND == MX_FP8 ? 2 : 1);
+    struct Acts {
+        u32x4 x[MT][RAW];
+        unsigned sc[MT];
+    };
+    auto load = [&](int s, int unit, Acts &a) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            if constexpr (SCALED) {
+                const uint8_t *c = p.a.codes + arow[t] * p.a_bytes;
+                a.sc[t] = ((const unsigned *)p.a.scales)[s * p.m + arow[t]];
+                if constexpr (KIND == MX_FP4) {
+                    a.x[t][0] = *(const u32x4 *)(c + (int64_t)s * (MX_PAD / 2) + 16 * g);
+                } else if constexpr (KIND == MX_FP8) {
+                    // e4m3 operands: a lane holds columns 16 g .. and 64 + 16 g ..
+                    a.x[t][0] = *(const u32x4 *)(c + (int64_t)s * MX_PAD + 16 * g);
+                    a.x[t][RAW - 1] = *(const u32x4 *)(c + (int64_t)s * MX_PAD + 64 + 16 * g);
+                } else {
+                    a.x[t][0] = *(const u32x4 *)(c + (int64_t)s * MX_PAD + MX_BLOCK * g + 16 * unit);
+                }
+            } else {
+                const int64_t k = (int64_t)s * MX_PAD + MX_BLOCK * g + 16 * unit;
+                constexpr int BYTES = KIND == MX_ACT_BF16 ? 2 : 4;
+                act_raw<BYTES>(p, arow[t], k, a.x[t]);
+                act_raw<BYTES>(p, arow[t], k + 8, a.x[t] + RAW / 2);
+            }
+        }
+    };
+    auto products = [&](const u32x4 &w, unsigned sc, int unit, const Acts &a) {
+        if constexpr (MX) {
+            const i32x8 wb = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+            const int ws = (int)(sc >> (8 * g));
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const u32x4 a0 = a.x[t][0], a1 = KIND == MX_FP8 ? a.x[t][RAW - 1] : u32x4{0u, 0u, 0u, 0u};
+                const i32x8 ab = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3],
+                                  (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
+                const int as = (int)(a.sc[t] >> (8 * g));
+                acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wb, ab, acc[t], 4, KIND == MX_FP4 ? 4 : 0, 0,
+                                                                         ws, 0, as);
+            }
+        } else {
+            const float scale = __builtin_bit_cast(float, ((sc >> (8 * g)) & 255u) << 23);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bf16x8 wb = codes_bf16(unit ? w[2 + j] : w[j], scale);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    if constexpr (KIND == MX_WIDE_FP8) {
+                        const float as = __builtin_bit_cast(float, ((a.sc[t] >> (8 * g)) & 255u) << 23);
+                        const u32x2 ac = {a.x[t][0][2 * j], a.x[t][0][2 * j + 1]};
+                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, codes8_bf16(ac, as), acc[t], 0, 0, 0);
+                    } else if constexpr (KIND == MX_ACT_BF16) {
+                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            wb, __builtin_bit_cast(bf16x8, a.x[t][j]), acc[t], 0, 0, 0);
+                    } else {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const unsigned bits = a.x[t][(RAW / 2) * j + (e >> 2)][e & 3];
+                            v[e] = __builtin_bit_cast(float, bits);
+                        }
+                        bf16x8 term[3];
+                        bf16_terms<3>(v, term);
+#pragma unroll
+                        for (int i = 2; i >= 0; --i)
+                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, term[i], acc[t], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    };
     auto steps = [&](int s0, auto count) {
         constexpr int N = decltype(count)::value;
         u32x4 w[N];
@@ -123,57 +208,13 @@ __global__ __launch_bounds__(64 * SK_WAVES) void mx_skinny_kernel(SkinnyArgs p) 
             w[u] = *(const u32x4 *)(wc + (int64_t)s * (MX_PAD / 2));
             sc[u] = wsc[(int64_t)s * p.d_out];
         }
+        Acts a[2];
+        load(s0, 0, a[0]);
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const int s = s0 + u * SK_WAVES;
-            if constexpr (KIND == MX_FP8 || KIND == MX_FP4) {
-                const i32x8 wb = {(int)w[u][0], (int)w[u][1], (int)w[u][2], (int)w[u][3], 0, 0, 0, 0};
-                const int ws = (int)(sc[u] >> (8 * g));
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    const uint8_t *a = p.a.codes + arow[t] * p.a_bytes + 16 * g;
-                    const int as = (int)(((const unsigned *)p.a.scales)[s * p.m + arow[t]] >> (8 * g));
-                    if constexpr (KIND == MX_FP8) {
-                        // e4m3 operands: a lane holds columns 16 g .. and 64 + 16 g ..
-                        const i32x4 a0 = *(const i32x4 *)(a + (int64_t)s * MX_PAD);
-                        const i32x4 a1 = *(const i32x4 *)(a + (int64_t)s * MX_PAD + 64);
-                        const i32x8 ab = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
-                        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wb, ab, acc[t], 4, 0, 0, ws, 0, as);
-                    } else {
-                        const i32x4 a0 = *(const i32x4 *)(a + (int64_t)s * (MX_PAD / 2));
-                        const i32x8 ab = {a0[0], a0[1], a0[2], a0[3], 0, 0, 0, 0};
-                        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wb, ab, acc[t], 4, 4, 0, ws, 0, as);
-                    }
-                }
-            } else {
-                const float scale = __builtin_bit_cast(float, ((sc[u] >> (8 * g)) & 255u) << 23);
-                const int64_t k = (int64_t)s * MX_PAD + MX_BLOCK * g;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bf16x8 wb = codes_bf16(w[u][j], scale);
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        if constexpr (KIND == WIDE_FP8) {
-                            const unsigned as = ((const unsigned *)p.a.scales)[s * p.m + arow[t]];
-                            const u32x2 ac = *(const u32x2 *)(p.a.codes + arow[t] * p.a_bytes + k + 8 * j);
-                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                wb, codes8_bf16(ac, __builtin_bit_cast(float, ((as >> (8 * g)) & 255u) << 23)), acc[t],
-                                0, 0, 0);
-                        } else if constexpr (KIND == MX_ACT_BF16) {
-                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, act_bf16(p, arow[t], k + 8 * j),
-                                                                            acc[t], 0, 0, 0);
-                        } else {
-                            float v[8];
-                            bf16x8 a[3];
-                            mx_ld8(p.A, arow[t], p.d_in, k + 8 * j, 0, p.vec, v);
-                            bf16_terms<3>(v, a);
-#pragma unroll
-                            for (int i = 2; i >= 0; --i)
-                                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, a[i], acc[t], 0, 0, 0);
-                        }
-                    }
-                }
-            }
+        for (int i = 0; i < N * UNITS; ++i) {
+            if (i + 1 < N * UNITS) load(s0 + (i + 1) / UNITS * SK_WAVES, (i + 1) % UNITS, a[(i + 1) & 1]);
+            if (KIND != MX_ACT_F32) __builtin_amdgcn_sched_barrier(0);   // (fp32's terms fill the time themselves)
+            products(w[i / UNITS], sc[i / UNITS], i % UNITS, a[i & 1]);
         }
     };
     int s = wave;
@@ -398,7 +439,23 @@ hipError_t launch_backward(const SkinnyBack &p, hipStream_t st) {
 
 }  // namespace
 
-bool mx_skinny_takes(int64_t m, int64_t, int64_t, int) { return m <= 64; }
+// Few rows: where this form takes less time than the tiled ones.  Its time goes
+// with the row tiles times a work group's steps times the rounds of groups; us a
+// call, few / many: fp8 4096 x 4096, 64 rows (128 of them) 10.8 / 13.9, 4096 x
+// 11008, 32 rows (172) 15.3 / 15.2; fp4 1024 x 8192, 64 rows (256) 12.0 / 13.6, 4096
+// x 11008, 64 rows (344) 15.6 / 14.8.  The dense form of bf16 and fp32
+// activations writes the whole layer first: bf16 4096 x 4096, 64 rows 22 / 29, 11008
+// x 4096 55 / 59, 1024 x 8192 (few work groups) 32 / 28; fp32 4096 x 4096, 32 rows 25 /
+// 34, 4096 x 11008, 32 rows 61 / 61, 64 rows 121 / 64.
+bool mx_skinny_takes(int64_t m, int64_t d_out, int64_t d_in, int kind) {
+    const int64_t cost = cdiv(m, 16) * mx_steps(d_in) * cdiv(cdiv(d_out, 16), 256);
+    switch (kind) {
+        case MX_FP8: return m <= 16 || (m <= 64 && cost <= 160);
+        case MX_FP4: return m <= 16 || (m <= 64 && cost <= 300);
+        case MX_ACT_F32: return m <= 32;
+        default: return m <= 32 || (m <= 64 && d_out >= 2048);
+    }
+}
 
 hipError_t mx_skinny_launch(const MxLinear &a, hipStream_t st) {
     SkinnyArgs p{};
@@ -413,9 +470,13 @@ hipError_t mx_skinny_launch(const MxLinear &a, hipStream_t st) {
     p.a_bytes = a.A ? 0 : mx_row_bytes(a.d_in, a.a.fmt);
     p.vec = a.d_in % 8 == 0 && reinterpret_cast<uintptr_t>(a.A) % 16 == 0;
     p.out = mx_epilogue_of(a);
-    if (!a.A && a.a.fmt == MX_FP8) return a.out_bf16 ? launch<MX_FP8>(p, st) : launch<WIDE_FP8>(p, st);
-    if (!a.A) return launch<MX_FP4>(p, st);
-    return a.a_bf16 ? launch<MX_ACT_BF16>(p, st) : launch<MX_ACT_F32>(p, st);
+    switch (mx_kind(a)) {
+        case MX_FP8: return launch<MX_FP8>(p, st);
+        case MX_FP4: return launch<MX_FP4>(p, st);
+        case MX_WIDE_FP8: return launch<MX_WIDE_FP8>(p, st);
+        case MX_ACT_BF16: return launch<MX_ACT_BF16>(p, st);
+        default: return launch<MX_ACT_F32>(p, st);
+    }
 }
 
 bool mx_skinny_backward_takes(const FusedShape &s) { return s.m <= 32; }

@@ -284,7 +284,7 @@ def test_linear(m, n, k, act, bias, res, save, kind, out):
     y, z = got if save else (got, None)
     assert y.dtype == DT[out]
     z64 = a64 @ w64.t() + (b.double() if bias else 0)
-    e = bounds(kind, out, m, a64, w64, m > 64 and (kind in DT or (kind, out) == ("fp8", "f32"))) + 2.0 ** -24 * z64.abs()
+    e = bounds(kind, out, m, a64, w64, m > 32 and (kind in DT or (kind, out) == ("fp8", "f32"))) + 2.0 ** -24 * z64.abs()
     if save:
         assert ((z.double() - z64).abs() <= e + HALF_STEP[out] * (z64.abs() + e)).all()
     y64 = act64(z64, act) + (r.double() if res else 0)
@@ -303,7 +303,7 @@ def test_fp8_activations_of_wide_range_in_fp32(m):
     w64 = values_of(wq)
     got = P.mx_linear(t, wq, out_dtype=torch.float32)
     want = a64 @ w64.t()
-    assert ((got.double() - want).abs() <= bounds("fp8", "f32", m, a64, w64, m > 64)).all()
+    assert ((got.double() - want).abs() <= bounds("fp8", "f32", m, a64, w64, m > 32)).all()
     assert float((got.double() - want).norm() / want.norm()) < 1e-6
 
 
