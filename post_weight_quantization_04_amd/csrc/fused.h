@@ -63,6 +63,49 @@ __device__ __forceinline__ void fz_st4(void *p, int64_t i, f32x4 v, int bf16) {
         *(f32x4 *)((float *)p + i) = v;
 }
 
+// eight values to an aligned place
+__device__ __forceinline__ void fz_st8(void *x, int64_t o, int bf16, const float (&v)[8]) {
+    if (bf16) {
+        *(u32x4 *)((uint16_t *)x + o) = u32x4{fz_pack_bf16(v[0], v[1]), fz_pack_bf16(v[2], v[3]),
+                                              fz_pack_bf16(v[4], v[5]), fz_pack_bf16(v[6], v[7])};
+    } else {
+        fz_st4(x, o, f32x4{v[0], v[1], v[2], v[3]}, 0);
+        fz_st4(x, o + 4, f32x4{v[4], v[5], v[6], v[7]}, 0);
+    }
+}
+// eight values from column n of a row (offset o) on, `width` at a time, those
+// inside n_all (as n itself is)
+__device__ __forceinline__ void fz_ld_row8(const void *x, int64_t o, int64_t n, int64_t n_all, int bf16, int width,
+                                           float (&v)[8]) {
+    if (width == 8) {
+        fz_ld8(x, o, bf16, v);
+    } else if (width == 4) {
+        const bool more = n + 4 < n_all;
+        const f32x4 a = fz_ld4(x, o, bf16), b = fz_ld4(x, more ? o + 4 : o, bf16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = a[e];
+            v[4 + e] = b[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fz_ld(x, n + e < n_all ? o + e : o, bf16);
+    }
+}
+__device__ __forceinline__ void fz_st_row8(void *x, int64_t o, int64_t n, int64_t n_all, int bf16, int width,
+                                           const float (&v)[8]) {
+    if (width == 8) {
+        fz_st8(x, o, bf16, v);
+    } else if (width == 4) {
+        fz_st4(x, o, f32x4{v[0], v[1], v[2], v[3]}, bf16);
+        if (n + 4 < n_all) fz_st4(x, o + 4, f32x4{v[4], v[5], v[6], v[7]}, bf16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (n + e < n_all) fz_st(x, o + e, v[e], bf16);
+    }
+}
+
 // The factor 2^t that brings v, positive and finite, to [2^14, 2^15) (f16's
 // range), and the exponent -t that undoes it; 1 and 0 for 0.  A sum of scaled
 // products returns by ldexpf with both operands' exponents added: the sums are

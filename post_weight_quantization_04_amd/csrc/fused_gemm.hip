@@ -754,6 +754,7 @@ struct Gemm {
     void *Y;
     void *pre[2];
     int out_bf16, vec;          // vec: four consecutive outputs load and store together (n % 4 == 0)
+    int width;                  // how many do: 8, 4 or 1
     float *part;                // [nsplit][layers][m][np] when nsplit > 1
     int64_t np;                 // n padded to whole quads
     int nsplit;
@@ -810,6 +811,62 @@ __device__ __forceinline__ void epilogue(const Gemm &p, const Columns<GATED, W> 
     store(p.Y, y);
 }
 
+// The same for eight consecutive columns, and R rows (those below m) together:
+// loads first, so that they overlap
+template <bool GATED>
+struct Columns8 {
+    int ew[GATED ? 2 : 1][8];
+    float bias[GATED ? 2 : 1][8];
+    __device__ __forceinline__ Columns8(const Gemm &p, int64_t n) {
+#pragma unroll
+        for (int l = 0; l < (GATED ? 2 : 1); ++l) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ew[l][e] = n + e < p.n ? p.ew[l * p.n + n + e] : 0;
+                bias[l][e] = 0.f;
+            }
+            if (p.bias[l] && n < p.n) fz_ld_row8(p.bias[l], n, n, p.n, p.bias_bf16, p.width, bias[l]);
+        }
+    }
+};
+template <bool GATED, int R>
+__device__ __forceinline__ void epilogue8(const Gemm &p, const Columns8<GATED> &col, const int64_t (&row)[R],
+                                          const int (&ea)[R], int64_t n, float (&z)[GATED ? 2 : 1][R][8]) {
+    float res[R][8];
+    if (p.residual) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            fz_ld_row8(p.residual, std::min(row[r], p.m - 1) * p.n + n, n, p.n, p.out_bf16, p.width, res[r]);
+    }
+#pragma unroll
+    for (int l = 0; l < (GATED ? 2 : 1); ++l) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[l][r][e] = fz_ldexp(z[l][r][e], ea[r] + col.ew[l][e]) + col.bias[l][e];
+        if (p.pre[l]) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (row[r] < p.m) fz_st_row8(p.pre[l], row[r] * p.n + n, n, p.n, p.out_bf16, p.width, z[l][r]);
+        }
+    }
+    fz_with_act(p.act, [&](auto act) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[0][r][e] = fz_act<decltype(act)::value>(z[0][r][e]);
+    });
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (GATED) z[0][r][e] *= z[1][r][e];
+            if (p.residual) z[0][r][e] += res[r][e];
+        }
+        if (row[r] < p.m) fz_st_row8(p.Y, row[r] * p.n + n, n, p.n, p.out_bf16, p.width, z[0][r]);
+    }
+}
+
 // C tile of 64 NJ columns n by 64 MI rows, four waves of 32 NJ by 32 MI as
 // 32 x 32 MFMA tiles.  The weights are the MFMA's first operand, so that a lane holds
 // four consecutive columns of one activation row.  Both operands move by
@@ -822,18 +879,15 @@ __device__ __forceinline__ void epilogue(const Gemm &p, const Columns<GATED, W> 
 // between the reads of the next half's operands and half of a refill; the
 // wait for a stage counts loads, so two later stages stay in flight across
 // the one barrier per stage.
-//
-// The sums leave through LDS, 64 rows at a time in two buffers, so that the
-// epilogue reads and writes whole row segments.
 template <int MI, int NJ, bool GATED>
-__global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
+__global__ __launch_bounds__(256, MI * NJ == 16 ? 1 : 2) void fused_gemm_kernel(Gemm p) {
     constexpr int BM = 64 * MI, BN = 64 * NJ, NBUF = 4;
     constexpr int NSIDE = BN * GK * 2, STAGE = NSIDE + BM * GK * 2;   // bytes
     constexpr int NDMA = NJ, MDMA = MI;                               // loads per wave and stage
     constexpr int PER_STAGE = NDMA + MDMA;
     constexpr int COLS = GATED ? BN / 2 : BN;                         // columns n of one layer
-    constexpr int EROW = BN + 4;                                      // floats of an epilogue row (padded)
-    __shared__ __attribute__((aligned(16))) char lds[std::max(NBUF * STAGE, (2 * 64 * EROW + BM) * 4)];
+    constexpr int EROW = 32 * NJ + 4;                                 // floats of an epilogue row (padded)
+    __shared__ __attribute__((aligned(16))) char lds[std::max(NBUF * STAGE, (4 * 64 * EROW + BM) * 4)];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave >> 1, wm = wave & 1;
@@ -974,58 +1028,72 @@ __global__ __launch_bounds__(256) void fused_gemm_kernel(Gemm p) {
     gm_wait<0>();   // the loads past the end must land before the ring is reused
     gm_barrier();
 
-    // lane (h, li), register 4 q + e of tile (j, i) <-> column 8 q + 4 h + e, row li
-    const int tid = threadIdx.x;
-    int *eas = (int *)lds + 2 * 64 * EROW;
-    auto leave = [&](auto width, const float *out, int i) {
-        constexpr int W = decltype(width)::value, TPR = COLS / W;   // threads per row of outputs
-        const int c = W * (tid % TPR);
-        const int64_t n = n0 + c;
-        if (n >= p.n) return;
-        const int64_t first = m0 + 32 * i;
-        if (p.nsplit > 1) {
-            for (int rr = tid / TPR; rr < 64; rr += 256 / TPR) {
-                const int64_t row = first + (rr >> 5) * 32 * MI + (rr & 31);
-                if (row >= p.m) continue;
-                float *part = p.part + (((int64_t)split * p.layers * p.m) + row) * p.np + n;
-                *(f32x4 *)part = *(const f32x4 *)(out + rr * EROW + c);   // (W is 4: see below)
-                if (GATED) *(f32x4 *)(part + p.m * p.np) = *(const f32x4 *)(out + rr * EROW + BN / 2 + c);
-            }
-            return;
-        }
-        const Columns<GATED, W> col(p, n);
-#pragma unroll 4
-        for (int rr = tid / TPR; rr < 64; rr += 256 / TPR) {
-            const int64_t row = first + (rr >> 5) * 32 * MI + (rr & 31);
-            if (row < p.m) {
-                f32x4 z = {0.f, 0.f, 0.f, 0.f}, u = z;
-#pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    z[e] = out[rr * EROW + c + e];
-                    if (GATED) u[e] = out[rr * EROW + BN / 2 + c + e];
-                }
-                epilogue<GATED, W>(p, col, row, n, eas[row - m0], z, u);
-            }
-        }
-    };
-    // the tile's row exponents (visible behind the first barrier below)
+    // lane (h, li), register 4 q + e of tile (j, i) <-> column 8 q + 4 h + e, row li.
+    // Each wave turns 64 rows at a time around through its own part of LDS, so
+    // that it reads and writes whole row segments, eight columns a lane, R rows
+    // in flight together (through buffers of the work group, one row at a time,
+    // the sums of a 256 x 256 tile took as long as the products of K = 1200).
+    constexpr int WCOLS = GATED ? 16 * NJ : 32 * NJ;   // columns n of a wave
+    constexpr int LPR = WCOLS / 8, RPP = 64 / LPR, R = GATED ? 2 : 4;
+    const int tid = threadIdx.x, lc = 8 * (lane % LPR), lr = lane / LPR;
+    const int64_t n = n0 + wn * WCOLS + lc;
+    float *out = (float *)lds + wave * 64 * EROW;
+    int *eas = (int *)lds + 4 * 64 * EROW;
     for (int r = tid; r < BM; r += 256) eas[r] = m0 + r < p.m ? p.ea[m0 + r] : 0;
+    gm_barrier();   // (the tile's row exponents are there)
+    const Columns8<GATED> col(p, n);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        float *out = (float *)lds + (i & 1) * 64 * EROW;
+    for (int i0 = 0; i0 < MI; i0 += 2) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int col = brow[j] - li + 8 * q + 4 * h;
-                *(f32x4 *)(out + (wm * 32 + li) * EROW + col) =
-                    f32x4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *(f32x4 *)(out + (32 * i + li) * EROW + 32 * j + 8 * q + 4 * h) =
+                        f32x4{acc[j][i0 + i][4 * q], acc[j][i0 + i][4 * q + 1], acc[j][i0 + i][4 * q + 2],
+                              acc[j][i0 + i][4 * q + 3]};
+        // (other lanes of the wave read what this one wrote)
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (n < p.n)
+#pragma unroll 1
+            for (int c0 = 0; c0 < 64 / RPP; c0 += R) {
+                int64_t row[R];
+                int ea[R];
+                float z[GATED ? 2 : 1][R][8];
+#pragma unroll
+                for (int c = 0; c < R; ++c) {
+                    const int at = (c0 + c) * RPP + lr, r = wm * 32 * MI + 32 * i0 + at;
+                    row[c] = m0 + r;
+                    ea[c] = eas[r];
+#pragma unroll
+                    for (int l = 0; l < (GATED ? 2 : 1); ++l) {
+                        const float *in = out + at * EROW + l * WCOLS + lc;
+                        const f32x4 z0 = *(const f32x4 *)in, z1 = *(const f32x4 *)(in + 4);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            z[l][c][e] = z0[e];
+                            z[l][c][4 + e] = z1[e];
+                        }
+                    }
+                }
+                if (p.nsplit > 1) {
+#pragma unroll
+                    for (int c = 0; c < R; ++c) {
+                        if (row[c] >= p.m) continue;
+                        float *part = p.part + (((int64_t)split * p.layers * p.m) + row[c]) * p.np + n;
+#pragma unroll
+                        for (int l = 0; l < (GATED ? 2 : 1); ++l) {
+                            const float (&v)[8] = z[l][c];
+                            *(f32x4 *)(part + l * p.m * p.np) = f32x4{v[0], v[1], v[2], v[3]};
+                            if (n + 4 < p.np) *(f32x4 *)(part + l * p.m * p.np + 4) = f32x4{v[4], v[5], v[6], v[7]};
+                        }
+                    }
+                } else {
+                    epilogue8<GATED, R>(p, col, row, ea, n, z);
+                }
             }
-        gm_barrier();   // (the buffer two passes back was read before the previous barrier)
-        if (p.vec || p.nsplit > 1)
-            leave(std::integral_constant<int, 4>{}, out, i);
-        else
-            leave(std::integral_constant<int, 1>{}, out, i);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (read before the next rows overwrite them)
     }
 }
 
@@ -1155,7 +1223,8 @@ BackwardWs backward_layout(const FusedShape &s, char *base) {
 }
 
 template <int MI, int NJ, bool GATED>
-hipError_t launch_gemm_k(const Gemm &g, hipStream_t st) {
+hipError_t launch_gemm_k(Gemm g, hipStream_t st) {
+    g.width = !g.vec ? 1 : (g.n % 8 ? 4 : 8);
     fused_gemm_kernel<MI, NJ, GATED><<<(unsigned)(g.mt * g.nt * g.nsplit), 256, 0, st>>>(g);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || g.nsplit == 1) return e;

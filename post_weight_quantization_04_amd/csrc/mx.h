@@ -70,16 +70,6 @@ __device__ __forceinline__ void mx_put8(const float (&v)[8], int64_t rows, int64
     if ((piece & 3) == 0) scales[((piece >> 4) * rows + row) * 4 + ((piece >> 2) & 3)] = (uint8_t)byte;
 }
 
-// eight values to an aligned place
-__device__ __forceinline__ void mx_st8(void *x, int64_t o, int bf16, const float (&v)[8]) {
-    if (bf16) {
-        *(u32x4 *)((uint16_t *)x + o) = u32x4{fz_pack_bf16(v[0], v[1]), fz_pack_bf16(v[2], v[3]),
-                                              fz_pack_bf16(v[4], v[5]), fz_pack_bf16(v[6], v[7])};
-    } else {
-        fz_st4(x, o, f32x4{v[0], v[1], v[2], v[3]}, 0);
-        fz_st4(x, o + 4, f32x4{v[4], v[5], v[6], v[7]}, 0);
-    }
-}
 // eight values of a row from column k on, zeros past its end
 __device__ __forceinline__ void mx_ld8(const void *x, int64_t row, int64_t d, int64_t k, int bf16, int vec,
                                        float (&v)[8]) {
@@ -103,38 +93,6 @@ struct MxEpilogue {
     int out_bf16;
     int width;                  // consecutive outputs that load and store together: 8, 4 or 1
 };
-// eight values from column n of a row (offset o) on, `width` at a time, those
-// inside n_all (as n itself is)
-__device__ __forceinline__ void mx_ld_row8(const void *x, int64_t o, int64_t n, int64_t n_all, int bf16, int width,
-                                           float (&v)[8]) {
-    if (width == 8) {
-        fz_ld8(x, o, bf16, v);
-    } else if (width == 4) {
-        const bool more = n + 4 < n_all;
-        const f32x4 a = fz_ld4(x, o, bf16), b = fz_ld4(x, more ? o + 4 : o, bf16);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = a[e];
-            v[4 + e] = b[e];
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fz_ld(x, n + e < n_all ? o + e : o, bf16);
-    }
-}
-__device__ __forceinline__ void mx_st_row8(void *x, int64_t o, int64_t n, int64_t n_all, int bf16, int width,
-                                           const float (&v)[8]) {
-    if (width == 8) {
-        mx_st8(x, o, bf16, v);
-    } else if (width == 4) {
-        fz_st4(x, o, f32x4{v[0], v[1], v[2], v[3]}, bf16);
-        if (n + 4 < n_all) fz_st4(x, o + 4, f32x4{v[4], v[5], v[6], v[7]}, bf16);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (n + e < n_all) fz_st(x, o + e, v[e], bf16);
-    }
-}
 // R rows (those below m) of eight outputs from column n, inside the row, on:
 // their sums z become the outputs.  Loads first, so that they overlap.
 template <int R>
@@ -144,7 +102,7 @@ __device__ __forceinline__ void mx_epilogue(const MxEpilogue &p, int64_t m, cons
     if (p.residual) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            mx_ld_row8(p.residual, std::min(row[r], m - 1) * p.n + n, n, p.n, p.out_bf16, p.width, res[r]);
+            fz_ld_row8(p.residual, std::min(row[r], m - 1) * p.n + n, n, p.n, p.out_bf16, p.width, res[r]);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -153,7 +111,7 @@ __device__ __forceinline__ void mx_epilogue(const MxEpilogue &p, int64_t m, cons
     if (p.pre) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            if (row[r] < m) mx_st_row8(p.pre, row[r] * p.n + n, n, p.n, p.out_bf16, p.width, z[r]);
+            if (row[r] < m) fz_st_row8(p.pre, row[r] * p.n + n, n, p.n, p.out_bf16, p.width, z[r]);
     }
     fz_with_act(p.act, [&](auto act) {
 #pragma unroll
@@ -169,12 +127,12 @@ __device__ __forceinline__ void mx_epilogue(const MxEpilogue &p, int64_t m, cons
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
-        if (row[r] < m) mx_st_row8(p.Y, row[r] * p.n + n, n, p.n, p.out_bf16, p.width, z[r]);
+        if (row[r] < m) fz_st_row8(p.Y, row[r] * p.n + n, n, p.n, p.out_bf16, p.width, z[r]);
 }
 __device__ __forceinline__ void mx_bias8(const MxEpilogue &p, int64_t n, float (&b)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) b[e] = 0.f;
-    if (p.bias) mx_ld_row8(p.bias, n, n, p.n, p.bias_bf16, p.width, b);
+    if (p.bias) fz_ld_row8(p.bias, n, n, p.n, p.bias_bf16, p.width, b);
 }
 
 // the products' forms

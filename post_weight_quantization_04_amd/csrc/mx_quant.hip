@@ -102,7 +102,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantMx p) {
             }
             const int64_t o = row * p.d + k;
             if (p.vec) {
-                mx_st8(p.Y, o, p.bf16, v);
+                fz_st8(p.Y, o, p.bf16, v);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)

@@ -63,7 +63,7 @@ __device__ __forceinline__ void put8(void *x, int64_t row, int64_t d, int64_t k,
                                      const float (&v)[8]) {
     const int64_t o = row * d + k;
     if (vec && k < d) {
-        mx_st8(x, o, bf16, v);
+        fz_st8(x, o, bf16, v);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
