@@ -444,25 +444,29 @@ def _operand(t, name, dtype, shape, device) -> int:
     raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
-class _DeviceCall:
-    """Checks and buffers of one call: operands on one device, a workspace and
-    outputs that belong to the stream the work goes to."""
-    __slots__ = ("device", "act", "out_dtype", "out_code", "stream", "given_ws", "guard")
+class _FusedCall:
+    """Checks and buffers of one fused call: operands on one device, a
+    workspace and outputs that belong to the stream the work goes to."""
+    __slots__ = ("device", "in_code", "act", "out_dtype", "out_code", "d_in", "d_out", "words", "groups", "perm",
+                 "bits", "group", "stream", "given_ws", "guard")
 
-    def epilogue(self, activation, out_dtype):
+    def __init__(self, x, name, q, activation, out_dtype, workspace, stream):
         torch = _torch()
+        _require(x, name, ndim=2)
+        self.in_code = _dtype_code(x)
+        device = self.device = x.device
         if activation not in ACTIVATIONS:
             raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}; got {activation!r}")
         self.act = ACTIVATIONS[activation]
-        self.out_dtype = out_dtype
+        self.out_dtype = out_dtype or x.dtype
         if self.out_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"unsupported out_dtype {self.out_dtype}; use float32 or bfloat16")
         self.out_code = F32 if self.out_dtype == torch.float32 else BF16
-
-    def place(self, device, name, workspace, stream):
-        """The device and stream of the call (name: the operand whose device it is)."""
-        torch = _torch()
-        self.device = device
+        self.d_in, self.d_out, self.bits, self.group = q.d_in, q.scales.shape[1], q.bits, q.group_size
+        one = self.group == -1 or self.group >= self.d_in
+        self.words = -(-self.bits * self.d_in // 32)
+        self.groups = 1 if one or self.group < 1 else -(-self.d_in // self.group)
+        self.perm = _operand(q.perm, "perm", torch.int32, (self.d_in,), device) if q.act_order else None
         self.guard = None
         if stream is not None:
             if stream.device != device:
@@ -477,71 +481,6 @@ class _DeviceCall:
         self.given_ws = workspace
         if workspace is not None:
             _operand(workspace, "workspace", workspace.dtype, workspace.shape, device)
-
-    def take(self, t, name, dtype, shape):
-        """An optional operand's pointer."""
-        if t is None:
-            return None
-        p = _operand(t, name, dtype, shape, self.device)
-        self.no_grad(t)
-        return p
-
-    @staticmethod
-    def no_grad(*tensors):
-        """Raises for operands whose gradients, or forward-mode tangents, would be dropped."""
-        if _TORCH.is_grad_enabled():
-            for t in tensors:
-                if t.requires_grad:
-                    raise ValueError("autograd does not see through the fused products: call them under "
-                                     "torch.no_grad() (or inside a torch.autograd.Function) and their _backward "
-                                     "calls for the gradients")
-        if _FORWARD_AD._current_level >= 0:
-            for t in tensors:
-                if _FORWARD_AD.unpack_dual(t).tangent is not None:
-                    raise ValueError("forward-mode tangents do not pass through the fused products: give them the "
-                                     "primals of dual tensors")
-
-    def empty(self, shape, dtype=None):
-        # (the strides given: a third less time than torch.empty takes)
-        n = len(shape)
-        strides = (shape[1], 1) if n == 2 else (1,) if n == 1 else (shape[1] * shape[2], shape[2], 1)
-        return _TORCH.empty_strided(shape, strides, dtype=dtype or self.out_dtype, device=self.device)
-
-    def workspace(self, need):
-        """(owner, pointer, bytes): the caller's when it suffices, otherwise allocated."""
-        w = self.given_ws
-        if w is not None and w.numel() * w.element_size() >= need:
-            return w, w.data_ptr(), w.numel() * w.element_size()
-        if need == 0:
-            return None, None, 0
-        w = self.empty((need,), dtype=_torch().uint8)
-        return w, w.data_ptr(), need
-
-    def __enter__(self):
-        # allocations belong to the stream that uses them, on its own device
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-class _FusedCall(_DeviceCall):
-    """A call of the fused products on packed layers."""
-    __slots__ = ("in_code", "d_in", "d_out", "words", "groups", "perm", "bits", "group")
-
-    def __init__(self, x, name, q, activation, out_dtype, workspace, stream):
-        torch = _torch()
-        _require(x, name, ndim=2)
-        self.in_code = _dtype_code(x)
-        self.epilogue(activation, out_dtype or x.dtype)
-        self.d_in, self.d_out, self.bits, self.group = q.d_in, q.scales.shape[1], q.bits, q.group_size
-        one = self.group == -1 or self.group >= self.d_in
-        self.words = -(-self.bits * self.d_in // 32)
-        self.groups = 1 if one or self.group < 1 else -(-self.d_in // self.group)
-        self.perm = _operand(q.perm, "perm", torch.int32, (self.d_in,), x.device) if q.act_order else None
-        self.place(x.device, name, workspace, stream)
         self.no_grad(x, q.scales, q.zeros)
 
     def layer(self, q):
@@ -569,6 +508,51 @@ class _FusedCall(_DeviceCall):
                 raise ValueError("during a graph's capture the layers must share one perm tensor (two cannot be "
                                  "compared)")
             return torch.equal(a, b)
+
+    def take(self, t, name, dtype, shape):
+        """An optional operand's pointer."""
+        if t is None:
+            return None
+        p = _operand(t, name, dtype, shape, self.device)
+        self.no_grad(t)
+        return p
+
+    @staticmethod
+    def no_grad(*tensors):
+        """Raises for operands whose gradients, or forward-mode tangents, would be dropped."""
+        if _TORCH.is_grad_enabled():
+            for t in tensors:
+                if t.requires_grad:
+                    raise ValueError("autograd does not see through the fused products: call them under "
+                                     "torch.no_grad() (or inside a torch.autograd.Function) and their _backward "
+                                     "calls for the gradients")
+        if _FORWARD_AD._current_level >= 0:
+            for t in tensors:
+                if _FORWARD_AD.unpack_dual(t).tangent is not None:
+                    raise ValueError("forward-mode tangents do not pass through the fused products: give them the "
+                                     "primals of dual tensors")
+
+    def empty(self, shape, dtype=None):
+        return _torch().empty(shape, dtype=dtype or self.out_dtype, device=self.device)
+
+    def workspace(self, need):
+        """(owner, pointer, bytes): the caller's when it suffices, otherwise allocated."""
+        w = self.given_ws
+        if w is not None and w.numel() * w.element_size() >= need:
+            return w, w.data_ptr(), w.numel() * w.element_size()
+        if need == 0:
+            return None, None, 0
+        w = self.empty((need,), dtype=_torch().uint8)
+        return w, w.data_ptr(), need
+
+    def __enter__(self):
+        # allocations belong to the stream that uses them, on its own device
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def dequant_linear(A, q: "QuantizedLayer", bias=None, activation="none", residual=None, out_dtype=None,
@@ -702,53 +686,76 @@ def dequant_gated_backward(dH, gate: "QuantizedLayer", up: "QuantizedLayer", gat
 # ---------------------------------------------------------------------------
 # microscaled (MX) formats, products with MX weights, and the norm before them
 # ---------------------------------------------------------------------------
-@dataclass
 class MxTensor:
     """A matrix [rows, d] in blocks of 32 columns that share a power of two
     (gptq.h has the layout): codes uint8 [rows, row bytes], scales uint8
     [ceil(d / 128), rows, 4], format "fp8" (e4m3) or "fp4" (e2m1)."""
-    codes: "object"
-    scales: "object"
-    format: str
-    d: int
+    __slots__ = ("_codes", "_scales", "_buffer", "rows", "format", "d")
+
+    def __init__(self, codes, scales, format, d):
+        self._codes, self._scales, self._buffer = codes, scales, None
+        self.rows, self.format, self.d = codes.shape[0], format, d
+
+    @classmethod
+    def _empty(cls, rows, d, format, device):
+        """One allocation, codes before scales; its two views are made when asked for."""
+        t = cls.__new__(cls)
+        t._codes = t._scales = None
+        t.rows, t.format, t.d = rows, format, d
+        steps = -(-d // 128)
+        t._buffer = _TORCH.empty_strided((rows * steps * (68 if format == "fp4" else 132),), (1,),
+                                         dtype=_TORCH.uint8, device=device)
+        return t
+
+    def _split(self):
+        row = _mx_row_bytes(self.d, self.format)
+        n = self.rows * row
+        self._codes = self._buffer[:n].view(self.rows, row)
+        self._scales = self._buffer[n:].view(-(-self.d // 128), self.rows, 4)
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._split()
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._split()
+        return self._scales
 
     @property
     def shape(self):
-        return (self.codes.shape[0], self.d)
+        return (self.rows, self.d)
+
+    @property
+    def device(self):
+        return (self._codes if self._buffer is None else self._buffer).device
+
+    def _pointers(self, name, device):
+        """The device pointers of codes and scales; raises if they do not fit the matrix."""
+        b = self._buffer
+        if b is not None and b.device == device:
+            p = b.data_ptr()
+            return p, p + self.rows * _mx_row_bytes(self.d, self.format)
+        c, s, u8 = self.codes, self.scales, _TORCH.uint8
+        codes = (self.rows, _mx_row_bytes(self.d, self.format))
+        scales = (-(-self.d // 128), self.rows, 4)
+        if (c.dtype is u8 and s.dtype is u8 and c.shape == codes and s.shape == scales and c.device == device
+                and s.device == device and c.is_contiguous() and s.is_contiguous()):
+            return c.data_ptr(), s.data_ptr()
+        return _operand(c, f"{name}.codes", u8, codes, device), _operand(s, f"{name}.scales", u8, scales, device)
 
 
-def _mx_shapes(rows, d, format):
-    """The shapes of an MX matrix's codes and scales."""
-    steps = -(-d // 128)
-    return (rows, steps * (64 if format == "fp4" else 128)), (steps, rows, 4)
+def _mx_row_bytes(d, format):
+    return -(-d // 128) * (64 if format == "fp4" else 128)
 
 
 def _mx_format(format) -> int:
     if format not in MX_FORMATS:
         raise ValueError(f"format must be one of {', '.join(MX_FORMATS)}; got {format!r}")
     return MX_FORMATS[format]
-
-
-class _MxCall(_DeviceCall):
-    """A call of the MX operators and the norm."""
-    __slots__ = ()
-
-    def __init__(self, device, name, workspace=None, stream=None):
-        self.place(device, name, workspace, stream)
-
-    def matrix(self, t, name):
-        """An MX matrix's pointers."""
-        c, s, device, u8 = t.codes, t.scales, self.device, _TORCH.uint8
-        codes, scales = _mx_shapes(c.shape[0], t.d, t.format)
-        if (c.dtype is u8 and s.dtype is u8 and c.shape == codes and s.shape == scales and c.device == device
-                and s.device == device and c.is_contiguous() and s.is_contiguous()):
-            return c.data_ptr(), s.data_ptr()
-        return (_operand(c, f"{name}.codes", u8, codes, device), _operand(s, f"{name}.scales", u8, scales, device))
-
-    def new_matrix(self, rows, d, format):
-        u8 = _torch().uint8
-        codes, scales = _mx_shapes(rows, d, format)
-        return MxTensor(self.empty(codes, u8), self.empty(scales, u8), format, d)
 
 
 def _mx_tensor(t, name, format=None):
@@ -758,7 +765,74 @@ def _mx_tensor(t, name, format=None):
         _mx_format(t.format)
     if format is not None and t.format != format:
         raise ValueError(f"{name} must be in {format}, got {t.format}")
-    _require(t.codes, f"{name}.codes", ndim=2)
+    if t._buffer is None:
+        _require(t._codes, f"{name}.codes", ndim=2)
+
+
+class _Here:
+    """No change of device or stream."""
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+
+
+def _place(device, name, stream):
+    """(stream handle, context that allocations belong into) of a call whose operand `name` is on `device`."""
+    if stream is None:
+        # (the current stream's handle without a Stream object around it)
+        i = device.index
+        here = i == _TORCH._C._cuda_getDevice()
+        return _TORCH._C._cuda_getCurrentRawStream(i), _HERE if here else _TORCH.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, {name} to {device}")
+    return stream.cuda_stream, _TORCH.cuda.stream(stream)
+
+
+def _no_grad(*tensors):
+    """Raises for operands whose gradients, or forward-mode tangents, would be dropped (None: no operand)."""
+    if _TORCH.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                _FusedCall.no_grad(t)
+    if _FORWARD_AD._current_level >= 0:
+        _FusedCall.no_grad(*[t for t in tensors if t is not None])
+
+
+def _empty2(rows, cols, dtype, device):
+    # (the strides given: a third less time than torch.empty takes)
+    return _TORCH.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
+def _scratch(workspace, need, device):
+    """(owner, pointer, bytes) of a workspace: the caller's when it suffices, otherwise allocated."""
+    if workspace is not None:
+        _operand(workspace, "workspace", workspace.dtype, workspace.shape, device)
+        n = workspace.numel() * workspace.element_size()
+        if n >= need:
+            return workspace, workspace.data_ptr(), n
+    if need == 0:
+        return None, None, 0
+    w = _TORCH.empty_strided((need,), (1,), dtype=_TORCH.uint8, device=device)
+    return w, w.data_ptr(), need
+
+
+def _out_code(dtype, name="out_dtype") -> int:
+    if dtype is _TORCH.bfloat16:
+        return BF16
+    if dtype is _TORCH.float32:
+        return F32
+    raise TypeError(f"unsupported {name} {dtype}; use float32 or bfloat16")
+
+
+def _activation(activation) -> int:
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}; got {activation!r}")
+    return ACTIVATIONS[activation]
 
 
 def mx_quantize(X, format="fp4", stream=None) -> MxTensor:
@@ -766,13 +840,14 @@ def mx_quantize(X, format="fp4", stream=None) -> MxTensor:
     for weights, "fp8" or "fp4" for activations."""
     _require(X, "X", ndim=2)
     code, fmt = _dtype_code(X), _mx_format(format)
-    f = _MxCall(X.device, "X", stream=stream)
-    f.no_grad(X)
+    _no_grad(X)
+    device = X.device
+    st, where = _place(device, "X", stream)
     rows, d = X.shape
-    with f:
-        t = f.new_matrix(rows, d, format)
-        _check(_lib().gptq_mx_quantize(X.data_ptr(), code, rows, d, fmt, t.codes.data_ptr(), t.scales.data_ptr(),
-                                       f.stream))
+    with where:
+        t = MxTensor._empty(rows, d, format, device)
+        codes, scales = t._pointers("t", device)
+        _check(_lib().gptq_mx_quantize(X.data_ptr(), code, rows, d, fmt, codes, scales, st))
     return t
 
 
@@ -781,27 +856,25 @@ def mx_dequantize(t: MxTensor, dtype=None, stream=None):
     torch = _torch()
     _mx_tensor(t, "t")
     dtype = dtype or torch.float32
-    if dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
-    f = _MxCall(t.codes.device, "t", stream=stream)
-    codes, scales = f.matrix(t, "t")
-    rows = t.codes.shape[0]
-    with f:
-        Y = f.empty((rows, t.d), dtype)
-        _check(_lib().gptq_mx_dequantize(codes, scales, MX_FORMATS[t.format], rows, t.d, Y.data_ptr(),
-                                         F32 if dtype == torch.float32 else BF16, f.stream))
+    code = _out_code(dtype, "dtype")
+    device = t.device
+    st, where = _place(device, "t", stream)
+    codes, scales = t._pointers("t", device)
+    with where:
+        Y = _empty2(t.rows, t.d, dtype, device)
+        _check(_lib().gptq_mx_dequantize(codes, scales, MX_FORMATS[t.format], t.rows, t.d, Y.data_ptr(), code, st))
     return Y
 
 
 def mx_linear_workspace_size(m, d_out, d_in, a_kind, y_dtype_code) -> int:
     """a_kind: the activations' dtype code (F32, BF16) or MX format ("fp8", "fp4")."""
     if isinstance(a_kind, str):
-        return int(_lib().gptq_mx_linear_mx_workspace_size(m, d_out, d_in, _mx_format(a_kind), y_dtype_code))
-    return int(_lib().gptq_mx_linear_workspace_size(m, d_out, d_in, a_kind, y_dtype_code))
+        return _lib().gptq_mx_linear_mx_workspace_size(m, d_out, d_in, _mx_format(a_kind), y_dtype_code)
+    return _lib().gptq_mx_linear_workspace_size(m, d_out, d_in, a_kind, y_dtype_code)
 
 
 def mx_linear_backward_workspace_size(m, d_out, d_in, dy_dtype_code, da_dtype_code) -> int:
-    return int(_lib().gptq_mx_linear_backward_workspace_size(m, d_out, d_in, dy_dtype_code, da_dtype_code))
+    return _lib().gptq_mx_linear_backward_workspace_size(m, d_out, d_in, dy_dtype_code, da_dtype_code)
 
 
 def mx_linear(A, w: MxTensor, bias=None, activation="none", residual=None, out_dtype=None, save_preact=False,
@@ -819,32 +892,34 @@ def mx_linear(A, w: MxTensor, bias=None, activation="none", residual=None, out_d
     mx = isinstance(A, MxTensor)
     if mx:
         _mx_tensor(A, "A")
+        kind, dtype = A.format, out_dtype or torch.bfloat16
     else:
         _require(A, "A", ndim=2)
-    (m, d_in), d_out = A.shape, w.codes.shape[0]
-    f = _MxCall(A.codes.device if mx else A.device, "A", workspace, stream)
-    f.epilogue(activation, out_dtype or (torch.bfloat16 if mx else A.dtype))
+        kind, dtype = _dtype_code(A), out_dtype or A.dtype
+    act, code, device = _activation(activation), _out_code(dtype), A.device
+    st, where = _place(device, "A", stream)
+    (m, d_in), d_out = A.shape, w.rows
     if d_in != w.d:
         raise ValueError(f"A has {d_in} columns, the layer {w.d}")
-    if mx:
-        a, kind = f.matrix(A, "A"), A.format
-    else:
-        kind = _dtype_code(A)
-        f.no_grad(A)
-    codes, scales = f.matrix(w, "w")
-    b = f.take(bias, "bias", bias.dtype, (d_out,)) if bias is not None else None
-    bcode = _dtype_code(bias) if bias is not None else 0
-    r = f.take(residual, "residual", f.out_dtype, (m, d_out))
-    with f:
-        Y = f.empty((m, d_out))
-        Z = f.empty((m, d_out)) if save_preact else None
-        _own, ws, wsb = f.workspace(mx_linear_workspace_size(m, d_out, d_in, kind, f.out_code))
-        rest = (m, d_in, codes, scales, d_out, b, bcode, f.act, r, Y.data_ptr(), f.out_code,
-                Z.data_ptr() if save_preact else None, ws, wsb, f.stream)
+    codes, scales = w._pointers("w", device)
+    b, bcode, r = None, 0, None
+    if bias is not None:
+        b, bcode = _operand(bias, "bias", bias.dtype, (d_out,), device), _dtype_code(bias)
+    if residual is not None:
+        r = _operand(residual, "residual", dtype, (m, d_out), device)
+    _no_grad(None if mx else A, bias, residual)
+    with where:
+        Y = _empty2(m, d_out, dtype, device)
+        Z = _empty2(m, d_out, dtype, device) if save_preact else None
+        _own, ws, wsb = _scratch(workspace, mx_linear_workspace_size(m, d_out, d_in, kind, code), device)
+        z = Z.data_ptr() if save_preact else None
         if mx:
-            _check(_lib().gptq_mx_linear_mx(a[0], a[1], MX_FORMATS[kind], *rest))
+            a, s = A._pointers("A", device)
+            _check(_lib().gptq_mx_linear_mx(a, s, MX_FORMATS[kind], m, d_in, codes, scales, d_out, b, bcode, act, r,
+                                            Y.data_ptr(), code, z, ws, wsb, st))
         else:
-            _check(_lib().gptq_mx_linear(A.data_ptr(), kind, *rest))
+            _check(_lib().gptq_mx_linear(A.data_ptr(), kind, m, d_in, codes, scales, d_out, b, bcode, act, r,
+                                         Y.data_ptr(), code, z, ws, wsb, st))
     return (Y, Z) if save_preact else Y
 
 
@@ -856,24 +931,23 @@ def mx_linear_backward(dY, w: MxTensor, activation="none", preact=None, bias_gra
     dequant_linear_backward."""
     _mx_tensor(w, "w", "fp4")
     _require(dY, "dY", ndim=2)
-    code = _dtype_code(dY)
-    f = _MxCall(dY.device, "dY", workspace, stream)
-    f.epilogue(activation, out_dtype or dY.dtype)
-    f.no_grad(dY)
+    dcode, act, dtype, device = _dtype_code(dY), _activation(activation), out_dtype or dY.dtype, dY.device
+    code = _out_code(dtype)
+    st, where = _place(device, "dY", stream)
     m, d_out = dY.shape
-    if d_out != w.codes.shape[0]:
-        raise ValueError(f"dY has {d_out} columns, the layer {w.codes.shape[0]} rows")
-    if preact is None and f.act:
+    if d_out != w.rows:
+        raise ValueError(f"dY has {d_out} columns, the layer {w.rows} rows")
+    if preact is None and act:
         raise ValueError("preact is required unless activation is 'none'")
-    codes, scales = f.matrix(w, "w")
-    z = f.take(preact, "preact", dY.dtype, (m, d_out))
-    with f:
-        dA = f.empty((m, w.d))
-        db = f.empty((d_out,), _torch().float32) if bias_grad else None
-        _own, ws, wsb = f.workspace(mx_linear_backward_workspace_size(m, d_out, w.d, code, f.out_code))
-        _check(_lib().gptq_mx_linear_backward(dY.data_ptr(), code, m, d_out, z, f.act, codes, scales, w.d,
-                                              dA.data_ptr(), f.out_code, db.data_ptr() if bias_grad else None, ws,
-                                              wsb, f.stream))
+    codes, scales = w._pointers("w", device)
+    z = None if preact is None else _operand(preact, "preact", dY.dtype, (m, d_out), device)
+    _no_grad(dY, preact)
+    with where:
+        dA = _empty2(m, w.d, dtype, device)
+        db = _TORCH.empty_strided((d_out,), (1,), dtype=_TORCH.float32, device=device) if bias_grad else None
+        _own, ws, wsb = _scratch(workspace, mx_linear_backward_workspace_size(m, d_out, w.d, dcode, code), device)
+        _check(_lib().gptq_mx_linear_backward(dY.data_ptr(), dcode, m, d_out, z, act, codes, scales, w.d,
+                                              dA.data_ptr(), code, db.data_ptr() if bias_grad else None, ws, wsb, st))
     return dA, db
 
 
@@ -886,30 +960,31 @@ def rms_norm(X, weight, residual=None, eps=1e-6, format=None, stream=None):
     mx_linear takes).  S is the residual stream behind the addition, X itself
     without a residual; rms_norm_backward takes it."""
     _require(X, "X", ndim=2)
-    code = _dtype_code(X)
+    code, dtype, device = _dtype_code(X), X.dtype, X.device
     fmt = None if format is None else _mx_format(format)
-    f = _MxCall(X.device, "X", stream=stream)
-    f.no_grad(X)
-    m, d = X.shape
-    if weight is None:
-        raise ValueError("weight is required")
-    w = f.take(weight, "weight", X.dtype, (d,))
-    r = f.take(residual, "residual", X.dtype, (m, d))
-    with f:
-        S = X if residual is None else f.empty((m, d), X.dtype)
-        s = None if residual is None else S.data_ptr()
+    st, where = _place(device, "X", stream)
+    m, d = shape = X.shape
+    w = _operand(weight, "weight", dtype, (d,), device)
+    r = None if residual is None else _operand(residual, "residual", dtype, shape, device)
+    _no_grad(X, weight, residual)
+    with where:
+        S, s = X, None
+        if residual is not None:
+            S = _empty2(m, d, dtype, device)
+            s = S.data_ptr()
         if fmt is None:
-            Y = f.empty((m, d), X.dtype)
-            _check(_lib().gptq_rms_norm(X.data_ptr(), r, w, code, m, d, float(eps), s, Y.data_ptr(), f.stream))
+            Y = _empty2(m, d, dtype, device)
+            _check(_lib().gptq_rms_norm(X.data_ptr(), r, w, code, m, d, float(eps), s, Y.data_ptr(), st))
         else:
-            Y = f.new_matrix(m, d, format)
-            _check(_lib().gptq_rms_norm_mx(X.data_ptr(), r, w, code, m, d, float(eps), s, fmt, Y.codes.data_ptr(),
-                                           Y.scales.data_ptr(), f.stream))
+            Y = MxTensor._empty(m, d, format, device)
+            codes, scales = Y._pointers("Y", device)
+            _check(_lib().gptq_rms_norm_mx(X.data_ptr(), r, w, code, m, d, float(eps), s, fmt, codes, scales,
+                                           st))
     return Y, S
 
 
 def rms_norm_backward_workspace_size(m, d) -> int:
-    return int(_lib().gptq_rms_norm_backward_workspace_size(m, d))
+    return _lib().gptq_rms_norm_backward_workspace_size(m, d)
 
 
 def rms_norm_backward(dY, S, weight, eps=1e-6, dS=None, weight_grad=True, workspace=None, stream=None):
@@ -920,21 +995,19 @@ def rms_norm_backward(dY, S, weight, eps=1e-6, dS=None, weight_grad=True, worksp
     residual stream's), added to dX.  dX: of that dtype; dweight: [d] float32,
     or None unless weight_grad."""
     _require(dY, "dY", ndim=2)
-    code = _dtype_code(dY)
-    f = _MxCall(dY.device, "dY", workspace, stream)
-    f.no_grad(dY)
-    m, d = dY.shape
-    if S is None or weight is None:
-        raise ValueError("S and weight are required")
-    s = f.take(S, "S", dY.dtype, (m, d))
-    w = f.take(weight, "weight", dY.dtype, (d,))
-    t = f.take(dS, "dS", dY.dtype, (m, d))
-    with f:
-        dX = f.empty((m, d), dY.dtype)
-        dw = f.empty((d,), _torch().float32) if weight_grad else None
-        _own, ws, wsb = f.workspace(rms_norm_backward_workspace_size(m, d))
+    code, dtype, device = _dtype_code(dY), dY.dtype, dY.device
+    st, where = _place(device, "dY", stream)
+    m, d = shape = dY.shape
+    s = _operand(S, "S", dtype, shape, device)
+    w = _operand(weight, "weight", dtype, (d,), device)
+    t = None if dS is None else _operand(dS, "dS", dtype, shape, device)
+    _no_grad(dY, S, weight, dS)
+    with where:
+        dX = _empty2(m, d, dtype, device)
+        dw = _TORCH.empty_strided((d,), (1,), dtype=_TORCH.float32, device=device) if weight_grad else None
+        _own, ws, wsb = _scratch(workspace, rms_norm_backward_workspace_size(m, d), device)
         _check(_lib().gptq_rms_norm_backward(dY.data_ptr(), s, w, t, code, m, d, float(eps), dX.data_ptr(),
-                                             dw.data_ptr() if weight_grad else None, ws, wsb, f.stream))
+                                             dw.data_ptr() if weight_grad else None, ws, wsb, st))
     return dX, dw
 
 

@@ -73,12 +73,16 @@ __device__ __forceinline__ void mx_put8(const float (&v)[8], int64_t rows, int64
 // eight values of a row from column k on, zeros past its end
 __device__ __forceinline__ void mx_ld8(const void *x, int64_t row, int64_t d, int64_t k, int bf16, int vec,
                                        float (&v)[8]) {
-    const int64_t o = row * d + k;
-    if (vec && k < d) {
-        fz_ld8(x, o, bf16, v);
-    } else {
+    if (k >= d) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = k + e < d ? fz_ld(x, o + e, bf16) : 0.f;
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    } else if (vec) {
+        fz_ld8(x, row * d + k, bf16, v);
+    } else {   // (clamped and selected: a branch around each load would wait for each)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fz_ld(x, row * d + std::min(k + e, d - 1), bf16);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = k + e < d ? v[e] : 0.f;
     }
 }
 

@@ -8,7 +8,7 @@
 //
 // Both directions are bound by memory.  A lane takes eight columns, four lanes
 // a block, a wave four pieces of 512 columns of one row, so that four loads of
-// each lane are in flight.
+// each lane are in flight; of rows up to 256 columns wide, several at a time.
 #include "mx.h"
 
 #include <algorithm>
@@ -19,28 +19,55 @@ namespace {
 
 constexpr int QC = 4, QCOLS = QC * 512;   // pieces, and columns, of a wave
 
+// The units of work of the waves: QC pieces of a row, or of 64 >> shift rows
+// with 1 << shift lanes each
+struct Units {
+    int64_t chunks, units;      // a row's waves, all waves
+    int shift;                  // 4 or 5: narrow rows; 0: not
+    __device__ __forceinline__ void at(int64_t u, int c, int64_t &row, int64_t &k) const {
+        const int lane = threadIdx.x & 63;
+        if (shift) {
+            row = ((u * QC + c) << (6 - shift)) + (lane >> shift);
+            k = 8 * (lane & ((1 << shift) - 1));
+        } else {
+            row = u / chunks;
+            k = (u - row * chunks) * QCOLS + 512 * c + 8 * lane;
+        }
+    }
+};
+Units units_of(int64_t rows, int64_t d) {
+    Units u{};
+    const int64_t steps = mx_steps(d);
+    u.shift = steps == 1 ? 4 : (steps == 2 ? 5 : 0);
+    u.chunks = cdiv(steps * MX_PAD, QCOLS);
+    u.units = u.shift ? cdiv(rows, (int64_t)QC << (6 - u.shift)) : rows * u.chunks;
+    return u;
+}
+
 struct QuantMx {
     const void *X;
     int bf16, vec;
     int64_t rows, d, steps, row_bytes;
     uint8_t *codes, *scales;
-    int64_t chunks, units;      // a row's waves, all waves
+    Units w;
 };
 
-template <int FMT>
+template <int FMT, bool VEC>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(QuantMx p) {
-    const int lane = threadIdx.x & 63;
-    for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < p.units; u += (int64_t)gridDim.x * 4) {
-        const int64_t row = u / p.chunks, k0 = (u - row * p.chunks) * QCOLS + 8 * lane;
+    p.vec = VEC;   // (known here: the other way of loading costs registers)
+    for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < p.w.units; u += (int64_t)gridDim.x * 4) {
+        int64_t row[QC], k[QC];
         float v[QC][8];
 #pragma unroll
-        for (int c = 0; c < QC; ++c) mx_ld8(p.X, row, p.d, k0 + 512 * c, p.bf16, p.vec, v[c]);
-#pragma unroll
         for (int c = 0; c < QC; ++c) {
-            const int64_t k = k0 + 512 * c;
-            // (a block's four lanes are inside or outside together)
-            if (k < p.steps * MX_PAD) mx_put8<FMT>(v[c], p.rows, row, k >> 3, p.row_bytes, p.codes, p.scales);
+            p.w.at(u, c, row[c], k[c]);
+            mx_ld8(p.X, row[c], p.d, row[c] < p.rows ? k[c] : p.d, p.bf16, p.vec, v[c]);
         }
+#pragma unroll
+        for (int c = 0; c < QC; ++c)
+            // (a block's four lanes are inside or outside together)
+            if (row[c] < p.rows && k[c] < p.steps * MX_PAD)
+                mx_put8<FMT>(v[c], p.rows, row[c], k[c] >> 3, p.row_bytes, p.codes, p.scales);
     }
 }
 
@@ -49,22 +76,22 @@ struct DequantMx {
     int64_t rows, d, row_bytes;
     void *Y;
     int bf16, vec;
-    int64_t chunks, units;
+    Units w;
 };
 
 template <int FMT>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantMx p) {
-    const int lane = threadIdx.x & 63;
-    for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < p.units; u += (int64_t)gridDim.x * 4) {
-        const int64_t row = u / p.chunks, k0 = (u - row * p.chunks) * QCOLS + 8 * lane;
+    for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < p.w.units; u += (int64_t)gridDim.x * 4) {
+        int64_t at[QC], k[QC];
         u32x2 w[QC];
         unsigned byte[QC];
 #pragma unroll
         for (int c = 0; c < QC; ++c) {
-            const int64_t piece = (k0 + 512 * c) >> 3;
+            p.w.at(u, c, at[c], k[c]);
+            const int64_t row = at[c], piece = k[c] >> 3;
             w[c] = u32x2{0u, 0u};
             byte[c] = 0;
-            if (k0 + 512 * c < p.d) {
+            if (row < p.rows && k[c] < p.d) {
                 const uint8_t *in = p.x.codes + row * p.row_bytes + piece * (FMT == MX_FP4 ? 4 : 8);
                 if constexpr (FMT == MX_FP4)
                     w[c][0] = *(const unsigned *)in;
@@ -75,8 +102,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantMx p) {
         }
 #pragma unroll
         for (int c = 0; c < QC; ++c) {
-            const int64_t k = k0 + 512 * c;
-            if (k >= p.d) break;
+            if (at[c] >= p.rows || k[c] >= p.d) continue;
             float v[8];
             if constexpr (FMT == MX_FP4) {
                 // (the conversion reads the scale's exponent bits: 0 is 2^-127, 255 NaN)
@@ -100,13 +126,13 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantMx p) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = byte[c] == 255u ? __builtin_nanf("") : fz_ldexp(v[e], e2);
             }
-            const int64_t o = row * p.d + k;
+            const int64_t o = at[c] * p.d + k[c];
             if (p.vec) {
                 fz_st8(p.Y, o, p.bf16, v);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (k + e < p.d) fz_st(p.Y, o + e, v[e], p.bf16);
+                    if (k[c] + e < p.d) fz_st(p.Y, o + e, v[e], p.bf16);
             }
         }
     }
@@ -129,12 +155,16 @@ hipError_t mx_quantize_launch(const void *X, int x_bf16, int64_t rows, int64_t d
     p.row_bytes = mx_row_bytes(d, fmt);
     p.codes = codes;
     p.scales = scales;
-    p.chunks = cdiv(p.steps * MX_PAD, QCOLS);
-    p.units = rows * p.chunks;
-    if (fmt == MX_FP4)
-        mx_quantize_kernel<MX_FP4><<<wave_blocks(p.units), 256, 0, st>>>(p);
+    p.w = units_of(rows, d);
+    const unsigned blocks = wave_blocks(p.w.units);
+    if (fmt == MX_FP4 && p.vec)
+        mx_quantize_kernel<MX_FP4, true><<<blocks, 256, 0, st>>>(p);
+    else if (fmt == MX_FP4)
+        mx_quantize_kernel<MX_FP4, false><<<blocks, 256, 0, st>>>(p);
+    else if (p.vec)
+        mx_quantize_kernel<MX_FP8, true><<<blocks, 256, 0, st>>>(p);
     else
-        mx_quantize_kernel<MX_FP8><<<wave_blocks(p.units), 256, 0, st>>>(p);
+        mx_quantize_kernel<MX_FP8, false><<<blocks, 256, 0, st>>>(p);
     return hipGetLastError();
 }
 
@@ -147,12 +177,11 @@ hipError_t mx_dequantize_launch(const MxMatrix &x, int64_t rows, int64_t d, void
     p.Y = Y;
     p.bf16 = y_bf16;
     p.vec = d % 8 == 0 && aligned16(Y);
-    p.chunks = cdiv(d, QCOLS);
-    p.units = rows * p.chunks;
+    p.w = units_of(rows, d);
     if (x.fmt == MX_FP4)
-        mx_dequantize_kernel<MX_FP4><<<wave_blocks(p.units), 256, 0, st>>>(p);
+        mx_dequantize_kernel<MX_FP4><<<wave_blocks(p.w.units), 256, 0, st>>>(p);
     else
-        mx_dequantize_kernel<MX_FP8><<<wave_blocks(p.units), 256, 0, st>>>(p);
+        mx_dequantize_kernel<MX_FP8><<<wave_blocks(p.w.units), 256, 0, st>>>(p);
     return hipGetLastError();
 }
 

@@ -48,16 +48,26 @@ __device__ __forceinline__ void act_raw(const SkinnyArgs &p, int64_t row, int64_
             const u32x4 u = *(const u32x4 *)(a + (in ? k : 0) * BYTES + 16 * i);
             out[i] = in ? u : u32x4{0u, 0u, 0u, 0u};
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < BYTES / 2; ++i) out[i] = u32x4{0u, 0u, 0u, 0u};
+    } else {   // (clamped and selected: a branch around each load would wait for each)
+        unsigned v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (k + e >= p.d_in) continue;
+            const int64_t at = std::min(k + e, p.d_in - 1);
             if constexpr (BYTES == 2)
-                out[0][e >> 1] |= (unsigned)((const uint16_t *)a)[k + e] << (16 * (e & 1));
+                v[e] = ((const uint16_t *)a)[at];
             else
-                out[e >> 2][e & 3] = ((const unsigned *)a)[k + e];
+                v[e] = ((const unsigned *)a)[at];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = k + e < p.d_in ? v[e] : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (BYTES == 2) {
+                out[0][i] = v[2 * i] | v[2 * i + 1] << 16;
+            } else {
+                out[0][i] = v[i];
+                out[BYTES / 2 - 1][i] = v[4 + i];
+            }
         }
     }
 }

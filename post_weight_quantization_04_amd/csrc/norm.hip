@@ -19,20 +19,20 @@ namespace gptq {
 
 namespace {
 
-// Sums over the threads of a row: WPR waves (4 / WPR rows of a block where
-// WPR is 1).  Fixed order: lanes by halves, then waves in turn.
-template <int WPR, class T>
+// Sums over the LANES threads of a row (256 / LANES rows of a block up to a
+// wave each).  Fixed order: lanes by halves, then waves in turn.
+template <int LANES, class T>
 __device__ __forceinline__ T row_sum(T v, T *lds) {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    if constexpr (WPR > 1) {
+    for (int o = std::min(LANES, 64) / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    if constexpr (LANES > 64) {
         const int wave = threadIdx.x >> 6;
         __syncthreads();   // (the sums of the row before have been read)
         if ((threadIdx.x & 63) == 0) lds[wave] = v;
         __syncthreads();
         v = lds[0];
 #pragma unroll
-        for (int w = 1; w < WPR; ++w) v += lds[w];
+        for (int w = 1; w < LANES / 64; ++w) v += lds[w];
     }
     return v;
 }
@@ -91,15 +91,16 @@ __device__ __forceinline__ void norm_store(const NormArgs &p, int64_t row, int64
     }
 }
 
-// WPR waves per row, each thread NC pieces of eight columns held in registers
+// LANES threads per row, each NC pieces of eight columns held in registers
 // between the two sweeps; columns beyond them are formed again from the inputs
-template <int WPR, int NC>
-__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rms_norm_kernel(NormArgs p) {
-    constexpr int STEP = 512 * WPR;
-    __shared__ double lds[WPR];
-    const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-    if (row >= p.a.m) return;   // (whole waves, and whole blocks where they meet at barriers)
-    const int64_t k0 = 8 * (WPR == 1 ? threadIdx.x & 63 : threadIdx.x);
+template <int LANES, int NC, bool VEC>
+__global__ __launch_bounds__(std::max(LANES, 256)) void rms_norm_kernel(NormArgs p) {
+    p.vec = VEC;   // (known here: the other way of loading costs registers)
+    constexpr int STEP = 8 * LANES, ROWS = std::max(1, 256 / LANES);
+    __shared__ double lds[std::max(1, LANES / 64)];
+    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
+    if (row >= p.a.m) return;   // (all lanes of a row together)
+    const int64_t k0 = 8 * (threadIdx.x % LANES);
     float v[NC][8];
 #pragma unroll
     for (int c = 0; c < NC; ++c) norm_load(p, row, k0 + c * STEP, v[c]);
@@ -116,7 +117,7 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rms_norm_kernel(Nor
         norm_load(p, row, k, x);
         take(k, x);
     }
-    const double r = 1.0 / sqrt(row_sum<WPR>(sum, lds) * p.inv_d + p.a.eps);
+    const double r = 1.0 / sqrt(row_sum<LANES>(sum, lds) * p.inv_d + p.a.eps);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
         if (k0 + c * STEP < p.padded) norm_store(p, row, k0 + c * STEP, r, v[c]);
@@ -147,20 +148,30 @@ template <bool BF16>
 struct Raw8 {
     u32x4 q[BF16 ? 1 : 2];
     __device__ __forceinline__ void load(const void *x, int64_t row, int64_t d, int64_t k, int vec) {
-        const int64_t o = row * d + k;
         if (vec) {
             const bool in = k < d;
-            const u32x4 *src = (const u32x4 *)((const char *)x + (in ? o : 0) * (BF16 ? 2 : 4));
+            const u32x4 *src = (const u32x4 *)((const char *)x + (in ? row * d + k : 0) * (BF16 ? 2 : 4));
 #pragma unroll
             for (int i = 0; i < (BF16 ? 1 : 2); ++i) q[i] = in ? src[i] : u32x4{0u, 0u, 0u, 0u};
-        } else {
+        } else {   // (clamped and selected: a branch around each load would wait for each)
+            unsigned v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
+                const int64_t o = row * d + std::min(k + e, d - 1);
+                if constexpr (BF16)
+                    v[e] = ((const uint16_t *)x)[o];
+                else
+                    v[e] = ((const unsigned *)x)[o];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = k + e < d ? v[e] : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 if constexpr (BF16) {
-                    const unsigned v = k + e < d ? ((const uint16_t *)x)[o + e] : 0u;
-                    q[0][e >> 1] = (e & 1) ? q[0][e >> 1] | v << 16 : v;
+                    q[0][i] = v[2 * i] | v[2 * i + 1] << 16;
                 } else {
-                    q[e >> 2][e & 3] = k + e < d ? ((const unsigned *)x)[o + e] : 0u;
+                    q[0][i] = v[i];
+                    q[BF16 ? 0 : 1][i] = v[4 + i];
                 }
             }
         }
@@ -212,8 +223,9 @@ __device__ __forceinline__ void norm_put_sums(const NormBackArgs &p, int64_t gro
 // Rows that fit a group of WPR waves, eight columns a thread: read once.  A
 // group takes every groups-th row, the next one's loads in flight behind the
 // present one's sums; the weights and its sums of dw stay in registers.
-template <int WPR, bool BF16>
+template <int WPR, bool BF16, bool VEC>
 __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_backward_kernel(NormBackArgs p) {
+    p.vec = VEC;
     constexpr int PER = WPR < 4 ? 4 / WPR : 1;   // groups of a block
     __shared__ double lds[2][PER][2][WPR];
     const int sub = threadIdx.x / (64 * WPR), tid = threadIdx.x % (64 * WPR);
@@ -267,8 +279,9 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_backward_ke
 }
 
 // Wider rows: their factors first ...
-template <bool BF16>
+template <bool BF16, bool VEC>
 __global__ __launch_bounds__(1024) void norm_factors_kernel(NormBackArgs p) {
+    p.vec = VEC;
     __shared__ double lds[2][16];
     const int64_t row = blockIdx.x, d = p.a.d;
     double sq = 0.0, dot = 0.0;
@@ -279,13 +292,14 @@ __global__ __launch_bounds__(1024) void norm_factors_kernel(NormBackArgs p) {
         w.load(p.a.weight, 0, d, k, p.vec);
         norm_sums(s, g, w, sq, dot);
     }
-    sq = row_sum<16>(sq, lds[0]);
-    dot = row_sum<16>(dot, lds[1]);
+    sq = row_sum<1024>(sq, lds[0]);
+    dot = row_sum<1024>(dot, lds[1]);
     if (threadIdx.x == 0) norm_factors(p, sq, dot, p.stats[2 * row], p.stats[2 * row + 1]);
 }
 // ... then 2048 columns of every groups-th row to a block
-template <bool BF16>
+template <bool BF16, bool VEC>
 __global__ __launch_bounds__(256) void norm_columns_kernel(NormBackArgs p) {
+    p.vec = VEC;
     const int64_t k = (int64_t)blockIdx.x * 2048 + 8 * threadIdx.x, group = blockIdx.y, d = p.a.d;
     if (k >= d) return;
     Raw8<BF16> w;
@@ -302,6 +316,53 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(NormBackArgs p) {
         norm_leave(p, row, k, p.stats[2 * row], p.stats[2 * row + 1], s, g, w, t, dw);
     }
     norm_put_sums(p, group, k, dw);
+}
+
+// Few rows of whole pieces of eight: one launch.  A block takes 512 columns and
+// finds every row's factors by itself, a wave per row; the waves' terms of dw
+// meet in LDS.  us a call from Python, this / two launches: bf16 1 x 4096 8.3 /
+// 12.1, 16 x 4096 9.4 / 12.0; beyond, the blocks' repeated reads cost more: fp32 46 x
+// 1408 14.8 / 12, rows that are not whole pieces (16 x 1407) 47 / 12.
+constexpr int SMALL_ROWS = 16, SMALL_COLS = 4096;
+template <bool BF16>
+__global__ __launch_bounds__(64 * SMALL_ROWS) void norm_backward_small_kernel(NormBackArgs p) {
+    __shared__ float sums[SMALL_ROWS][512];
+    const int lane = threadIdx.x & 63, row = threadIdx.x >> 6;
+    const int64_t d = p.a.d, k0 = (int64_t)blockIdx.x * 512 + 8 * lane;
+    float dw[8] = {};
+    if (row < p.a.m) {
+        Raw8<BF16> s, g, w, t;
+        double sq = 0.0, dot = 0.0;
+        for (int64_t k = 8 * lane; k < d; k += 512) {
+            s.load(p.a.S, row, d, k, p.vec);
+            g.load(p.a.dY, row, d, k, p.vec);
+            w.load(p.a.weight, 0, d, k, p.vec);
+            norm_sums(s, g, w, sq, dot);
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            sq += __shfl_xor(sq, o);
+            dot += __shfl_xor(dot, o);
+        }
+        float r, f;
+        norm_factors(p, sq, dot, r, f);
+        s.load(p.a.S, row, d, k0, p.vec);
+        g.load(p.a.dY, row, d, k0, p.vec);
+        w.load(p.a.weight, 0, d, k0, p.vec);
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) t.q[i] = u32x4{0u, 0u, 0u, 0u};
+        if (p.a.dS) t.load(p.a.dS, row, d, k0, p.vec);
+        if (k0 < d) norm_leave(p, row, k0, r, f, s, g, w, t, dw);
+    }
+    if (!p.a.dweight) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[row][8 * lane + e] = dw[e];
+    __syncthreads();
+    const int64_t k = (int64_t)blockIdx.x * 512 + threadIdx.x;
+    if (threadIdx.x >= 512 || k >= d) return;
+    double sum = 0.0;
+    for (int i = 0; i < p.a.m; ++i) sum += (double)sums[i][threadIdx.x];
+    p.a.dweight[k] = (float)sum;
 }
 
 // dw from the groups' sums: 32 columns of a block, 32 threads a column, each
@@ -323,37 +384,31 @@ __global__ __launch_bounds__(1024) void norm_weight_reduce_kernel(const float *p
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Pieces per thread and waves per row.  Few rows: many waves (a row's latency
-// counts); many: one or eight, so that a CU holds several rows.  (4096 x 4096
-// fp32 with a residual: eight waves 45 us, four 53; bf16 26 and 27; sixteen 48.)
+// Threads per row and pieces per thread.  Few rows: many threads (a row's latency
+// counts); many: as many as hold it in a few pieces, so that a CU holds several
+// rows.  us with a residual: 4096 x 4096 fp32 512 threads 45, 256 53, bf16 26, 27,
+// and 1024 48; 64000 x 128 bf16 16 threads 13, 64 44.
 struct RowPlan {
-    int wpr, nc;
+    int lanes, nc;
 };
 RowPlan row_plan(int64_t m, int64_t d) {
-    if (d <= 2048 && m >= 256) return {1, d <= 512 ? 1 : d <= 1024 ? 2 : 4};
-    if (d <= 8192 && m >= 256) return {8, d <= 4096 ? 1 : 2};
-    return {16, d <= 8192 ? 1 : d <= 16384 ? 2 : 4};
+    if (d <= 128 && m >= 256) return {16, 1};
+    if (d <= 2048 && m >= 256) return {64, d <= 512 ? 1 : d <= 1024 ? 2 : 4};
+    if (d <= 8192 && m >= 256) return {512, d <= 4096 ? 1 : 2};
+    return {1024, d <= 8192 ? 1 : d <= 16384 ? 2 : 4};
 }
-template <class F>
-hipError_t with_plan(const RowPlan &p, F f) {
-    using std::integral_constant;
-    auto waves = [&](auto w) {
-        switch (p.nc) {
-            case 1: f(w, integral_constant<int, 1>{}); break;
-            case 2: f(w, integral_constant<int, 2>{}); break;
-            default: f(w, integral_constant<int, 4>{}); break;
-        }
-    };
-    switch (p.wpr) {
-        case 1: waves(integral_constant<int, 1>{}); break;
-        case 8: waves(integral_constant<int, 8>{}); break;
-        default: waves(integral_constant<int, 16>{}); break;
-    }
+template <int LANES, int NC>
+hipError_t launch_norm(const NormArgs &p, hipStream_t st) {
+    const unsigned blocks = (unsigned)cdiv(p.a.m, std::max(1, 256 / LANES)), threads = std::max(LANES, 256);
+    if (p.vec)
+        rms_norm_kernel<LANES, NC, true><<<blocks, threads, 0, st>>>(p);
+    else
+        rms_norm_kernel<LANES, NC, false><<<blocks, threads, 0, st>>>(p);
     return hipGetLastError();
 }
 
-// The backward pass: waves of a group (0: rows wider than one group reads), and
-// the groups of rows that sum dw at once, multiples of a block's.
+// The backward pass: waves of a group (0: rows wider than one group reads; -1:
+// few rows), and the groups of rows that sum dw at once, multiples of a block's.
 struct BackPlan {
     int wpr;
     int64_t groups;
@@ -361,6 +416,7 @@ struct BackPlan {
 constexpr int64_t NORM_WAVES = 4096;
 BackPlan back_plan(int64_t m, int64_t d) {
     BackPlan p{1, 0};
+    if (m <= SMALL_ROWS && d <= SMALL_COLS && d % 8 == 0) return {-1, 0};
     if (d > 8192) {
         p.wpr = 0;
         p.groups = std::min(m, std::max<int64_t>(1, 1024 / cdiv(d, 2048)));
@@ -371,20 +427,20 @@ BackPlan back_plan(int64_t m, int64_t d) {
     p.groups = std::min(cdiv(m, per) * per, NORM_WAVES / p.wpr);
     return p;
 }
-template <bool BF16>
+template <bool BF16, bool VEC>
 hipError_t launch_backward(const NormBackArgs &p, int wpr, hipStream_t st) {
     const unsigned blocks = (unsigned)p.groups;
     switch (wpr) {
-        case 1: rms_norm_backward_kernel<1, BF16><<<blocks / 4, 256, 0, st>>>(p); break;
-        case 2: rms_norm_backward_kernel<2, BF16><<<blocks / 2, 256, 0, st>>>(p); break;
-        case 4: rms_norm_backward_kernel<4, BF16><<<blocks, 256, 0, st>>>(p); break;
-        case 8: rms_norm_backward_kernel<8, BF16><<<blocks, 512, 0, st>>>(p); break;
-        case 16: rms_norm_backward_kernel<16, BF16><<<blocks, 1024, 0, st>>>(p); break;
+        case 1: rms_norm_backward_kernel<1, BF16, VEC><<<blocks / 4, 256, 0, st>>>(p); break;
+        case 2: rms_norm_backward_kernel<2, BF16, VEC><<<blocks / 2, 256, 0, st>>>(p); break;
+        case 4: rms_norm_backward_kernel<4, BF16, VEC><<<blocks, 256, 0, st>>>(p); break;
+        case 8: rms_norm_backward_kernel<8, BF16, VEC><<<blocks, 512, 0, st>>>(p); break;
+        case 16: rms_norm_backward_kernel<16, BF16, VEC><<<blocks, 1024, 0, st>>>(p); break;
         default: {
-            norm_factors_kernel<BF16><<<(unsigned)p.a.m, 1024, 0, st>>>(p);
+            norm_factors_kernel<BF16, VEC><<<(unsigned)p.a.m, 1024, 0, st>>>(p);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
-            norm_columns_kernel<BF16><<<dim3((unsigned)cdiv(p.a.d, 2048), blocks), 256, 0, st>>>(p);
+            norm_columns_kernel<BF16, VEC><<<dim3((unsigned)cdiv(p.a.d, 2048), blocks), 256, 0, st>>>(p);
         }
     }
     return hipGetLastError();
@@ -401,16 +457,23 @@ hipError_t rms_norm_launch(const RmsNorm &a, hipStream_t st) {
     p.row_bytes = a.Y ? 0 : mx_row_bytes(a.d, a.fmt);
     p.inv_d = 1.0 / (double)a.d;
     const RowPlan plan = row_plan(a.m, a.d);
-    return with_plan(plan, [&](auto w, auto n) {
-        constexpr int W = decltype(w)::value, N = decltype(n)::value;
-        const unsigned blocks = (unsigned)(W == 1 ? cdiv(a.m, 4) : a.m);
-        rms_norm_kernel<W, N><<<blocks, W == 1 ? 256 : 64 * W, 0, st>>>(p);
-    });
+    switch (plan.lanes * 8 + plan.nc) {
+        case 16 * 8 + 1: return launch_norm<16, 1>(p, st);
+        case 64 * 8 + 1: return launch_norm<64, 1>(p, st);
+        case 64 * 8 + 2: return launch_norm<64, 2>(p, st);
+        case 64 * 8 + 4: return launch_norm<64, 4>(p, st);
+        case 512 * 8 + 1: return launch_norm<512, 1>(p, st);
+        case 512 * 8 + 2: return launch_norm<512, 2>(p, st);
+        case 1024 * 8 + 1: return launch_norm<1024, 1>(p, st);
+        case 1024 * 8 + 2: return launch_norm<1024, 2>(p, st);
+        default: return launch_norm<1024, 4>(p, st);
+    }
 }
 
 size_t rms_norm_backward_ws(int64_t m, int64_t d) {
     if (m == 0) return 0;
     const BackPlan p = back_plan(m, d);
+    if (p.wpr < 0) return 0;
     return align256((size_t)p.groups * d * sizeof(float)) + (p.wpr ? 0 : align256((size_t)m * 2 * sizeof(float)));
 }
 
@@ -422,10 +485,22 @@ hipError_t rms_norm_backward_launch(const RmsNormBackward &a, hipStream_t st) {
     p.inv_d = 1.0 / (double)a.d;
     if (a.m > 0) {
         const BackPlan plan = back_plan(a.m, a.d);
+        if (plan.wpr < 0) {
+            const unsigned blocks = (unsigned)cdiv(a.d, 512);
+            if (a.bf16)
+                norm_backward_small_kernel<true><<<blocks, 64 * SMALL_ROWS, 0, st>>>(p);
+            else
+                norm_backward_small_kernel<false><<<blocks, 64 * SMALL_ROWS, 0, st>>>(p);
+            return hipGetLastError();
+        }
         p.groups = plan.groups;
         p.part = a.dweight ? (float *)a.ws : nullptr;
         p.stats = (float *)(a.ws + align256((size_t)p.groups * a.d * sizeof(float)));
-        const hipError_t e = a.bf16 ? launch_backward<true>(p, plan.wpr, st) : launch_backward<false>(p, plan.wpr, st);
+        hipError_t e;
+        if (p.vec)
+            e = a.bf16 ? launch_backward<true, true>(p, plan.wpr, st) : launch_backward<false, true>(p, plan.wpr, st);
+        else
+            e = a.bf16 ? launch_backward<true, false>(p, plan.wpr, st) : launch_backward<false, false>(p, plan.wpr, st);
         if (e != hipSuccess) return e;
     }
     if (!a.dweight) return hipSuccess;

@@ -109,7 +109,7 @@ def gauss(seed, *shape):
     return torch.randn(*shape, generator=gen, device=DEV)
 
 
-SHAPES = [(1, 1), (3, 31), (2, 32), (5, 33), (17, 127), (4, 128), (3, 129), (9, 1000), (1, 4096), (257, 520),
+SHAPES = [(1, 1), (3, 31), (2, 32), (5, 33), (17, 127), (4, 128), (3, 129), (9, 1000), (1, 4096), (257, 520), (1000, 128), (999, 100), (70, 256), (131, 200),
           (2, 20001), (0, 64)]
 
 
@@ -412,7 +412,7 @@ def test_no_rows_and_bias_gradients():
 # the norm
 # ---------------------------------------------------------------------------
 NORMS = [(1, 1), (1, 4096), (3, 7), (5, 64), (300, 96), (257, 513), (256, 1024), (300, 2048), (2, 2056), (259, 4096),
-         (260, 8192), (3, 8200), (2, 16384), (5, 33000), (2, 70000), (1000, 130)]
+         (260, 8192), (3, 8200), (2, 16384), (5, 33000), (2, 70000), (1000, 130), (1000, 128), (999, 100), (257, 1)]
 
 
 @pytest.mark.parametrize("fmt", [None, "fp8", "fp4"])
@@ -463,7 +463,7 @@ def test_norm_of_unusual_rows():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("m,d", NORMS + [(3000, 64), (1500, 4096)])
+@pytest.mark.parametrize("m,d", NORMS + [(3000, 64), (1500, 4096), (37, 1407), (16, 4096), (17, 4096), (16, 4104), (9, 1000), (9, 1001)])
 def test_norm_backward(m, d, dtype):
     say("norm backward", m, d, dtype)
     s = (gauss(d, m, d) * torch.exp(gauss(1, d))).to(DT[dtype])

@@ -66,7 +66,7 @@ def norm_mx(**kw):
 
 
 def norm_backward(**kw):
-    a = dict(A=FAKE, S_=FAKE, w=FAKE, xt=P.BF16, m=2, d_in=256, eps=1e-6, X=FAKE, dw=FAKE, ws=FAKE, wsb=BIG)
+    a = dict(A=FAKE, S_=FAKE, w=FAKE, xt=P.BF16, m=1024, d_in=256, eps=1e-6, X=FAKE, dw=FAKE, ws=FAKE, wsb=BIG)
     a.update(kw)
     return P.lib.gptq_rms_norm_backward(a["A"], a["S_"], a["w"], None, a["xt"], a["m"], a["d_in"], a["eps"], a["X"],
                                         a["dw"], a["ws"], a["wsb"], None)
@@ -147,7 +147,7 @@ def test_sizes_on_the_host():
         assert P.mx_linear_backward_workspace_size(*bad, P.BF16, P.BF16) == 0
     assert P.mx_linear_workspace_size(300, 8, 8, 5, P.BF16) == 0
     assert P.rms_norm_backward_workspace_size(-1, 8) == 0 and P.rms_norm_backward_workspace_size(0, 8) == 0
-    assert P.rms_norm_backward_workspace_size(4096, 4096) > 0
+    assert P.rms_norm_backward_workspace_size(4096, 4096) > 0 and P.rms_norm_backward_workspace_size(4, 64) == 0
 
 
 def test_binding_refuses_host_tensors():
