@@ -406,7 +406,7 @@ GPTQ_API gptq_status gptq_mx_dequantize(const uint8_t *codes, const uint8_t *sca
  *   gptq_mx_linear_backward  dZ = dY act'(Z),  dA = dZ W,  dbias[r] = sum_i dZ[i][r]
  * Activations, epilogue operands, dtypes, aliasing, aligning, workspace, limits and
  * errors are those of gptq_dequant_linear and gptq_dequant_linear_backward, with
- * the code and scale alignments above.
+ * the code and scale alignments above and m up to 2^30.
  * Numerics: fp32 sums, one rounding of each output to its dtype.  MX operands
  * enter as they are stored and their products are exact; but where FP8
  * activations give a BF16 result, the matrix cores add a group's products with

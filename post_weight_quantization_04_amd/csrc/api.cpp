@@ -382,6 +382,7 @@ gptq_status check_mx(const void *codes, const void *scales) {
 gptq_status check_mx_linear(int64_t m, int64_t d_out, int64_t d_in) {
     gptq_status s = check_rows(m, d_in);
     if (s != GPTQ_OK) return s;
+    if (m > (int64_t)1 << 30) return fail(GPTQ_EINVAL, "m must be at most 2^30");   // (a launch's threads)
     if (d_out < 1 || d_out > (int64_t)1 << 19) return fail(GPTQ_EINVAL, "d_out must be in [1, 2^19]");
     return GPTQ_OK;
 }

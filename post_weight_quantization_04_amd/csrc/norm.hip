@@ -44,6 +44,7 @@ struct NormArgs {
     RmsNorm a;
     int vec;                    // whole aligned pieces of eight
     int64_t padded, row_bytes;  // columns that are written (MX: whole 128), code bytes of a row
+    int64_t row0;               // the launch's first row
     double inv_d;
 };
 
@@ -98,7 +99,7 @@ __global__ __launch_bounds__(std::max(LANES, 256)) void rms_norm_kernel(NormArgs
     p.vec = VEC;   // (known here: the other way of loading costs registers)
     constexpr int STEP = 8 * LANES, ROWS = std::max(1, 256 / LANES);
     __shared__ double lds[std::max(1, LANES / 64)];
-    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
+    const int64_t row = p.row0 + (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
     if (row >= p.a.m) return;   // (all lanes of a row together)
     const int64_t k0 = 8 * (threadIdx.x % LANES);
     float v[NC][8];
@@ -140,6 +141,7 @@ struct NormBackArgs {
     double inv_d;
     float *part;                // [groups][d] the groups' sums of dw, or NULL
     float *stats;               // [m][2] r and r^2 c of wide rows
+    int64_t row0;               // the first row whose factors a launch finds
     int64_t groups;
 };
 
@@ -283,7 +285,7 @@ template <bool BF16, bool VEC>
 __global__ __launch_bounds__(1024) void norm_factors_kernel(NormBackArgs p) {
     p.vec = VEC;
     __shared__ double lds[2][16];
-    const int64_t row = blockIdx.x, d = p.a.d;
+    const int64_t row = p.row0 + blockIdx.x, d = p.a.d;
     double sq = 0.0, dot = 0.0;
     for (int64_t k = 8 * threadIdx.x; k < d; k += 8 * 1024) {
         Raw8<BF16> s, g, w;
@@ -397,14 +399,20 @@ RowPlan row_plan(int64_t m, int64_t d) {
     if (d <= 8192 && m >= 256) return {512, d <= 4096 ? 1 : 2};
     return {1024, d <= 8192 ? 1 : d <= 16384 ? 2 : 4};
 }
+constexpr int64_t MAX_BLOCKS = 1 << 20;   // of a launch (which has less than 2^32 threads)
 template <int LANES, int NC>
-hipError_t launch_norm(const NormArgs &p, hipStream_t st) {
-    const unsigned blocks = (unsigned)cdiv(p.a.m, std::max(1, 256 / LANES)), threads = std::max(LANES, 256);
-    if (p.vec)
-        rms_norm_kernel<LANES, NC, true><<<blocks, threads, 0, st>>>(p);
-    else
-        rms_norm_kernel<LANES, NC, false><<<blocks, threads, 0, st>>>(p);
-    return hipGetLastError();
+hipError_t launch_norm(NormArgs p, hipStream_t st) {
+    constexpr int ROWS = std::max(1, 256 / LANES), THREADS = std::max(LANES, 256);
+    for (p.row0 = 0; p.row0 < p.a.m; p.row0 += MAX_BLOCKS * ROWS) {
+        const unsigned blocks = (unsigned)std::min(cdiv(p.a.m - p.row0, ROWS), MAX_BLOCKS);
+        if (p.vec)
+            rms_norm_kernel<LANES, NC, true><<<blocks, THREADS, 0, st>>>(p);
+        else
+            rms_norm_kernel<LANES, NC, false><<<blocks, THREADS, 0, st>>>(p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // The backward pass: waves of a group (0: rows wider than one group reads; -1:
@@ -428,7 +436,7 @@ BackPlan back_plan(int64_t m, int64_t d) {
     return p;
 }
 template <bool BF16, bool VEC>
-hipError_t launch_backward(const NormBackArgs &p, int wpr, hipStream_t st) {
+hipError_t launch_backward(NormBackArgs p, int wpr, hipStream_t st) {
     const unsigned blocks = (unsigned)p.groups;
     switch (wpr) {
         case 1: rms_norm_backward_kernel<1, BF16, VEC><<<blocks / 4, 256, 0, st>>>(p); break;
@@ -437,9 +445,12 @@ hipError_t launch_backward(const NormBackArgs &p, int wpr, hipStream_t st) {
         case 8: rms_norm_backward_kernel<8, BF16, VEC><<<blocks, 512, 0, st>>>(p); break;
         case 16: rms_norm_backward_kernel<16, BF16, VEC><<<blocks, 1024, 0, st>>>(p); break;
         default: {
-            norm_factors_kernel<BF16, VEC><<<(unsigned)p.a.m, 1024, 0, st>>>(p);
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return e;
+            for (p.row0 = 0; p.row0 < p.a.m; p.row0 += MAX_BLOCKS) {
+                const unsigned rows = (unsigned)std::min(p.a.m - p.row0, MAX_BLOCKS);
+                norm_factors_kernel<BF16, VEC><<<rows, 1024, 0, st>>>(p);
+                const hipError_t e = hipGetLastError();
+                if (e != hipSuccess) return e;
+            }
             norm_columns_kernel<BF16, VEC><<<dim3((unsigned)cdiv(p.a.d, 2048), blocks), 256, 0, st>>>(p);
         }
     }

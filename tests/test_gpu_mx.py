@@ -93,20 +93,18 @@ def same(a, b):
     return torch.equal(torch.nan_to_num(a.double(), nan=-77.0), torch.nan_to_num(b.double(), nan=-77.0))
 
 
-def normal(gen, *shape):
-    return torch.randn(*shape, generator=gen, device=DEV)
-
-
-def seeded(*key):
+def seeded_gen(seed):
     gen = torch.Generator(device=DEV)
-    gen.manual_seed(hash(key) % (1 << 31))
+    gen.manual_seed(seed)
     return gen
 
 
+def ints(seed, lo, hi, *shape):
+    return torch.randint(lo, hi, shape, generator=seeded_gen(seed), device=DEV).float()
+
+
 def gauss(seed, *shape):
-    gen = torch.Generator(device=DEV)
-    gen.manual_seed(seed)
-    return torch.randn(*shape, generator=gen, device=DEV)
+    return torch.randn(*shape, generator=seeded_gen(seed), device=DEV)
 
 
 SHAPES = [(1, 1), (3, 31), (2, 32), (5, 33), (17, 127), (4, 128), (3, 129), (9, 1000), (1, 4096), (257, 520), (1000, 128), (999, 100), (70, 256), (131, 200),
@@ -118,7 +116,7 @@ SHAPES = [(1, 1), (3, 31), (2, 32), (5, 33), (17, 127), (4, 128), (3, 129), (9, 
 @pytest.mark.parametrize("rows,d", SHAPES)
 def test_quantize(rows, d, dtype, fmt):
     say("quantize", rows, d, dtype, fmt)
-    x = (gauss(rows * 7 + d, rows, d) * torch.exp2(torch.randint(-20, 20, (rows, 1), device=DEV).float())).to(DT[dtype])
+    x = (gauss(rows * 7 + d, rows, d) * torch.exp2(ints(d, -20, 20, rows, 1))).to(DT[dtype])
     t = P.mx_quantize(x, fmt)
     assert t.shape == (rows, d)
     if rows == 0:
@@ -239,8 +237,8 @@ PRODUCTS = [(1, 1, 1), (1, 16, 128), (2, 17, 33), (7, 100, 129), (16, 64, 4096),
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
 def test_products_of_exact_operands(m, n, k, kind):
     say("exact", m, n, k, kind)
-    x = torch.randint(-2, 3, (m, k), generator=None, device=DEV).float()
-    w = torch.randint(-3, 4, (n, k), device=DEV).float() * torch.exp2(torch.randint(-2, 3, (n, 1), device=DEV).float())
+    x = ints(m * 31 + k, -2, 3, m, k)
+    w = ints(n * 17 + k, -3, 4, n, k) * torch.exp2(ints(n, -2, 3, n, 1))
     x[:, 0] = 2.0
     wq = P.mx_quantize(w, "fp4")
     a, a64 = make_acts(kind, x)
@@ -297,7 +295,7 @@ def test_fp8_activations_of_wide_range_in_fp32(m):
     """Elements and blocks that span the format's range: an F32 result adds their products in fp32, not in the
     scaled matrix cores' 14 bits."""
     n, k = 60, 640
-    x = gauss(1, m, k) * torch.exp2(torch.randint(-17, 1, (m, k), device=DEV).float()) * 448
+    x = gauss(1, m, k) * torch.exp2(ints(3, -17, 1, m, k)) * 448
     t, a64 = make_acts("fp8", x)
     wq = P.mx_quantize(gauss(2, n, k), "fp4")
     w64 = values_of(wq)
@@ -336,12 +334,11 @@ def test_linear_backward(m, n, k, act, bias, dtype, out):
 def test_linear_backward_against_differences():
     # the gradient of sum(dY * linear(A)) along directions of A, in exact arithmetic of small integers
     n, k, m = 37, 96, 5
-    wq = P.mx_quantize(torch.randint(-3, 4, (n, k), device=DEV).float(), "fp4")
-    a = torch.randint(-4, 5, (m, k), device=DEV).float()
-    dy = torch.randint(-2, 3, (m, n), device=DEV).float()
+    wq = P.mx_quantize(ints(1, -3, 4, n, k), "fp4")
+    a, dy = ints(2, -4, 5, m, k), ints(3, -2, 3, m, n)
     da, _ = P.mx_linear_backward(dy, wq)
-    for _ in range(4):
-        v = torch.randint(-2, 3, (m, k), device=DEV).float()
+    for i in range(4):
+        v = ints(10 + i, -2, 3, m, k)
         up, down = P.mx_linear(a + v, wq), P.mx_linear(a - v, wq)
         assert float(((up - down).double() / 2 * dy.double()).sum()) == float((da.double() * v.double()).sum())
 
@@ -383,16 +380,80 @@ def test_values_that_are_not_finite(m, kind):
 def test_scales_of_any_size(kind):
     # rows of weights and activations at both ends of the exponents' range, products that fp32 holds
     m, n, k = 80, 40, 256
-    x, w = torch.randint(-2, 3, (m, k), device=DEV).float(), torch.randint(-3, 4, (n, k), device=DEV).float()
+    x, w = ints(1, -2, 3, m, k), ints(2, -3, 4, n, k)
     x[:, 0], w[:, 0] = 2.0, 3.0
-    se = torch.randint(-60, 60, (m, 1), device=DEV).float()
-    we = torch.randint(-50, 40, (n, 1), device=DEV).float()
+    se = ints(3, -60, 60, m, 1)
+    we = ints(4, -50, 40, n, 1)
     wq = P.mx_quantize(w * torch.exp2(we), "fp4")
     for rows in (80, 12):
         a, a64 = make_acts(kind, (x * torch.exp2(se))[:rows].contiguous())
         want = a64 @ values_of(wq).t()
         got = P.mx_linear(a, wq, out_dtype=torch.float32)
         assert torch.equal(got.double(), want.float().double())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_rows(kind):
+    """More rows than one pass of the dense form takes (16384)."""
+    m, n, k = 16384 + 131, 72, 160
+    wq = P.mx_quantize(ints(1, -3, 4, n, k), "fp4")
+    x = ints(2, -2, 3, m, k)
+    x[:, 0] = 2.0
+    a, a64 = make_acts(kind, x)
+    assert torch.equal(P.mx_linear(a, wq, out_dtype=torch.float32).double(), a64 @ values_of(wq).t())
+    if kind in DT:
+        dy = ints(3, -2, 3, m, n).to(DT[kind])
+        da, db = P.mx_linear_backward(dy, wq, bias_grad=True, out_dtype=torch.float32)
+        assert torch.equal(da.double(), dy.double() @ values_of(wq))
+        assert torch.equal(db.double(), dy.double().sum(0))
+
+
+def test_rows_of_an_mx_matrix():
+    w = P.mx_quantize(gauss(1, 48, 200), "fp4")
+    t = P.mx_quantize(gauss(2, 40, 200), "fp8")
+    part = P.MxTensor(t.codes[3:20], t.scales[:, 3:20].contiguous(), "fp8", 200)
+    assert torch.equal(P.mx_dequantize(part), P.mx_dequantize(t)[3:20])
+    assert torch.equal(P.mx_linear(part, w), P.mx_linear(t, w)[3:20])
+    assert torch.equal(P.mx_linear(t, P.MxTensor(w.codes[16:], w.scales[:, 16:].contiguous(), "fp4", 200)),
+                       P.mx_linear(t, w)[:, 16:])
+
+
+def test_outputs_over_inputs():
+    """What the C interface allows: Y over the residual, S over X or the residual, dX over dS."""
+    m, k, n = 90, 264, 72
+    st = torch.cuda.current_stream().cuda_stream
+    L = P.lib
+    for rows in (90, 7):
+        x, w = gauss(1, rows, k).bfloat16(), P.mx_quantize(gauss(2, n, k), "fp4")
+        for a in (x, P.mx_quantize(x, "fp8")):
+            r = gauss(3, rows, n).bfloat16()
+            want = P.mx_linear(a, w, activation="silu", residual=r)
+            kind = "fp8" if isinstance(a, P.MxTensor) else P.BF16
+            need = P.mx_linear_workspace_size(rows, n, k, kind, P.BF16)
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=DEV)
+            rest = (rows, k, w.codes.data_ptr(), w.scales.data_ptr(), n, None, 0, 4, r.data_ptr(), r.data_ptr(), P.BF16,
+                    None, ws.data_ptr(), ws.numel(), st)
+            if kind == "fp8":
+                assert L.gptq_mx_linear_mx(a.codes.data_ptr(), a.scales.data_ptr(), 0, *rest) == 0
+            else:
+                assert L.gptq_mx_linear(a.data_ptr(), kind, *rest) == 0
+            assert torch.equal(r, want)
+    for m, d in ((3, 100), (300, 4096), (2, 40000)):
+        x, r, g = gauss(4, m, d).bfloat16(), gauss(5, m, d).bfloat16(), gauss(6, d).bfloat16()
+        y, s = P.rms_norm(x, g, residual=r)
+        for over in (0, 1):
+            a, b, out = x.clone(), r.clone(), torch.empty_like(x)
+            S = (a, b)[over]
+            assert L.gptq_rms_norm(a.data_ptr(), b.data_ptr(), g.data_ptr(), P.BF16, m, d, 1e-6, S.data_ptr(),
+                                   out.data_ptr(), st) == 0
+            assert torch.equal(S, s) and torch.equal(out, y)
+        dx, dw = P.rms_norm_backward(y, s, g, dS=r)
+        b = r.clone()
+        ws = torch.empty(P.rms_norm_backward_workspace_size(m, d) + 256, dtype=torch.uint8, device=DEV)
+        dw2 = torch.empty_like(dw)
+        assert L.gptq_rms_norm_backward(y.data_ptr(), s.data_ptr(), g.data_ptr(), b.data_ptr(), P.BF16, m, d, 1e-6,
+                                        b.data_ptr(), dw2.data_ptr(), ws.data_ptr(), ws.numel(), st) == 0
+        assert torch.equal(b, dx) and torch.equal(dw, dw2)
 
 
 def test_no_rows_and_bias_gradients():
@@ -436,6 +497,21 @@ def test_norm(m, d, dtype, fmt):
             codes, scales = codes_of(y)
             want, byte = ref_quantize(y64, fmt)
             assert torch.equal(scales, byte.to(torch.int64)) and torch.equal(codes, want)
+
+
+def test_norm_of_very_many_rows():
+    m, d = (1 << 20) + 3, 2056                            # more rows than one launch takes
+    x = torch.empty(m, d, dtype=torch.bfloat16, device=DEV)
+    for i in range(0, m, 1 << 18):
+        x[i:i + (1 << 18)].normal_(generator=seeded_gen(i))
+    w = (1 + 0.2 * gauss(2, d)).bfloat16()
+    y, _ = P.rms_norm(x, w, format="fp8")
+    rows = torch.tensor([0, 1, 1000, (1 << 20) - 1, 1 << 20, m - 1], device=DEV)
+    v = x[rows].double()
+    want, byte = ref_quantize(v * w.double() / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6), "fp8")
+    part = P.MxTensor(y.codes[rows].contiguous(), y.scales[:, rows].contiguous(), "fp8", d)
+    codes, scales = codes_of(part)
+    assert torch.equal(scales, byte.to(torch.int64)) and torch.equal(codes, want)
 
 
 def test_norm_of_unusual_rows():

@@ -93,7 +93,7 @@ def test_sizes_and_types(call):
     (linear, dict(S=None), "NULL"), (linear, dict(C=ODD), "aligned"), (linear, dict(S=ODD2), "aligned"),
     (linear, dict(at=3), "a_dtype"), (linear, dict(act=5), "activation"), (linear, dict(act=-1), "activation"),
     (linear, dict(b=FAKE, bt=9), "bias_dtype"), (linear, dict(d_out=0), "d_out"),
-    (linear, dict(d_out=(1 << 19) + 1), "d_out"),
+    (linear, dict(d_out=(1 << 19) + 1), "d_out"), (linear, dict(m=(1 << 30) + 1), "2^30"),
     (linear_mx, dict(A=None), "NULL"), (linear_mx, dict(AS=None), "NULL"), (linear_mx, dict(fmt=2), "a_format"),
     (linear_mx, dict(A=ODD), "aligned"), (linear_mx, dict(AS=ODD2), "aligned"), (linear_mx, dict(C=ODD), "aligned"),
     (linear_mx, dict(act=9), "activation"), (linear_mx, dict(X=None), "NULL"), (linear_mx, dict(d_out=0), "d_out"),
