@@ -1055,7 +1055,21 @@ __global__ __launch_bounds__(256, MI * NJ == 16 ? 1 : 2) void fused_gemm_kernel(
                               acc[j][i0 + i][4 * q + 3]};
         // (other lanes of the wave read what this one wrote)
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (n < p.n)
+        if (p.nsplit > 1) {   // the sums as they are, a quad a lane
+            constexpr int QPR = WCOLS / 4, QROWS = 64 / QPR;
+            const int qc = 4 * (lane % QPR);
+            const int64_t nq = n0 + wn * WCOLS + qc;
+            if (nq < p.np)
+#pragma unroll 8
+                for (int at = lane / QPR; at < 64; at += QROWS) {
+                    const int64_t row = m0 + wm * 32 * MI + 32 * i0 + at;
+                    if (row >= p.m) continue;
+                    float *part = p.part + (((int64_t)split * p.layers * p.m) + row) * p.np + nq;
+#pragma unroll
+                    for (int l = 0; l < (GATED ? 2 : 1); ++l)
+                        *(f32x4 *)(part + l * p.m * p.np) = *(const f32x4 *)(out + at * EROW + l * WCOLS + qc);
+                }
+        } else if (n < p.n) {
 #pragma unroll 1
             for (int c0 = 0; c0 < 64 / RPP; c0 += R) {
                 int64_t row[R];
@@ -1077,22 +1091,9 @@ __global__ __launch_bounds__(256, MI * NJ == 16 ? 1 : 2) void fused_gemm_kernel(
                         }
                     }
                 }
-                if (p.nsplit > 1) {
-#pragma unroll
-                    for (int c = 0; c < R; ++c) {
-                        if (row[c] >= p.m) continue;
-                        float *part = p.part + (((int64_t)split * p.layers * p.m) + row[c]) * p.np + n;
-#pragma unroll
-                        for (int l = 0; l < (GATED ? 2 : 1); ++l) {
-                            const float (&v)[8] = z[l][c];
-                            *(f32x4 *)(part + l * p.m * p.np) = f32x4{v[0], v[1], v[2], v[3]};
-                            if (n + 4 < p.np) *(f32x4 *)(part + l * p.m * p.np + 4) = f32x4{v[4], v[5], v[6], v[7]};
-                        }
-                    }
-                } else {
-                    epilogue8<GATED, R>(p, col, row, ea, n, z);
-                }
+                epilogue8<GATED, R>(p, col, row, ea, n, z);
             }
+        }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (read before the next rows overwrite them)
     }
 }

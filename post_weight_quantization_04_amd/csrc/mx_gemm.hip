@@ -263,7 +263,19 @@ __global__ __launch_bounds__(256, MI * NJ == 16 ? 1 : 2) void mx_gemm_kernel(MxG
                               acc[j][i0 + i][4 * q + 3]};
         // (other lanes of the wave read what this one wrote)
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (n < p.n)
+        if (p.nsplit > 1) {   // the sums as they are, a quad a lane
+            constexpr int QPR = COLS / 4, QROWS = 64 / QPR;
+            const int qc = 4 * (lane % QPR);
+            const int64_t nq = n0 + wn * COLS + qc;
+            if (nq < p.np)
+#pragma unroll 8
+                for (int at = lane / QPR; at < 64; at += QROWS) {
+                    const int64_t row = m0 + wm * 32 * MI + 32 * i0 + at;
+                    if (row < p.m)
+                        *(f32x4 *)(p.part + ((int64_t)split * p.m + row) * p.np + nq) =
+                            *(const f32x4 *)(out + at * EROW + qc);
+                }
+        } else if (n < p.n) {
 #pragma unroll 1
             for (int c0 = 0; c0 < 64 / RPP; c0 += R) {
                 int64_t row[R];
@@ -279,18 +291,9 @@ __global__ __launch_bounds__(256, MI * NJ == 16 ? 1 : 2) void mx_gemm_kernel(MxG
                         z[c][4 + e] = z1[e];
                     }
                 }
-                if (p.nsplit > 1) {
-#pragma unroll
-                    for (int c = 0; c < R; ++c) {
-                        if (row[c] >= p.m) continue;
-                        float *part = p.part + ((int64_t)split * p.m + row[c]) * p.np + n;
-                        *(f32x4 *)part = f32x4{z[c][0], z[c][1], z[c][2], z[c][3]};
-                        *(f32x4 *)(part + 4) = f32x4{z[c][4], z[c][5], z[c][6], z[c][7]};
-                    }
-                } else {
-                    mx_epilogue(p.out, p.m, row, n, bias, z);
-                }
+                mx_epilogue(p.out, p.m, row, n, bias, z);
             }
+        }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (read before the next rows overwrite them)
     }
 }
