@@ -10,11 +10,11 @@
 // A layer's dequantization costs d_out d_in elements of traffic, the product
 // m times as many multiplications: from about a hundred rows on the products
 // dominate, and the inner loop then carries neither code extraction nor group
-// scales.  Measured: the product 1.19 PFLOP/s for the pair 28672 x 8192 with
-// 2048 rows (1.62 ms), 1.2-1.27 for K = 22016 and 4096 x 4096 outputs (0.58-0.62
-// ms), 1.0 where the last tiles leave CUs idle (pair 11008 x 4096, 4096 rows:
-// 0.74 ms); matrix cores busy 62-63% of cycles at a clock of 1.4-1.7 GHz, no
-// LDS conflicts.  A large library product reaches 1.31-1.42 on the same card.
+// scales.  Measured: the product 1.22 PFLOP/s for the pair 28672 x 8192 with
+// 2048 rows (1.58 ms), 1.25 for K = 22016 and 4096 x 4096 outputs (0.59 ms), 1.05
+// where the last tiles leave CUs idle (pair 11008 x 4096, 4096 rows: 0.70 ms);
+// matrix cores busy 62-63% of cycles at a clock of 1.4-1.7 GHz, no LDS conflicts.
+// A large library product reaches 1.31-1.42 on the same card.
 // The dequantized weights are written at 2.6-4.0 TB/s (pair 28672 x 8192: 940
 // MB in 287 us).
 //
