@@ -143,7 +143,7 @@ __device__ __forceinline__ void mx_bias8(const MxEpilogue &p, int64_t n, float (
 MxEpilogue mx_epilogue_of(const MxLinear &a);
 bool mx_skinny_takes(int64_t m, int64_t d_out, int64_t d_in, int kind);
 hipError_t mx_skinny_launch(const MxLinear &a, hipStream_t st);
-bool mx_skinny_backward_takes(const FusedShape &s);
+bool mx_skinny_backward_takes(const FusedShape &s, int act);
 size_t mx_skinny_backward_ws(const FusedShape &s);
 hipError_t mx_skinny_backward_launch(const FusedBackward &a, hipStream_t st);
 size_t mx_gemm_ws(int64_t m, int64_t d_out, int64_t d_in);

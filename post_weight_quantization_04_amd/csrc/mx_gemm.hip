@@ -437,12 +437,14 @@ hipError_t mx_linear_launch(const MxLinear &a, hipStream_t st) {
 
 size_t mx_linear_backward_ws(const FusedShape &s) {
     if (s.m == 0) return 0;
-    return mx_skinny_backward_takes(s) ? mx_skinny_backward_ws(s) : dense_backward_ws(s);
+    // (the size is asked for without the activation, on which the form may depend)
+    const bool with = mx_skinny_backward_takes(s, 1), without = mx_skinny_backward_takes(s, 0);
+    return std::max(with || without ? mx_skinny_backward_ws(s) : 0, with && without ? 0 : dense_backward_ws(s));
 }
 
 hipError_t mx_linear_backward_launch(const FusedBackward &a, hipStream_t st) {
     if (a.s.m == 0) return fused_backward_launch(a, st);   // (zero bias gradients)
-    return mx_skinny_backward_takes(a.s) ? mx_skinny_backward_launch(a, st) : dense_backward_launch(a, st);
+    return mx_skinny_backward_takes(a.s, a.act) ? mx_skinny_backward_launch(a, st) : dense_backward_launch(a, st);
 }
 
 }  // namespace gptq

@@ -439,7 +439,8 @@ hipError_t launch_backward(const SkinnyBack &p, hipStream_t st) {
     const dim3 grid((unsigned)mx_steps(p.d_in), (unsigned)p.nsplit);
     switch (cdiv(p.m, 16)) {
         case 1: mx_skinny_backward_kernel<TERMS, 1><<<grid, 64 * SK_WAVES, 0, st>>>(p); break;
-        default: mx_skinny_backward_kernel<TERMS, 2><<<grid, 64 * SK_WAVES, 0, st>>>(p); break;
+        case 2: mx_skinny_backward_kernel<TERMS, 2><<<grid, 64 * SK_WAVES, 0, st>>>(p); break;
+        default: mx_skinny_backward_kernel<TERMS, 4><<<grid, 64 * SK_WAVES, 0, st>>>(p); break;
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -489,7 +490,17 @@ hipError_t mx_skinny_launch(const MxLinear &a, hipStream_t st) {
     }
 }
 
-bool mx_skinny_backward_takes(const FusedShape &s) { return s.m <= 32; }
+// Few rows, us a call, this form / the dense one, with SiLU: bf16 32 rows 4096 x 4096
+// 22 / 31, 4096 x 11008 39 / 55; 64 rows 2048 x 2048 17 / 24, 8192 x 1024 21 / 34, but
+// 4096 x 4096 33 / 30 and 4096 x 11008 66 / 57: every group of columns forms dZ again,
+// which costs most there and little without an activation (bf16 25 / 30, 39 / 56).  f32
+// with bias gradients: 32 rows 25 / 39, 48 / 76; 64 rows 2048 x 2048 22 / 32, 8192 x 1024
+// 26 / 46, 4096 x 4096 42 / 39; with few outputs there are few ranges and so few groups:
+// 333 x 1000 bf16 22 / 18, 1000 x 1000 16 / 19.
+bool mx_skinny_backward_takes(const FusedShape &s, int act) {
+    if (s.m <= 32) return true;
+    return s.m <= 64 && ((s.d_out >= 768 && s.d_out * s.d_in <= (1 << 23)) || (!act && s.in_bf16));
+}
 size_t mx_skinny_backward_ws(const FusedShape &s) {
     return align256((size_t)back_splits(s.d_out, s.d_in) * s.m * mx_steps(s.d_in) * MX_PAD * sizeof(float));
 }

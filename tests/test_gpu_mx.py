@@ -306,7 +306,10 @@ def test_fp8_activations_of_wide_range_in_fp32(m):
 
 
 BACK = [(1, 48, 256, "none", False), (7, 333, 1000, "silu", True), (65, 100, 31, "gelu", True),
-        (300, 333, 1000, "relu", True), (513, 1100, 520, "gelu_tanh", False), (130, 257, 129, "silu", True)]
+        (300, 333, 1000, "relu", True), (513, 1100, 520, "gelu_tanh", False), (130, 257, 129, "silu", True),
+        (16, 40, 300, "gelu", True), (32, 257, 1000, "silu", True), (33, 333, 1000, "silu", True),
+        (48, 1100, 257, "none", True), (64, 64, 2048, "gelu", True), (64, 2500, 4100, "silu", True),
+        (50, 2500, 4100, "none", True)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
