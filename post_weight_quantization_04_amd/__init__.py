@@ -27,6 +27,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from operator import attrgetter
 
 __all__ = [
     "GptqError", "lib", "hessian_accumulate", "hessian_workspace_size", "quantize_layer",
@@ -690,18 +691,20 @@ class MxTensor:
     """A matrix [rows, d] in blocks of 32 columns that share a power of two
     (gptq.h has the layout): codes uint8 [rows, row bytes], scales uint8
     [ceil(d / 128), rows, 4], format "fp8" (e4m3) or "fp4" (e2m1)."""
-    __slots__ = ("_codes", "_scales", "_buffer", "rows", "format", "d")
+    __slots__ = ("_codes", "_scales", "_buffer", "_rows", "_format", "_d")
+    # (what the kernels index by stays what the memory was laid out for)
+    rows, format, d = (property(attrgetter(name)) for name in ("_rows", "_format", "_d"))
 
     def __init__(self, codes, scales, format, d):
         self._codes, self._scales, self._buffer = codes, scales, None
-        self.rows, self.format, self.d = codes.shape[0], format, d
+        self._rows, self._format, self._d = codes.shape[0], format, d
 
     @classmethod
     def _empty(cls, rows, d, format, device):
         """One allocation, codes before scales; its two views are made when asked for."""
         t = cls.__new__(cls)
         t._codes = t._scales = None
-        t.rows, t.format, t.d = rows, format, d
+        t._rows, t._format, t._d = rows, format, d
         steps = -(-d // 128)
         t._buffer = _TORCH.empty_strided((rows * steps * (68 if format == "fp4" else 132),), (1,),
                                          dtype=_TORCH.uint8, device=device)

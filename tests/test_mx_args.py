@@ -168,3 +168,15 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError, match="fp4"):
         P.mx_linear(x, P.MxTensor(t.codes, t.scales, "fp8", 64))
     assert t.shape == (4, 64)
+
+
+def test_an_mx_tensor_keeps_its_shape():
+    """Sizes and format cannot be changed behind the memory that was laid out for them; copies keep them."""
+    torch = pytest.importorskip("torch")
+    import copy
+    t = P.MxTensor(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(1, 4, 4, dtype=torch.uint8), "fp4", 64)
+    for name, value in (("rows", 400), ("d", 6400), ("format", "fp8")):
+        with pytest.raises(AttributeError):
+            setattr(t, name, value)
+    c = copy.deepcopy(t)
+    assert (c.rows, c.d, c.format, c.shape) == (t.rows, t.d, t.format, t.shape) == (4, 64, "fp4", (4, 64))
