@@ -4,7 +4,7 @@
 //
 //   S = X + residual, rounded to its type;  r = (mean_j S_j^2 + eps)^(-1/2)
 //   Y_j = S_j r w_j
-//   c = mean_j dY_j w_j S_j;  dX_j = r (w_j dY_j - S_j r^2 c) + dS_j
+//   c = mean_j dY_j w_j S_j;  dX_j = r (w_j dY_j - (S_j r) (r c)) + dS_j
 //   dw_j = sum over rows of dY_j S_j r
 //
 // S is the stream as it is stored, so that the backward pass, and a norm of
@@ -140,7 +140,7 @@ struct NormBackArgs {
     int vec;
     double inv_d;
     float *part;                // [groups][d] the groups' sums of dw, or NULL
-    float *stats;               // [m][2] r and r^2 c of wide rows
+    double *stats;              // [m][2] r and r c of wide rows
     int64_t row0;               // the first row whose factors a launch finds
     int64_t groups;
 };
@@ -157,13 +157,14 @@ struct Raw8 {
             for (int i = 0; i < (BF16 ? 1 : 2); ++i) q[i] = in ? src[i] : u32x4{0u, 0u, 0u, 0u};
         } else {   // (clamped and selected: a branch around each load would wait for each)
             unsigned v[8];
-#pragma unroll
+            const char *base = (const char *)x + row * d * (BF16 ? 2 : 4);   // (and 32-bit offsets: eight
+#pragma unroll                                                              //  addresses cost 16 registers)
             for (int e = 0; e < 8; ++e) {
-                const int64_t o = row * d + std::min(k + e, d - 1);
+                const unsigned o = std::min((unsigned)k + e, (unsigned)d - 1u);
                 if constexpr (BF16)
-                    v[e] = ((const uint16_t *)x)[o];
+                    v[e] = ((const uint16_t *)base)[o];
                 else
-                    v[e] = ((const unsigned *)x)[o];
+                    v[e] = ((const unsigned *)base)[o];
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = k + e < d ? v[e] : 0u;
@@ -177,6 +178,10 @@ struct Raw8 {
                 }
             }
         }
+    }
+    __device__ __forceinline__ void opaque() {   // nothing computed from it is kept from before
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) asm volatile("" : "+v"(q[i]));
     }
     __device__ __forceinline__ float at(int e) const {
         if constexpr (BF16)
@@ -194,29 +199,29 @@ __device__ __forceinline__ void norm_sums(const Raw8<BF16> &s, const Raw8<BF16> 
     for (int e = 0; e < 8; ++e) {
         const double v = (double)s.at(e);
         sq += v * v;
-        if constexpr (BF16)   // (dY w of bf16 values is exact in fp32)
-            dot += v * (double)(g.at(e) * w.at(e));
-        else
-            dot += v * ((double)g.at(e) * (double)w.at(e));
+        dot += v * ((double)g.at(e) * (double)w.at(e));
     }
 }
-// eight columns of a row: dX, and dw's terms
+// Eight columns of a row: dX = r (w dY - (S r) (r c)) + dS, and dw's terms.  In 64
+// bits but for dS's addition: of rows of very large or small values r, r^2 c or w dY
+// leave fp32's range where dX does not.  (us a call, in fp32 throughout / so: bf16 4096 x
+// 4096 30.0 / 30.6, 64000 x 128 36 / 43; f32 2048 x 8192 51 / 54, 4096 x 4099 159 / 186.)
 template <bool BF16>
-__device__ __forceinline__ void norm_leave(const NormBackArgs &p, int64_t row, int64_t k, float r, float f,
+__device__ __forceinline__ void norm_leave(const NormBackArgs &p, int64_t row, int64_t k, double r, double rc,
                                            const Raw8<BF16> &s, const Raw8<BF16> &g, const Raw8<BF16> &w,
                                            const Raw8<BF16> &t, float (&dw)[8]) {
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        x[e] = r * (g.at(e) * w.at(e) - s.at(e) * f) + t.at(e);
-        dw[e] += g.at(e) * (s.at(e) * r);
+        const double n = (double)s.at(e) * r;
+        x[e] = (float)(r * ((double)g.at(e) * (double)w.at(e) - n * rc)) + t.at(e);
+        dw[e] += g.at(e) * (float)n;
     }
     put8(p.a.dX, row, p.a.d, k, BF16, p.vec, x);
 }
-__device__ __forceinline__ void norm_factors(const NormBackArgs &p, double sq, double dot, float &r, float &f) {
-    const double rd = 1.0 / sqrt(sq * p.inv_d + p.a.eps);
-    r = (float)rd;
-    f = (float)(rd * rd * (dot * p.inv_d));
+__device__ __forceinline__ void norm_factors(const NormBackArgs &p, double sq, double dot, double &r, double &rc) {
+    r = 1.0 / sqrt(sq * p.inv_d + p.a.eps);
+    rc = r * (dot * p.inv_d);
 }
 __device__ __forceinline__ void norm_put_sums(const NormBackArgs &p, int64_t group, int64_t k, const float (&dw)[8]) {
     if (p.part && k < p.a.d) put8(p.part, group, p.a.d, k, 0, p.a.d % 4 == 0 && k + 8 <= p.a.d, dw);
@@ -231,7 +236,7 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_backward_ke
     constexpr int PER = WPR < 4 ? 4 / WPR : 1;   // groups of a block
     __shared__ double lds[2][PER][2][WPR];
     const int sub = threadIdx.x / (64 * WPR), tid = threadIdx.x % (64 * WPR);
-    const int64_t group = (int64_t)blockIdx.x * PER + sub, d = p.a.d, k = 8 * tid;
+    const int64_t group = (int64_t)blockIdx.x * PER + (PER > 1 ? sub : 0), d = p.a.d, k = 8 * tid;
     Raw8<BF16> w, s, g, t, s1, g1, t1;
     w.load(p.a.weight, 0, d, k, p.vec);
     auto load = [&](int64_t row) {
@@ -247,10 +252,11 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_backward_ke
     int turn = 0;
     // (every group of a block makes the same number of turns: they meet at the barriers)
     for (int64_t first = (int64_t)blockIdx.x * PER; first < p.a.m; first += p.groups, turn ^= 1) {
-        const int64_t row = first + sub;
+        const int64_t row = first + (PER > 1 ? sub : 0);
         s = s1;
         g = g1;
         t = t1;
+        w.opaque();   // (its 64-bit values, kept over the loop, would cost a third of the registers)
         load(row + p.groups);
         double sq = 0.0, dot = 0.0;
         norm_sums(s, g, w, sq, dot);
@@ -273,9 +279,9 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_backward_ke
                 dot += lds[turn][sub][1][i];
             }
         }
-        float r, f;
-        norm_factors(p, sq, dot, r, f);
-        if (row < p.a.m && k < d) norm_leave(p, row, k, r, f, s, g, w, t, dw);
+        double r, rc;
+        norm_factors(p, sq, dot, r, rc);
+        if (row < p.a.m && k < d) norm_leave(p, row, k, r, rc, s, g, w, t, dw);
     }
     if (group < p.groups) norm_put_sums(p, group, k, dw);
 }
@@ -346,15 +352,15 @@ __global__ __launch_bounds__(64 * SMALL_ROWS) void norm_backward_small_kernel(No
             sq += __shfl_xor(sq, o);
             dot += __shfl_xor(dot, o);
         }
-        float r, f;
-        norm_factors(p, sq, dot, r, f);
+        double r, rc;
+        norm_factors(p, sq, dot, r, rc);
         s.load(p.a.S, row, d, k0, p.vec);
         g.load(p.a.dY, row, d, k0, p.vec);
         w.load(p.a.weight, 0, d, k0, p.vec);
 #pragma unroll
         for (int i = 0; i < (BF16 ? 1 : 2); ++i) t.q[i] = u32x4{0u, 0u, 0u, 0u};
         if (p.a.dS) t.load(p.a.dS, row, d, k0, p.vec);
-        if (k0 < d) norm_leave(p, row, k0, r, f, s, g, w, t, dw);
+        if (k0 < d) norm_leave(p, row, k0, r, rc, s, g, w, t, dw);
     }
     if (!p.a.dweight) return;
 #pragma unroll
@@ -485,7 +491,7 @@ size_t rms_norm_backward_ws(int64_t m, int64_t d) {
     if (m == 0) return 0;
     const BackPlan p = back_plan(m, d);
     if (p.wpr < 0) return 0;
-    return align256((size_t)p.groups * d * sizeof(float)) + (p.wpr ? 0 : align256((size_t)m * 2 * sizeof(float)));
+    return align256((size_t)p.groups * d * sizeof(float)) + (p.wpr ? 0 : align256((size_t)m * 2 * sizeof(double)));
 }
 
 hipError_t rms_norm_backward_launch(const RmsNormBackward &a, hipStream_t st) {
@@ -506,7 +512,7 @@ hipError_t rms_norm_backward_launch(const RmsNormBackward &a, hipStream_t st) {
         }
         p.groups = plan.groups;
         p.part = a.dweight ? (float *)a.ws : nullptr;
-        p.stats = (float *)(a.ws + align256((size_t)p.groups * a.d * sizeof(float)));
+        p.stats = (double *)(a.ws + align256((size_t)p.groups * a.d * sizeof(float)));
         hipError_t e;
         if (p.vec)
             e = a.bf16 ? launch_backward<true, true>(p, plan.wpr, st) : launch_backward<false, true>(p, plan.wpr, st);

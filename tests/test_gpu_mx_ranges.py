@@ -1,0 +1,47 @@
+"""GPU tests of the MX operators and the norm at the ends of their range, and
+of the product forms that only large or particular shapes select.
+
+Tolerances as in test_gpu_mx.py unless a test states its own.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_mx import DEV, DT, F64, P, gauss, say  # noqa: E402
+
+
+# ---------------------------------------------------------------------------
+# the norm's backward pass
+# ---------------------------------------------------------------------------
+# sizes of a row's S and dY, such that r dY w stays inside fp32 (and bf16)
+SIZES = [(1e38, 1e10), (1e30, 1e-5), (1.0, 1.0), (1e-25, 1e-10), (1e-36, 1e-12), (3e37, 1e25), (1e-40, 1e-20)]
+
+
+@pytest.mark.parametrize("wsize", [1.0, 1e-20, 1e20])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,d", [(9, 1000), (14, 96), (300, 520), (260, 8192), (37, 1407), (20, 9000), (7, 33000)])
+def test_norm_backward_at_the_ends_of_the_range(m, d, dtype, wsize):
+    """Rows whose factor r, r^2, or whose products dY w leave fp32 although the results do not; eps = 0.
+
+    In 64 bits, with a relative error far below 2^-40 of the terms; dX is rounded to fp32, and from
+    there to bf16, dw's groups to fp32 and their sum again."""
+    say("norm backward range", m, d, dtype, wsize)
+    size = torch.tensor(SIZES, dtype=F64, device=DEV)[torch.arange(m, device=DEV) % len(SIZES)]
+    # (clamped: no value beyond the type's largest, and of subnormal rows some that are not zero)
+    s = (gauss(d, m, d).double().clamp(-3, 3) * size[:, :1]).to(DT[dtype])
+    w = ((1 + 0.2 * gauss(2, d)).double() * wsize).to(DT[dtype])
+    dy = (gauss(3, m, d).double() * size[:, 1:] * (1e-8 if wsize > 1 else 1)).to(DT[dtype])
+    v, g = s.double(), dy.double()
+    r = 1 / torch.sqrt((v * v).mean(1, keepdim=True))
+    n, gw = v * r, g * w.double()
+    want = r * (gw - n * (gw * n).mean(1, keepdim=True))
+    assert torch.isfinite(want).all() and float(want.abs().max()) < 1e38
+    size = r * (gw.abs() + n.abs() * (gw * n).abs().mean(1, keepdim=True))
+    step = {"bf16": 2.0 ** -8 + 2.0 ** -23, "f32": 2.0 ** -24}[dtype]
+    least = {"bf16": 2.0 ** -134 + 2.0 ** -150, "f32": 2.0 ** -150}[dtype]
+    dx, dw = P.rms_norm_backward(dy, s, w, eps=0.0)
+    e = 2.0 ** -40 * size
+    assert ((dx.double() - want).abs() <= e + step * (want.abs() + e) + least).all()
+    terms = g * n
+    assert ((dw.double() - terms.sum(0)).abs() <= 2.0 ** -22 * terms.abs().sum(0)).all()
