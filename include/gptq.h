@@ -465,8 +465,9 @@ GPTQ_API gptq_status gptq_mx_linear_backward(const void *dY, gptq_dtype dy_dtype
  *   dweight  fp32 [d], overwritten; NULL: not formed
  * Row sums, and dX but for dS, in 64 bits; a plain Y is rounded once from there, dX
  * to fp32, where dS is added, and then to dtype: rows of any finite size have the
- * gradients that fp32 holds.  dweight is summed in fp32.  All results are
- * deterministic.  No other output may overlap an input or another output.
+ * gradients that fp32 holds.  dweight is summed in 64 bits (work groups' sums are
+ * stored in fp32 between).  All results are deterministic.  No other output may
+ * overlap an input or another output.
  * Limits: d in [1, 2^19], m in [0, 2^31 - 1], eps finite and >= 0.  m == 0 leaves
  * dweight zero and is a no-op otherwise.  workspace (backward):
  * gptq_rms_norm_backward_workspace_size bytes, 256-byte aligned, in any state.

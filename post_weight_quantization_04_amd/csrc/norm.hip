@@ -209,13 +209,13 @@ __device__ __forceinline__ void norm_sums(const Raw8<BF16> &s, const Raw8<BF16> 
 template <bool BF16>
 __device__ __forceinline__ void norm_leave(const NormBackArgs &p, int64_t row, int64_t k, double r, double rc,
                                            const Raw8<BF16> &s, const Raw8<BF16> &g, const Raw8<BF16> &w,
-                                           const Raw8<BF16> &t, float (&dw)[8]) {
+                                           const Raw8<BF16> &t, double (&dw)[8]) {
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const double n = (double)s.at(e) * r;
         x[e] = (float)(r * ((double)g.at(e) * (double)w.at(e) - n * rc)) + t.at(e);
-        dw[e] += g.at(e) * (float)n;
+        dw[e] += (double)g.at(e) * n;   // (in fp32 a long chain of rows would lose its small terms)
     }
     put8(p.a.dX, row, p.a.d, k, BF16, p.vec, x);
 }
@@ -223,8 +223,12 @@ __device__ __forceinline__ void norm_factors(const NormBackArgs &p, double sq, d
     r = 1.0 / sqrt(sq * p.inv_d + p.a.eps);
     rc = r * (dot * p.inv_d);
 }
-__device__ __forceinline__ void norm_put_sums(const NormBackArgs &p, int64_t group, int64_t k, const float (&dw)[8]) {
-    if (p.part && k < p.a.d) put8(p.part, group, p.a.d, k, 0, p.a.d % 4 == 0 && k + 8 <= p.a.d, dw);
+__device__ __forceinline__ void norm_put_sums(const NormBackArgs &p, int64_t group, int64_t k, const double (&dw)[8]) {
+    if (!p.part || k >= p.a.d) return;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (float)dw[e];
+    put8(p.part, group, p.a.d, k, 0, p.a.d % 4 == 0 && k + 8 <= p.a.d, v);
 }
 
 // Rows that fit a group of WPR waves, eight columns a thread: read once.  A
@@ -247,7 +251,7 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_backward_ke
     };
 #pragma unroll
     for (int i = 0; i < (BF16 ? 1 : 2); ++i) t1.q[i] = u32x4{0u, 0u, 0u, 0u};
-    float dw[8] = {};
+    double dw[8] = {};
     load(group);
     int turn = 0;
     // (every group of a block makes the same number of turns: they meet at the barriers)
@@ -312,7 +316,7 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(NormBackArgs p) {
     if (k >= d) return;
     Raw8<BF16> w;
     w.load(p.a.weight, 0, d, k, p.vec);
-    float dw[8] = {};
+    double dw[8] = {};
 #pragma unroll 2
     for (int64_t row = group; row < p.a.m; row += p.groups) {
         Raw8<BF16> s, g, t;
@@ -337,7 +341,7 @@ __global__ __launch_bounds__(64 * SMALL_ROWS) void norm_backward_small_kernel(No
     __shared__ float sums[SMALL_ROWS][512];
     const int lane = threadIdx.x & 63, row = threadIdx.x >> 6;
     const int64_t d = p.a.d, k0 = (int64_t)blockIdx.x * 512 + 8 * lane;
-    float dw[8] = {};
+    double dw[8] = {};
     if (row < p.a.m) {
         Raw8<BF16> s, g, w, t;
         double sq = 0.0, dot = 0.0;
@@ -364,7 +368,7 @@ __global__ __launch_bounds__(64 * SMALL_ROWS) void norm_backward_small_kernel(No
     }
     if (!p.a.dweight) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[row][8 * lane + e] = dw[e];
+    for (int e = 0; e < 8; ++e) sums[row][8 * lane + e] = (float)dw[e];
     __syncthreads();
     const int64_t k = (int64_t)blockIdx.x * 512 + threadIdx.x;
     if (threadIdx.x >= 512 || k >= d) return;

@@ -45,3 +45,19 @@ def test_norm_backward_at_the_ends_of_the_range(m, d, dtype, wsize):
     assert ((dx.double() - want).abs() <= e + step * (want.abs() + e) + least).all()
     terms = g * n
     assert ((dw.double() - terms.sum(0)).abs() <= 2.0 ** -22 * terms.abs().sum(0)).all()
+
+
+@pytest.mark.parametrize("m,d", [(51456, 8192), (10251, 40000)])
+def test_norm_weight_gradients_of_many_rows(m, d):
+    """dw where a column's later terms are 2^-25 of the first ones: a chain of fp32 additions would lose each.
+
+    Terms are exact; the groups' sums and the result are rounded to fp32: 2^-23 of the sum, as all are positive."""
+    first, small = 256, 2.0 ** -25
+    s = torch.ones(m, d, dtype=torch.bfloat16, device=DEV)
+    dy = torch.ones(m, d, dtype=torch.bfloat16, device=DEV)
+    column = (1 + (torch.arange(d, device=DEV) % 8) / 8).bfloat16()
+    dy[first:] = column * small
+    w = torch.ones(d, dtype=torch.bfloat16, device=DEV)
+    _, dw = P.rms_norm_backward(dy, s, w, eps=0.0)
+    want = first + (m - first) * small * column.double()
+    assert ((dw.double() - want).abs() <= 2.0 ** -23 * want).all()
