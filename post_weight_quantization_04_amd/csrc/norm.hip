@@ -45,7 +45,6 @@ struct NormArgs {
     int vec;                    // whole aligned pieces of eight
     int64_t padded, row_bytes;  // columns that are written (MX: whole 128), code bytes of a row
     int64_t row0;               // the launch's first row
-    double inv_d;
 };
 
 __device__ __forceinline__ void norm_load(const NormArgs &p, int64_t row, int64_t k, float (&v)[8]) {
@@ -71,30 +70,45 @@ __device__ __forceinline__ void put8(void *x, int64_t row, int64_t d, int64_t k,
             if (k + e < d) fz_st(x, o + e, v[e], bf16);
     }
 }
-// Y = S w r in 64 bits (S w is exact there), rounded once to its type or its
-// grid: a value next to a border of a grid of 8 or 4 bits falls on the side
-// the definition says.  The 64-bit operations hide behind the memory.
-__device__ __forceinline__ void norm_store(const NormArgs &p, int64_t row, int64_t k, double r, const float (&v)[8]) {
+// a / q with r = 1 / q: the product's last bits mended by what it leaves of a, so
+// that exact quotients come out as they are (S = 49 in a row of 49s: 49 r is 1 -
+// 2^-53, which on a grid of 8 or 4 bits is another value than 1).  Zeros, infinities
+// and NaN leave nothing to mend by.
+__device__ __forceinline__ double norm_quotient(double a, double q, double r) {
+    constexpr int FINITE = 0x198;   // normal and subnormal, either sign
+    const double y = a * r, rest = fma(-y, q, a);
+    return __builtin_amdgcn_class(rest, FINITE) ? fma(rest, r, y) : y;
+}
+// Y = S w / q, q = 1 / r, in 64 bits (S w is exact there), rounded once to its type
+// or its grid: a value on or next to a border of a grid of 8 or 4 bits falls on the
+// side the definition says.  The 64-bit operations hide behind the memory, but for
+// the quotient's (us with an fp8 output and a residual, S w r / so: 2048 x 8192 26.6 /
+// 28.5, 64000 x 128 13.0 / 14.3).
+template <bool MX>
+__device__ __forceinline__ void norm_store(const NormArgs &p, int64_t row, int64_t k, double q, double r,
+                                           const float (&v)[8]) {
     float w[8], y[8];
     mx_ld8(p.a.weight, 0, p.a.d, k, p.a.bf16, p.vec, w);
+    if constexpr (!MX) {   // (one 64-bit step off or not, a value rounds to the nearest of its type)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = mx_odd((double)v[e] * (double)w[e] * r);
-    if (p.a.Y) {
-        if (!p.a.bf16) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = (float)((double)v[e] * (double)w[e] * r);
+        for (int e = 0; e < 8; ++e) {
+            const double z = (double)v[e] * (double)w[e] * r;
+            y[e] = p.a.bf16 ? mx_odd(z) : (float)z;
         }
         put8(p.a.Y, row, p.a.d, k, p.a.bf16, p.vec, y);
-    } else if (p.a.fmt == MX_FP8) {
-        mx_put8<MX_FP8>(y, p.a.m, row, k >> 3, p.row_bytes, p.a.codes, p.a.scales);
     } else {
-        mx_put8<MX_FP4>(y, p.a.m, row, k >> 3, p.row_bytes, p.a.codes, p.a.scales);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = mx_odd(norm_quotient((double)v[e] * (double)w[e], q, r));
+        if (p.a.fmt == MX_FP8)
+            mx_put8<MX_FP8>(y, p.a.m, row, k >> 3, p.row_bytes, p.a.codes, p.a.scales);
+        else
+            mx_put8<MX_FP4>(y, p.a.m, row, k >> 3, p.row_bytes, p.a.codes, p.a.scales);
     }
 }
 
 // LANES threads per row, each NC pieces of eight columns held in registers
 // between the two sweeps; columns beyond them are formed again from the inputs
-template <int LANES, int NC, bool VEC>
+template <int LANES, int NC, bool VEC, bool MX>
 __global__ __launch_bounds__(std::max(LANES, 256)) void rms_norm_kernel(NormArgs p) {
     p.vec = VEC;   // (known here: the other way of loading costs registers)
     constexpr int STEP = 8 * LANES, ROWS = std::max(1, 256 / LANES);
@@ -118,17 +132,17 @@ __global__ __launch_bounds__(std::max(LANES, 256)) void rms_norm_kernel(NormArgs
         norm_load(p, row, k, x);
         take(k, x);
     }
-    const double r = 1.0 / sqrt(row_sum<LANES>(sum, lds) * p.inv_d + p.a.eps);
+    const double q = sqrt(row_sum<LANES>(sum, lds) / (double)p.a.d + p.a.eps), r = 1.0 / q;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-        if (k0 + c * STEP < p.padded) norm_store(p, row, k0 + c * STEP, r, v[c]);
+        if (k0 + c * STEP < p.padded) norm_store<MX>(p, row, k0 + c * STEP, q, r, v[c]);
     for (int64_t k = k0 + NC * STEP; k < p.padded; k += STEP) {
         float x[8];
         if (p.a.S)   // (the inputs may be S itself, which holds the sums by now)
             mx_ld8(p.a.S, row, p.a.d, k, p.a.bf16, p.vec, x);
         else
             norm_load(p, row, k, x);
-        norm_store(p, row, k, r, x);
+        norm_store<MX>(p, row, k, q, r, x);
     }
 }
 
@@ -415,10 +429,14 @@ hipError_t launch_norm(NormArgs p, hipStream_t st) {
     constexpr int ROWS = std::max(1, 256 / LANES), THREADS = std::max(LANES, 256);
     for (p.row0 = 0; p.row0 < p.a.m; p.row0 += MAX_BLOCKS * ROWS) {
         const unsigned blocks = (unsigned)std::min(cdiv(p.a.m - p.row0, ROWS), MAX_BLOCKS);
-        if (p.vec)
-            rms_norm_kernel<LANES, NC, true><<<blocks, THREADS, 0, st>>>(p);
+        if (p.a.Y && p.vec)
+            rms_norm_kernel<LANES, NC, true, false><<<blocks, THREADS, 0, st>>>(p);
+        else if (p.a.Y)
+            rms_norm_kernel<LANES, NC, false, false><<<blocks, THREADS, 0, st>>>(p);
+        else if (p.vec)
+            rms_norm_kernel<LANES, NC, true, true><<<blocks, THREADS, 0, st>>>(p);
         else
-            rms_norm_kernel<LANES, NC, false><<<blocks, THREADS, 0, st>>>(p);
+            rms_norm_kernel<LANES, NC, false, true><<<blocks, THREADS, 0, st>>>(p);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -476,7 +494,6 @@ hipError_t rms_norm_launch(const RmsNorm &a, hipStream_t st) {
             (!a.S || aligned16(a.S)) && (!a.Y || aligned16(a.Y));
     p.padded = a.Y ? a.d : mx_steps(a.d) * MX_PAD;
     p.row_bytes = a.Y ? 0 : mx_row_bytes(a.d, a.fmt);
-    p.inv_d = 1.0 / (double)a.d;
     const RowPlan plan = row_plan(a.m, a.d);
     switch (plan.lanes * 8 + plan.nc) {
         case 16 * 8 + 1: return launch_norm<16, 1>(p, st);

@@ -3,12 +3,14 @@ of the product forms that only large or particular shapes select.
 
 Tolerances as in test_gpu_mx.py unless a test states its own.
 """
+from fractions import Fraction
+
 import pytest
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_mx import DEV, DT, F64, P, gauss, say  # noqa: E402
+from test_gpu_mx import DEV, DT, F64, P, codes_of, gauss, ref_quantize, say  # noqa: E402
 
 
 # ---------------------------------------------------------------------------
@@ -61,3 +63,39 @@ def test_norm_weight_gradients_of_many_rows(m, d):
     _, dw = P.rms_norm_backward(dy, s, w, eps=0.0)
     want = first + (m - first) * small * column.double()
     assert ((dw.double() - want).abs() <= 2.0 ** -23 * want).all()
+
+
+# ---------------------------------------------------------------------------
+# the norm's outputs
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", [None, "fp8", "fp4"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [1, 32, 98, 100, 1407, 4096, 9000])
+def test_norm_of_rows_with_exact_results(d, dtype, fmt):
+    """Constant rows with eps = 0: the results are the weights themselves, on the borders of the grids."""
+    m = 256
+    x = (torch.arange(m, device=DEV) + 1.0).view(m, 1).expand(m, d)
+    sign = 1 - 2 * (torch.arange(d, device=DEV) % 3 == 1).float()
+    w = torch.tensor([1.0, 2.0, 0.5, 448.0, 6.0, 0.875], device=DEV)[torch.arange(d, device=DEV) % 6]
+    y, _ = P.rms_norm((x * sign).to(DT[dtype]).contiguous(), w.to(DT[dtype]), eps=0.0, format=fmt)
+    want = (w * sign).double().expand(m, d)
+    if fmt is None:
+        assert torch.equal(y.double(), want)
+    else:
+        codes, byte = ref_quantize(want, fmt)
+        got, scales = codes_of(y)
+        assert torch.equal(scales, byte.to(torch.int64)) and torch.equal(got, codes)
+
+
+def test_norm_with_eps_of_exact_results():
+    """mean + eps a square: 3^2 + 7 = 4^2, 12^2 + 25 = 13^2, 49^2 + 200 = 51^2, 0 + 9."""
+    for value, eps, root in ((3, 7, 4), (12, 25, 13), (49, 200, 51), (0, 9, 3)):
+        x = torch.full((300, 200), float(value), device=DEV)
+        for weight in (1.0, 7.0, float(root)):
+            want = Fraction(value) * Fraction(weight) / root
+            y, _ = P.rms_norm(x, torch.full((200,), weight, device=DEV), eps=float(eps))
+            assert torch.equal(y, torch.full_like(y, float(want))), (value, weight)
+            q, _ = P.rms_norm(x, torch.full((200,), weight, device=DEV), eps=float(eps), format="fp8")
+            codes, byte = ref_quantize(torch.full((300, 200), float(want), dtype=F64), "fp8")
+            got, scales = codes_of(q)
+            assert torch.equal(scales, byte.to(torch.int64)) and torch.equal(got, codes), (value, weight)
