@@ -97,6 +97,7 @@ __device__ __forceinline__ void norm_store(const NormArgs &p, int64_t row, int64
         }
         put8(p.a.Y, row, p.a.d, k, p.a.bf16, p.vec, y);
     } else {
+        if (k >= p.a.d) r = 0.0;   // (padding, 0 whatever the row's factor is)
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = mx_odd(norm_quotient((double)v[e] * (double)w[e], q, r));
         if (p.a.fmt == MX_FP8)

@@ -99,3 +99,20 @@ def test_norm_with_eps_of_exact_results():
             codes, byte = ref_quantize(torch.full((300, 200), float(want), dtype=F64), "fp8")
             got, scales = codes_of(q)
             assert torch.equal(scales, byte.to(torch.int64)) and torch.equal(got, codes), (value, weight)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,d", [(5, 200), (300, 70), (300, 130), (3, 20010)])
+def test_padding_behind_rows_that_are_not_finite(m, d, dtype, fmt):
+    """Columns and blocks behind d have codes and scale bytes 0, whatever the row."""
+    x = gauss(1, m, d)
+    x[0] = 0                                              # with eps = 0: 0 / 0
+    x[1, 3], x[2, d - 1] = float("inf"), float("nan")
+    y, _ = P.rms_norm(x.to(DT[dtype]), (1 + 0.1 * gauss(2, d)).to(DT[dtype]), eps=0.0, format=fmt)
+    for t in (y, P.mx_quantize(x.to(DT[dtype]), fmt)):
+        codes, scales = codes_of(t)
+        assert (codes[:, d:] == 0).all() and (scales[:, -(-d // 32):] == 0).all()
+    codes, scales = codes_of(y)
+    assert (scales[0, :-(-d // 32)] == 255).all() and (scales[2, :-(-d // 32)] == 255).all()
+    assert (scales[3:] != 255).all()
