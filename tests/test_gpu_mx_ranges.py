@@ -10,7 +10,8 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_mx import DEV, DT, F64, P, codes_of, gauss, ref_quantize, say  # noqa: E402
+from test_gpu_mx import (DEV, DT, F64, HALF_STEP, P, SLOPE, act64, bounds, codes_of, gauss, ints,  # noqa: E402
+                         make_acts, ref_quantize, say, slope64, values_of)
 
 
 # ---------------------------------------------------------------------------
@@ -116,3 +117,67 @@ def test_padding_behind_rows_that_are_not_finite(m, d, dtype, fmt):
     codes, scales = codes_of(y)
     assert (scales[0, :-(-d // 32)] == 255).all() and (scales[2, :-(-d // 32)] == 255).all()
     assert (scales[3:] != 255).all()
+
+
+# ---------------------------------------------------------------------------
+# product forms that particular shapes select
+# ---------------------------------------------------------------------------
+# (m, n, k, kind, out): MX activations through tiles of 256 x 256 (at least 128 of them, 32 stages), ragged at
+# both ends, outputs 8, 4 and 1 at a time; the dense form's tiles of that size with MX weights, and with fp8
+# activations; rows up to 64 through the few-row form
+FORMS = [(2051, 3864, 4129, "fp8", "bf16"), (2051, 3860, 4129, "fp4", "f32"), (2051, 3857, 4129, "fp8", "bf16"),
+         (2051, 3857, 4129, "fp4", "bf16"), (2051, 3857, 1033, "f32", "f32"), (2051, 3860, 1033, "fp8", "f32"),
+         (2051, 3864, 1033, "bf16", "bf16"), (2051, 3857, 1033, "f32", "bf16"),
+         *((m, n, k, kind, out) for m, n, k in ((33, 2049, 1000), (64, 2500, 4100))
+           for kind in ("bf16", "f32", "fp8", "fp4") for out in ("bf16", "f32"))]
+
+
+@pytest.mark.parametrize("m,n,k,kind,out", FORMS)
+def test_forms_with_exact_operands(m, n, k, kind, out):
+    say("form, exact", m, n, k, kind, out)
+    x = ints(m * 31 + k, -2, 3, m, k)
+    w = ints(n * 17 + k, -3, 4, n, k) * torch.exp2(ints(n, -2, 3, n, 1))
+    x[:, 0] = 2.0
+    wq = P.mx_quantize(w, "fp4")
+    a, a64 = make_acts(kind, x)
+    want = a64 @ values_of(wq).t()
+    b, r = ints(1, -9, 10, n).to(DT[out]), ints(2, -9, 10, m, n).to(DT[out])
+    y = P.mx_linear(a, wq, out_dtype=DT[out])
+    assert torch.equal(y, want.float().to(DT[out]))
+    y, z = P.mx_linear(a, wq, bias=b, activation="relu", residual=r, out_dtype=DT[out], save_preact=True)
+    want = want + b.double()
+    assert torch.equal(z, want.float().to(DT[out]))
+    assert torch.equal(y, (want.clamp(min=0) + r.double()).float().to(DT[out]))
+
+
+@pytest.mark.parametrize("m,n,k,kind,out", FORMS)
+def test_forms(m, n, k, kind, out):
+    say("form", m, n, k, kind, out)
+    x = gauss(m + n, m, k) * torch.exp(gauss(k, k))
+    wq = P.mx_quantize(gauss(n * k, n, k) * 0.05, "fp4")
+    a, a64 = make_acts(kind, x)
+    w64 = values_of(wq)
+    b, r = gauss(1, n).to(DT[out]), gauss(2, m, n).to(DT[out])
+    y, z = P.mx_linear(a, wq, bias=b, activation="silu", residual=r, out_dtype=DT[out], save_preact=True)
+    z64 = a64 @ w64.t() + b.double()
+    e = bounds(kind, out, m, a64, w64, m > 32 and (kind in DT or (kind, out) == ("fp8", "f32"))) + 2.0 ** -24 * z64.abs()
+    assert ((z.double() - z64).abs() <= e + HALF_STEP[out] * (z64.abs() + e)).all()
+    y64 = act64(z64, "silu") + r.double()
+    e = SLOPE * e + 2.0 ** -20 * (z64.abs() + 1) + 2.0 ** -24 * y64.abs()
+    assert ((y.double() - y64).abs() <= e + HALF_STEP[out] * (y64.abs() + e)).all()
+
+
+@pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("m,n,k", [(2051, 1033, 3857), (2051, 1033, 3860), (2051, 1033, 3864)])
+def test_backward_through_large_tiles(m, n, k, dtype, out):
+    say("backward, large tiles", m, n, k, dtype, out)
+    wq = P.mx_quantize(gauss(n * k, n, k) * 0.05, "fp4")
+    w64 = values_of(wq)
+    dy, z = gauss(5, m, n).to(DT[dtype]), (gauss(6, m, n) * 1.5).to(DT[dtype])
+    da, db = P.mx_linear_backward(dy, wq, activation="gelu", preact=z, bias_grad=True, out_dtype=DT[out])
+    dz = dy.double() * slope64(z.double(), "gelu")
+    want = dz @ w64
+    e = bounds("dz", out, m, dz, w64.t(), True) + 2.0 ** -20 * (dy.double().abs() @ w64.abs())
+    assert ((da.double() - want).abs() <= e + HALF_STEP[out] * (want.abs() + e)).all()
+    e = 2.0 ** -24 * (m + 4) * dz.abs().sum(0) + 2.0 ** -20 * dy.double().abs().sum(0)
+    assert ((db.double() - dz.sum(0)).abs() <= e).all()
