@@ -254,10 +254,11 @@ __global__ __launch_bounds__(64 * SK_WAVES) void mx_skinny_kernel(SkinnyArgs p) 
 template <int KIND>
 hipError_t launch(const SkinnyArgs &p, hipStream_t st) {
     const unsigned blocks = (unsigned)cdiv(p.d_out, 16);
+    constexpr int MOST = KIND == MX_ACT_F32 ? 2 : 4;   // tiles of mx_skinny_takes' rows
     switch (cdiv(p.m, 16)) {
         case 1: mx_skinny_kernel<KIND, 1><<<blocks, 64 * SK_WAVES, 0, st>>>(p); break;
         case 2: mx_skinny_kernel<KIND, 2><<<blocks, 64 * SK_WAVES, 0, st>>>(p); break;
-        default: mx_skinny_kernel<KIND, 4><<<blocks, 64 * SK_WAVES, 0, st>>>(p); break;
+        default: mx_skinny_kernel<KIND, MOST><<<blocks, 64 * SK_WAVES, 0, st>>>(p); break;
     }
     return hipGetLastError();
 }
@@ -454,15 +455,18 @@ hipError_t launch_backward(const SkinnyBack &p, hipStream_t st) {
 // with the row tiles times a work group's steps times the rounds of groups; us a
 // call, few / many: fp8 4096 x 4096, 64 rows (128 of them) 10.8 / 13.9, 4096 x
 // 11008, 32 rows (172) 15.3 / 15.2; fp4 1024 x 8192, 64 rows (256) 12.0 / 13.6, 4096
-// x 11008, 64 rows (344) 15.6 / 14.8.  The dense form of bf16 and fp32
-// activations writes the whole layer first: bf16 4096 x 4096, 64 rows 22 / 29, 11008
-// x 4096 55 / 59, 1024 x 8192 (few work groups) 32 / 28; fp32 4096 x 4096, 32 rows 25 /
-// 34, 4096 x 11008, 32 rows 61 / 61, 64 rows 121 / 64.
+// x 11008, 64 rows (344) 15.6 / 14.8.  The dense form of the other kinds writes the
+// whole layer first: bf16 4096 x 4096, 64 rows 22 / 30, 11008 x 4096 56 / 54, 2048 x
+// 2048 10.5 / 22, 1024 x 8192 (few work groups) 32 / 28; fp8 with an F32 result, whose
+// rows are half as long, 64 rows of the same four 11.5 / 30, 32 / 55, 8.3 / 22, 20 / 28,
+// 28672 x 8192 137 / 265; fp32 4096 x 4096, 32 rows 27 / 34, 4096 x 11008 62 / 61, 64
+// rows 122 / 63.
 bool mx_skinny_takes(int64_t m, int64_t d_out, int64_t d_in, int kind) {
     const int64_t cost = cdiv(m, 16) * mx_steps(d_in) * cdiv(cdiv(d_out, 16), 256);
     switch (kind) {
         case MX_FP8: return m <= 16 || (m <= 64 && cost <= 160);
         case MX_FP4: return m <= 16 || (m <= 64 && cost <= 300);
+        case MX_WIDE_FP8: return m <= 64;
         case MX_ACT_F32: return m <= 32;
         default: return m <= 32 || (m <= 64 && d_out >= 2048);
     }
