@@ -193,15 +193,26 @@ def _check(status: int) -> None:
         raise GptqError(status, _lib().gptq_last_error().decode(errors="replace"))
 
 
-_TORCH = _FORWARD_AD = None
+_TORCH = _FORWARD_AD = _RAW_STREAM = _CURRENT_DEVICE = None
 
 
 def _torch():
-    global _TORCH, _FORWARD_AD
+    global _TORCH, _FORWARD_AD, _RAW_STREAM, _CURRENT_DEVICE
     if _TORCH is None:
         import torch  # memory and streams only
+        # The current stream's handle without a Stream object around it, and the
+        # current device without a check of the runtime: entry points that torch does
+        # not promise, so that the public ones serve where they are missing.
+        _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _CURRENT_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _TORCH, _FORWARD_AD = torch, torch.autograd.forward_ad
     return _TORCH
+
+
+def _dual_level() -> bool:
+    """Whether tensors may carry forward-mode tangents (yes where torch does not tell)."""
+    return getattr(_FORWARD_AD, "_current_level", 0) >= 0
 
 
 def _stream_ptr(stream=None) -> int:
@@ -475,8 +486,7 @@ class _FusedCall:
             self.stream = stream.cuda_stream
             self.guard = torch.cuda.stream(stream)
         else:
-            # (the current stream's handle without a Stream object around it)
-            self.stream = torch._C._cuda_getCurrentRawStream(device.index)
+            self.stream = _RAW_STREAM(device.index)
             if device.index != torch.cuda.current_device():
                 self.guard = torch.cuda.device(device)
         self.given_ws = workspace
@@ -527,7 +537,7 @@ class _FusedCall:
                     raise ValueError("autograd does not see through the fused products: call them under "
                                      "torch.no_grad() (or inside a torch.autograd.Function) and their _backward "
                                      "calls for the gradients")
-        if _FORWARD_AD._current_level >= 0:
+        if _dual_level():
             for t in tensors:
                 if _FORWARD_AD.unpack_dual(t).tangent is not None:
                     raise ValueError("forward-mode tangents do not pass through the fused products: give them the "
@@ -787,10 +797,8 @@ _HERE = _Here()
 def _place(device, name, stream):
     """(stream handle, context that allocations belong into) of a call whose operand `name` is on `device`."""
     if stream is None:
-        # (the current stream's handle without a Stream object around it)
         i = device.index
-        here = i == _TORCH._C._cuda_getDevice()
-        return _TORCH._C._cuda_getCurrentRawStream(i), _HERE if here else _TORCH.cuda.device(device)
+        return _RAW_STREAM(i), _HERE if i == _CURRENT_DEVICE() else _TORCH.cuda.device(device)
     if stream.device != device:
         raise ValueError(f"the stream belongs to {stream.device}, {name} to {device}")
     return stream.cuda_stream, _TORCH.cuda.stream(stream)
@@ -802,7 +810,7 @@ def _no_grad(*tensors):
         for t in tensors:
             if t is not None and t.requires_grad:
                 _FusedCall.no_grad(t)
-    if _FORWARD_AD._current_level >= 0:
+    if _dual_level():
         _FusedCall.no_grad(*[t for t in tensors if t is not None])
 
 
