@@ -410,9 +410,10 @@ GPTQ_API gptq_status gptq_mx_dequantize(const uint8_t *codes, const uint8_t *sca
  * Numerics: fp32 sums, one rounding of each output to its dtype.  MX operands
  * enter as they are stored and their products are exact; but where FP8
  * activations give a BF16 result, the matrix cores add a group's products with
- * about 14 bits below the largest (2^-14 of the sum of their magnitudes).  The
- * other operands may be rounded on the way, relative to the largest value M of
- * their row (activations; dZ as in gptq_dequant_linear_backward):
+ * about 14 bits below the largest (2^-14 of the sum of their magnitudes; a caller
+ * for whom that is too little asks for an F32 output).  The other operands may be
+ * rounded on the way, relative to the largest value M of their row (activations;
+ * dZ as in gptq_dequant_linear_backward):
  *   F32 output   to 22 significand bits down to 2^-17 M, and to within 2^-39 M
  *                below;
  *   BF16 output  dZ and F32 activations to 11 bits down to 2^-28 M, and to
@@ -421,8 +422,9 @@ GPTQ_API gptq_status gptq_mx_dequantize(const uint8_t *codes, const uint8_t *sca
  * Beside activations that are not MX, and FP8 ones with an F32 result, weights
  * (and those FP8 activations) below 2^-35 of M, here 6 (448) times the largest
  * scale of their row (in a backward call: of their 32 columns over all rows),
- * may be rounded to within 2^-39 of it.  Calls of few rows round less.  All
- * results are deterministic.
+ * may be rounded to within 2^-39 of it.  Calls of few rows round less, but hold
+ * F32 activations, dZ, and FP8 activations with an F32 result to within 2^-133 only
+ * (values below 2^-109 may lose precision).  All results are deterministic.
  * ------------------------------------------------------------------------- */
 GPTQ_API size_t gptq_mx_linear_workspace_size(int64_t m, int64_t d_out, int64_t d_in, gptq_dtype a_dtype,
                                               gptq_dtype y_dtype);

@@ -181,3 +181,23 @@ def test_backward_through_large_tiles(m, n, k, dtype, out):
     assert ((da.double() - want).abs() <= e + HALF_STEP[out] * (want.abs() + e)).all()
     e = 2.0 ** -24 * (m + 4) * dz.abs().sum(0) + 2.0 ** -20 * dy.double().abs().sum(0)
     assert ((db.double() - dz.sum(0)).abs() <= e).all()
+
+
+@pytest.mark.parametrize("m", [8, 20, 60])
+@pytest.mark.parametrize("kind", ["bf16", "f32", "fp8"])
+def test_subnormal_activations_in_few_rows(m, kind):
+    """The few-row form holds an activation to within 2^-133 (bf16's smallest step) at worst."""
+    n, k = 2100, 256
+    a, a64 = make_acts(kind, gauss(1, m, k) * 2.0 ** -126)
+    wq = P.mx_quantize(gauss(2, n, k) * 2.0 ** 20, "fp4")
+    w64 = values_of(wq)
+    want = a64 @ w64.t()
+    got = P.mx_linear(a, wq, out_dtype=torch.float32)
+    e = bounds(kind, "f32", m, a64, w64, m > 32) + 2.0 ** -133 * w64.abs().sum(1)
+    assert ((got.double() - want).abs() <= e + 2.0 ** -24 * (want.abs() + e)).all()
+    if kind in DT:
+        dy = (gauss(3, m, n) * 2.0 ** -126).to(DT[kind])
+        da, _ = P.mx_linear_backward(dy, wq, out_dtype=torch.float32)
+        want = dy.double() @ w64
+        e = bounds("dz", "f32", m, dy.double(), w64.t(), True) + 2.0 ** -133 * w64.abs().sum(0)
+        assert ((da.double() - want).abs() <= e + 2.0 ** -24 * (want.abs() + e)).all()
