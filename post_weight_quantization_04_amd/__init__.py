@@ -700,7 +700,12 @@ def dequant_gated_backward(dH, gate: "QuantizedLayer", up: "QuantizedLayer", gat
 class MxTensor:
     """A matrix [rows, d] in blocks of 32 columns that share a power of two
     (gptq.h has the layout): codes uint8 [rows, row bytes], scales uint8
-    [ceil(d / 128), rows, 4], format "fp8" (e4m3) or "fp4" (e2m1)."""
+    [ceil(d / 128), rows, 4], format "fp8" (e4m3) or "fp4" (e2m1).
+
+    Made from codes and scales of other origin, it needs zeros in what pads the
+    columns to whole 128: codes 0 behind column d, scale bytes 0 of the blocks
+    that lie behind it.  Sizes and types are checked at every call, this is
+    not, and the products add whatever lies there."""
     __slots__ = ("_codes", "_scales", "_buffer", "_rows", "_format", "_d")
     # (what the kernels index by stays what the memory was laid out for)
     rows, format, d = (property(attrgetter(name)) for name in ("_rows", "_format", "_d"))
