@@ -256,7 +256,9 @@ __device__ void prep_weights(const ForwardPrep &p, unsigned b, float *lds) {
 
 // MX weights as f16: a row's factor brings 6 times its largest scale to [2^14,
 // 2^15); two significant bits leave them exact in f16 down to 2^-37 of that,
-// one plane therefore serves F32 results too.
+// one plane therefore serves F32 results too.  (Weights below lose bits, 2^-39 of the
+// row's largest at most: beside the largest one's product that is beneath an fp32
+// sum's own rounding, 2^-24, unless the activations' sizes undo 2^15 of it.)
 typedef __attribute__((ext_vector_type(2))) _Float16 mx_f16x2;
 // the factor of a block of scale byte `byte` in a row (or a column) whose
 // largest is `top`, as the fp32 scale that the conversion takes (it reads the

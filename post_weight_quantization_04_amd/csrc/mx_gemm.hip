@@ -9,17 +9,20 @@
 // s-th of its two MFMAs takes blocks s and 2 + s, so that a lane's two scale
 // bytes lie side by side and the MFMA selects one by its immediate.
 //
-// Measured: fp8 2048 rows by 28672 outputs of K = 8192 2.70 PFLOP/s (357 us without
-// an activation), a large library product of two fp8 operands 2.73; the matrix
-// cores busy 58% of the cycles at 1.8 GHz, the clock under that load.  fp4 4096
-// rows by 11008 outputs: K = 16384 4.1 PFLOP/s, K = 4096 3.0 (120 us).
+// Measured, us a call without an activation: fp8 2048 rows by 28672 outputs of K =
+// 8192 360 (2.67 PFLOP/s; 4096 rows 2.90), a large library product of two fp8
+// operands 2.73; the matrix cores busy 59% of the cycles at 1.8 GHz, the clock under
+// that load.  fp4 4096 rows by 11008 outputs: K = 16384 365 (4.05 PFLOP/s), K = 4096
+// 113-116 (3.2; 142 with silu and a second output, which the epilogues write).
 //
 // Precision.  Products of two e2m1 operands add exactly into fp32.  With an e4m3
 // operand the MFMA aligns a group's products to the largest and keeps about 14
 // bits below it (measured: 2^-15 to 2^-14 of the sum of magnitudes, for any
-// length).  A BF16 result rounds at 2^-9; an F32 result of fp8 activations is
-// formed on the 16-bit matrix cores instead (the dense form of the fused
-// products, mx_skinny.hip), where both operands are exact.
+// length).  A BF16 result, which rounds at 2^-9, is as far from the 64-bit one as
+// with fp32 sums (1.7e-3 of its norm both; 2-3e-4 apart, as a few values in a hundred
+// cross a rounding border), for twice the 16-bit rate and no conversion.  An F32
+// result of fp8 activations is formed on the 16-bit matrix cores instead (the dense
+// form of the fused products, mx_skinny.hip), where both operands are exact.
 #include "mx.h"
 
 #include <algorithm>
@@ -322,8 +325,9 @@ __global__ __launch_bounds__(256) void mx_split_reduce_kernel(MxGemm p) {
 // Tiles of 256 x 256 where they fill half the CUs at once and K is long; otherwise
 // of 128 x 128, two groups to a CU, so that one's epilogue runs beside the
 // other's products.  Large / small, us a call: fp4 4096 x 11008 outputs K = 1024
-// 62 / 52, K = 4096 124 / 147; fp8 2048 x 28672 outputs K = 1024 93 / 70, 4096 209
-// / 202, 8192 369 / 386; fp4 1000 x 4096 outputs K = 11008 (four splits) 51 / 33.
+// 60 / 50, 4096 116 / 126, 16384 365 / 483; fp8 2048 x 28672 outputs K = 1024 87 /
+// 65, 4096 199 / 206, 8192 360 / 393; 1000 x 4096 outputs (64 large tiles) K = 11008
+// fp4 64 / 32, fp8 95 / 41.
 // k splits for grids that leave CUs idle, each of at least four stages.
 struct Plan {
     int size, mt, nt, nsplit;   // tile of 64 size rows and outputs

@@ -270,11 +270,12 @@ hipError_t launch(const SkinnyArgs &p, hipStream_t st) {
 // outputs r; a wave 32 outputs at a time: lane (g, l) loads 8 codes (columns 8 l ..)
 // of the 8 rows 8 g .., which it turns around in registers into the operands of
 // eight bf16 MFMAs (16 x 16 x 32), the c-th for columns 8 l + c.  The weights are
-// exact in bf16; dZ, formed from dY and the saved Z on the way, enters in two
-// bf16 terms (16 bits) for a BF16 result, three (24) for an F32 one, one where it
-// is bf16 itself.  The waves' sums meet in LDS, the ranges' in memory, both added
-// in their order.  Bias gradients: the groups of the first 128 columns add
-// their dZ over the rows.
+// exact in bf16; dZ, formed from dY and the saved Z on the way, enters in three bf16
+// terms (24 bits) for an F32 result, one where it is bf16 itself, and two (16) for a
+// BF16 result: what they leave, 2^-15 of dZ at most, is a 128th of that result's own
+// rounding, and a third term would be half as many MFMAs again.  The waves' sums meet
+// in LDS, the ranges' in memory, both added in their order.  Bias gradients: the
+// groups of the first 128 columns add their dZ over the rows.
 struct SkinnyBack {
     const void *dY, *pre;
     int in_bf16, act, vec;      // vec: whole aligned pieces of eight
