@@ -348,7 +348,7 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(NormBackArgs p) {
 // Few rows of whole pieces of eight: one launch.  A block takes 512 columns and
 // finds every row's factors by itself, a wave per row; the waves' terms of dw
 // meet in LDS.  us a call from Python, this / two launches: bf16 1 x 4096 8.3 /
-// 12.1, 16 x 4096 9.4 / 12.0; beyond, the blocks' repeated reads cost more: fp32 46 x
+// 11.8, 16 x 4096 10.7 / 11.6; beyond, the blocks' repeated reads cost more: fp32 46 x
 // 1408 14.8 / 12, rows that are not whole pieces (16 x 1407) 47 / 12.
 constexpr int SMALL_ROWS = 16, SMALL_COLS = 4096;
 template <bool BF16>
